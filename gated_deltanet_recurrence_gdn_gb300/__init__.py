@@ -9,6 +9,13 @@ raises -- there is no CPU fallback.
     o, hT = gdn_fwd_varlen(q, k, v, log_alpha, beta, cu_seqlens, h0=None)
     dq, dk, dv, dlog_alpha, dbeta, dh0 = gdn_bwd(q, k, v, log_alpha, beta, h0, dout, dhT)
 
+The softmax-attention layers of a hybrid decoder (``attention.py``,
+``include/gdn_attn.h``):
+
+    q, k = gdn_rope(q, k, cos, sin, pos)
+    q = gdn_kv_append(pages, k, v, page_table, kv_len, q=q, cos=cos, sin=sin, pos=pos)
+    o = gdn_kv_attn(q, pages, page_table, kv_len)
+
 Layouts follow ``include/gdn.h``: dense q, k [B,H,T,d_k], v [B,H,T,d_v]; packed
 q, k [H,T_total,d_k], v [H,T_total,d_v]; gates fp32; h0 / hT [.., H, d_v, d_k]
 fp32; q, k, v share one dtype (bf16 or fp32), which is also the dtype of o.
@@ -52,7 +59,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 
-# (name, restype, argtypes) of every symbol include/gdn.h declares.
+# (name, restype, argtypes) of every symbol the headers under include/ declare.
 ABI = [
     ("gdn_fwd", _i, [_vp] * 8 + [_i] * 7 + [_vp]),
     ("gdn_fwd_varlen", _i, [_vp] * 9 + [_i] * 7 + [_vp]),
@@ -76,6 +83,11 @@ ABI = [
     ("gdn_bounds_violation", _i, [_i]),
     ("gdn_last_impl", _i, []),
     ("gdn_release_scratch", _i, []),
+    ("gdn_rope", _i, [_vp] * 4 + [_i] * 3 + [_vp, _i, _vp]),
+    ("gdn_kv_page_bytes", ctypes.c_int64, [_i] * 2),
+    ("gdn_kv_append", _i, [_vp] * 6 + [_i, _vp]),
+    ("gdn_kv_read", _i, [_vp] * 3 + [_i, _vp]),
+    ("gdn_kv_attn", _i, [_vp] * 4 + [_i] * 2 + [ctypes.c_float, _i, ctypes.c_uint, _i, _vp]),
     ("gdn_selftest_wait", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
 ]
 
@@ -454,3 +466,7 @@ class use_impl:
         set_option(GDN_OPT_IMPL, self.prev[0])
         set_option(GDN_OPT_SEGMENTS, self.prev[1])
         return False
+
+
+from .attention import (gdn_kv_append, gdn_kv_attn, gdn_kv_page_bytes, gdn_kv_pages,  # noqa: E402,F401
+                        gdn_kv_read, gdn_rope, gdn_rope_axes, gdn_rope_bwd, gdn_rope_table)

@@ -1,0 +1,300 @@
+"""Binding of the softmax-attention layers of a hybrid decoder
+(``include/gdn_attn.h``): rotary positions, a paged key/value cache held in 4
+bits, and attention over that cache.
+
+Rows are found by strides: q, k, v and o may be any views whose last dimension
+is contiguous ([tokens, heads, d], or a transposed [heads, tokens, d]).  The
+cache entry points take the last tokens of each sequence, packed; ``kv_len``
+counts a sequence's tokens including them.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _DT, _check, _i, _ptr, _stream, _vp, load
+
+GDN_ROPE_ADJACENT = 1
+GDN_ROPE_INVERSE = 2
+GDN_ATTN_CAUSAL = 1
+
+_i64 = ctypes.c_int64
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("stride_seq", _i64), ("stride_head", _i64), ("stride_tok", _i64),
+                ("heads", _i)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("cos", _vp), ("sin", _vp), ("pos", _vp), ("axes", ctypes.c_char_p),
+                ("stride_axis", _i64), ("stride_seq", _i64), ("table_len", _i), ("d_rot", _i),
+                ("n_axes", _i), ("flags", ctypes.c_uint)]
+
+
+class _Kv(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("head_scale", _vp), ("page_table", _vp), ("kv_len", _vp),
+                ("cu_seqlens", _vp), ("n_pages", _i), ("page_size", _i), ("heads", _i), ("d", _i),
+                ("N", _i), ("max_pages", _i), ("n_tokens", _i), ("table_stride", _i64)]
+
+
+def _rows3(name, t, heads, n, d, dtype):
+    """[tokens, heads, d] rows."""
+    if not t.is_cuda or t.dtype != dtype or t.shape != (n, heads, d) or t.stride(2) != 1:
+        raise ValueError("%s must be a CUDA tensor [tokens, heads, d] of the call's dtype, its last "
+                         "dimension contiguous" % name)
+    # (a dimension of one entry may have any stride)
+    return _Rows(t.data_ptr(), 0, t.stride(1) if heads > 1 else 0, t.stride(0) if n > 1 else 0,
+                 heads)
+
+
+def _rows4(name, t, like, heads):
+    """[B, heads, T, d] rows."""
+    B, _, T, d = like.shape
+    if not t.is_cuda or t.dtype != like.dtype or t.shape != (B, heads, T, d) or t.stride(3) != 1:
+        raise ValueError("%s must be a CUDA tensor [B, heads, T, d] of the call's dtype, its last "
+                         "dimension contiguous" % name)
+    return _Rows(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if heads > 1 else 0,
+                 t.stride(2) if T > 1 else 0, heads)
+
+
+def _int32(name, t, dims):
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != dims or \
+            (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s must be a %d-D int32 CUDA tensor, its last dimension contiguous"
+                         % (name, dims))
+
+
+def _rotary(cos, sin, pos, axes, flags, shape):
+    """shape: the shape that one axis of `pos` has, or may have without its first part."""
+    if not cos.is_cuda or not sin.is_cuda or cos.dtype != torch.float32 or \
+            sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape or \
+            not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous fp32 CUDA tensors [positions, d_rot / 2]")
+    half = cos.shape[1]
+    lead = 0 if axes is None else 1
+    whole = pos.dim() == lead + len(shape)
+    _int32("pos", pos, lead + (len(shape) if whole else 1))
+    if tuple(pos.shape[lead:]) != (shape if whole else shape[-1:]):
+        raise ValueError("pos must hold a position per token%s" % (" on each axis" if lead else ""))
+    if axes is not None:
+        axes = bytes(axes)
+        if len(axes) != half:
+            raise ValueError("axes must give the axis of each of the d_rot / 2 pairs")
+    return _Rotary(cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), axes,
+                   pos.stride(0) if lead else 0,
+                   pos.stride(lead) if whole and len(shape) == 2 else 0, cos.shape[0], 2 * half,
+                   pos.shape[0] if lead else 1, flags)
+
+
+def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d):
+    if not pages.is_cuda or pages.dtype != torch.uint8 or pages.dim() != 3 or \
+            not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous uint8 CUDA tensor [n_pages, heads, page bytes]")
+    n_pages, heads, size = pages.shape
+    page_size = size * 8 // (9 * d)
+    if page_size * d * 9 != size * 8:
+        raise ValueError("a page of %d bytes does not hold rows of d = %d" % (size, d))
+    _int32("page_table", page_table, 2)
+    _int32("kv_len", kv_len, 1)
+    N = kv_len.shape[0]
+    if page_table.shape[0] != N:
+        raise ValueError("page_table must have a row per sequence")
+    cu = None
+    if cu_seqlens is not None:
+        _int32("cu_seqlens", cu_seqlens, 1)
+        if cu_seqlens.shape[0] != N + 1:
+            raise ValueError("cu_seqlens must have one entry more than there are sequences")
+        cu = cu_seqlens.data_ptr()
+    elif N == 0 or n_tokens % N:
+        if n_tokens:
+            raise ValueError("without cu_seqlens every sequence has the same number of tokens")
+    scale = None
+    if kv_scale is not None:
+        if not kv_scale.is_cuda or kv_scale.dtype != torch.float32 or \
+                kv_scale.shape != (2, heads) or not kv_scale.is_contiguous():
+            raise ValueError("kv_scale must be a contiguous fp32 CUDA tensor [2, heads]")
+        scale = kv_scale.data_ptr()
+    return _Kv(pages.data_ptr(), scale, page_table.data_ptr(), kv_len.data_ptr(), cu, n_pages,
+               page_size, heads, d, N, page_table.shape[1], n_tokens, page_table.stride(0))
+
+
+class _on:
+    """The tensor's device made current, where it is not already."""
+
+    def __init__(self, device):
+        self.guard = None
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _finish(rc, what, check, device):
+    _check(rc, what)
+    if check:
+        _check(load().gdn_sync_check(_stream(device)), what + " (device)")
+
+
+def gdn_kv_page_bytes(page_size: int, d: int) -> int:
+    """Bytes of one page of one head; 0 where the sizes are not supported."""
+    return int(load().gdn_kv_page_bytes(int(page_size), int(d)))
+
+
+def gdn_kv_pages(n_pages, heads, page_size, d, device=None):
+    """A new cache: uint8 [n_pages, heads, page bytes], zeroed."""
+    size = gdn_kv_page_bytes(page_size, d)
+    if size == 0:
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and d 64, 128 or 256")
+    return torch.zeros((n_pages, heads, size), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def gdn_rope_table(n_pos, d_rot, base=10000.0, device=None):
+    """(cos, sin), fp32 [n_pos, d_rot / 2], of position * base^(-2 i / d_rot), formed in fp64."""
+    device = "cuda" if device is None else device
+    f = torch.exp(torch.arange(0, d_rot, 2, dtype=torch.float64, device=device)
+                  * (-math.log(base) / max(d_rot, 1)))
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * f
+    return a.cos().float(), a.sin().float()
+
+
+def gdn_rope_axes(sections, interleave=False):
+    """The axis of each pair, for `axes`: sections[a] pairs go by axis a, in runs, or dealt out
+    in turn as long as an axis has some left."""
+    left = list(sections)
+    if not interleave:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    out = []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return bytes(out)
+
+
+def _rope(q, k, cos, sin, pos, axes, flags, out, check, what):
+    lib = load()
+    if q.dtype not in _DT or q.dim() != 4:
+        raise ValueError("q must be [B, heads, T, d], bf16 or fp32")
+    B, Hq, T, d = q.shape
+    qo, ko = out if out is not None else (torch.empty_like(q),
+                                          None if k is None else torch.empty_like(k))
+    rq, rqo = _rows4("q", q, q, Hq), _rows4("out[0]", qo, q, Hq)
+    rk = rko = None
+    if k is not None:
+        rk, rko = _rows4("k", k, q, k.shape[1]), _rows4("out[1]", ko, q, k.shape[1])
+    rot = _rotary(cos, sin, pos, axes, flags, (B, T))
+    with _on(q.device):
+        rc = lib.gdn_rope(ctypes.byref(rq), ctypes.byref(rqo), rk and ctypes.byref(rk),
+                          rko and ctypes.byref(rko), B, T, d, ctypes.byref(rot), _DT[q.dtype],
+                          _stream(q.device))
+        _finish(rc, what, check, q.device)
+    return qo, ko
+
+
+def gdn_rope(q, k, cos, sin, pos, *, axes=None, adjacent=False, out=None, check=False):
+    """Turns q [B, Hq, T, d] and k [B, Hk, T, d] (or None) by their positions: returns (q, k).
+
+    cos, sin: fp32 [positions, d_rot / 2] (gdn_rope_table); pos int32 [T] or [B, T].  With
+    several axes, `axes` gives the axis of each pair (gdn_rope_axes) and pos is [axes, T] or
+    [axes, B, T].  adjacent: pairs (2 i, 2 i + 1) instead of (i, i + d_rot / 2).  out: (q, k) to
+    write, which may be the inputs."""
+    return _rope(q, k, cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, out, check,
+                 "gdn_rope")
+
+
+def gdn_rope_bwd(dq, dk, cos, sin, pos, *, axes=None, adjacent=False, out=None, check=False):
+    """The gradient of gdn_rope with respect to q and k, from that of its results."""
+    return _rope(dq, dk, cos, sin, pos, axes,
+                 GDN_ROPE_INVERSE | (GDN_ROPE_ADJACENT if adjacent else 0), out, check,
+                 "gdn_rope_bwd")
+
+
+def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, kv_scale=None,
+                  cos=None, sin=None, pos=None, axes=None, adjacent=False, out=None, check=False):
+    """Appends k, v [tokens, heads, d] to the cache, k turned by its positions (where cos, sin
+    and pos int32 [tokens], or [axes, tokens], are given), and returns q [tokens, Hq, d] turned
+    likewise (None without q).
+
+    pages: the cache (gdn_kv_pages), written in place; page_table int32 [N, pages]; kv_len int32
+    [N], the sequences' tokens with the new ones; cu_seqlens int32 [N + 1] or None for the same
+    number of new tokens each; kv_scale fp32 [2, heads]: a further scale per head."""
+    lib = load()
+    if k.dtype not in _DT or k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, d], bf16 or fp32")
+    n, heads, d = k.shape
+    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
+    rk, rv = _rows3("k", k, kv.heads, n, d, k.dtype), _rows3("v", v, kv.heads, n, d, k.dtype)
+    rq = rqo = rot = None
+    if q is not None:
+        if out is None:
+            out = torch.empty_like(q)
+        rq = _rows3("q", q, q.shape[1], n, d, k.dtype)
+        rqo = _rows3("out", out, q.shape[1], n, d, k.dtype)
+    if cos is not None:
+        rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,))
+    with _on(k.device):
+        rc = lib.gdn_kv_append(ctypes.byref(kv), ctypes.byref(rk), ctypes.byref(rv),
+                               rq and ctypes.byref(rq), rqo and ctypes.byref(rqo),
+                               rot and ctypes.byref(rot), _DT[k.dtype], _stream(k.device))
+        _finish(rc, "gdn_kv_append", check, k.device)
+    return out if q is not None else None
+
+
+def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_scale=None,
+                dtype=torch.bfloat16, out=None, check=False):
+    """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
+    they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
+    lib = load()
+    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d)
+    if out is None:
+        k, v = torch.empty((2, n_tokens, kv.heads, d), dtype=dtype, device=pages.device).unbind(0)
+    else:
+        k, v = out
+    rk, rv = (_rows3("out", t, kv.heads, n_tokens, d, dtype) for t in (k, v))
+    with _on(pages.device):
+        rc = lib.gdn_kv_read(ctypes.byref(kv), ctypes.byref(rk), ctypes.byref(rv), _DT[dtype],
+                             _stream(pages.device))
+        _finish(rc, "gdn_kv_read", check, pages.device)
+    return k, v
+
+
+def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None, max_len=None,
+                max_new=None, scale=None, causal=True, window=0, out=None, return_lse=False,
+                check=False):
+    """Attention of the last tokens of each sequence, q [tokens, Hq, d] (turned already), over
+    the cached keys and values: o like q, or (o, lse fp32 [tokens, Hq]).
+
+    The cache arguments as in gdn_kv_append, after the append.  max_len and max_new: bounds on
+    kv_len and on a sequence's tokens in this call, known on the host (default: what the page
+    table and q can hold); they plan the launch.  scale: default d^-1/2.  window: a token sees
+    the last `window` places up to its own (0: all)."""
+    lib = load()
+    if q.dtype not in _DT or q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
+    n, Hq, d = q.shape
+    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
+    if out is None:
+        out = torch.empty_like(q)
+    rq, ro = _rows3("q", q, Hq, n, d, q.dtype), _rows3("out", out, Hq, n, d, q.dtype)
+    lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if max_len is None:
+        max_len = kv.max_pages * kv.page_size
+    if max_new is None:
+        max_new = n if cu_seqlens is not None else n // max(kv.N, 1)
+    with _on(q.device):
+        rc = lib.gdn_kv_attn(ctypes.byref(kv), ctypes.byref(rq), ctypes.byref(ro), _ptr(lse),
+                             max_len, max_new, d ** -0.5 if scale is None else scale, window,
+                             GDN_ATTN_CAUSAL if causal else 0, _DT[q.dtype], _stream(q.device))
+        _finish(rc, "gdn_kv_attn", check, q.device)
+    return (out, lse) if return_lse else out
