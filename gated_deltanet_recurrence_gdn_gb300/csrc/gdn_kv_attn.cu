@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "gdn_kv_attn.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace kv {
@@ -71,10 +72,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -114,25 +114,46 @@ struct Shape {
     static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
-// One group's 16 tokens of (page, head) into the ring, in the page's own order.
+// A lane's share of copying groups of one head into the ring: 16 tokens' key
+// codes, value codes, key scales and value scales, each contiguous in the page,
+// in this order.  Pieces of 16 bytes: kCode of key codes, as many of value
+// codes, then D / 8 of scales.
 template <int D>
-__device__ __forceinline__ void load_group(const Kv &kv, uint32_t dst, int page, int h, int row,
-                                           int lane) {
-    if (page < 0) return;
-    const int psz = kv.page_size();
-    const uint8_t *blk = kv.pages + kv.block(page, h);
-    constexpr int kCode = D / 2, kScale = D / 16;   // 16-byte pieces of each part
-#pragma unroll
-    for (int i = 0; i < (2 * (kCode + kScale) + 31) / 32; ++i) {
-        const int c = lane + 32 * i;
-        int at;
-        if (c < kCode) at = k_code_at(psz, D, row) + 16 * c;
-        else if (c < 2 * kCode) at = v_code_at(psz, D, row) + 16 * (c - kCode);
-        else if (c < 2 * kCode + kScale) at = k_scale_at(psz, D, row) + 16 * (c - 2 * kCode);
-        else at = v_scale_at(psz, D, row) + 16 * (c - 2 * kCode - kScale);
-        if (c < 2 * (kCode + kScale)) cp_async16(dst + 16 * c, blk + at);
+struct Loader {
+    static constexpr int kCode = D / 2, kScale = D / 16;
+    const uint8_t *code, *scale;   // of page 0, row 0
+    uint32_t page_bytes, v_code;
+    bool scales;                   // whether this lane copies scales
+
+    __device__ __forceinline__ void init(const Kv &kv, int h, int lane) {
+        const int psz = kv.page_size();
+        page_bytes = kv.H * block_bytes(psz, D);
+        const uint8_t *blk = kv.pages + (long long)h * block_bytes(psz, D);
+        code = blk + 16 * lane;
+        v_code = psz * (D / 2);
+        scales = lane < 2 * kScale;
+        scale = blk + (lane < kScale ? k_scale_at(psz, D, 0) + 16 * lane
+                                     : v_scale_at(psz, D, 0) + 16 * (lane - kScale));
     }
-}
+    __device__ __forceinline__ void copy(uint32_t dst, int page, int row, int lane) const {
+        const uint8_t *c = code + (uint64_t)page * page_bytes + (uint32_t)(row * (D / 2));
+        const uint8_t *v = c + v_code;
+        const uint32_t d = dst + 16 * lane;
+        if constexpr (D == 64) {
+            cp_async16(d, c);
+            cp_async16(d + 16 * kCode, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCode / 32; ++i) {
+                cp_async16(d + 512 * i, c + 512 * i);
+                cp_async16(d + 16 * kCode + 512 * i, v + 512 * i);
+            }
+        }
+        if (scales)
+            cp_async16(d + 32 * kCode,
+                       scale + (uint64_t)page * page_bytes + (uint32_t)(row * (D / 16)));
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T *p, float a, float b, float c, float d);
@@ -153,9 +174,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     constexpr int kV = D / 64;      // of a V row
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
     constexpr int kParts = kSplit ? 2 : 1;
-    // Least probability (lifted) whose fp16 parts keep all their bits, and how far
-    // the lifted maximum lies above it.
+    // Least probability (lifted) whose fp16 parts keep all their bits, how far the
+    // lifted maximum lies above it, and that range's middle and half in log2 units.
     constexpr float kLow = kSplit ? 0x1p-3f : 0x1p-14f, kBand = kSplit ? 0x1p18f : 0x1p29f;
+    constexpr float kMid = kSplit ? 6.f : 0.5f, kHalf = kLift + kRaise - kMid;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ P plan;
     __shared__ float2 warp_ml[kWarps][Sh::kRows];
@@ -164,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     const int g = lane >> 2, t4 = lane & 3;
     plan.build(a);
     const long long ctas = min((long long)gridDim.x, plan.total);
+    if (a.cuts && threadIdx.x == 0) a.cuts[blockIdx.x].pieces = 0;
     if (blockIdx.x >= ctas) return;
     const long long beg = plan.total * blockIdx.x / ctas, end = plan.total * (blockIdx.x + 1) / ctas;
     const uint32_t my_ring =
@@ -198,16 +221,20 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             return i + lane < steps ? a.kv.page_of(b, sq.lo + grp * kGroup, a.err) : -1;
         };
         int pages = fetch(0), ahead = steps > 32 ? fetch(32) : -1;
+        Loader<D> loader;
+        loader.init(a.kv, h, lane);
+        uint32_t fill = my_ring;
         auto issue = [&](int i) {   // whole warp, i in order
             if (i < steps) {
-                if (i > 0 && (i & 31) == 0) {
+                if ((i & 31) == 0 && i > 0) {
                     pages = ahead;
                     if (i + 32 < steps) ahead = fetch(i + 32);
                 }
                 const int page = __shfl_sync(0xffffffffu, pages, i & 31);
                 const int at = sq.lo + (grp0 + i * kWarps) * kGroup;
-                load_group<D>(a.kv, my_ring + (i % kStages) * Sh::kGroupBytes, page, h,
-                              at & (a.kv.page_size() - 1), lane);
+                if (page >= 0) loader.copy(fill, page, at & (a.kv.page_size() - 1), lane);
+                fill = fill == my_ring + (kStages - 1) * Sh::kGroupBytes ? my_ring
+                                                                         : fill + Sh::kGroupBytes;
             }
             cp_commit();
         };
@@ -276,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             all_to = min(all_to, __shfl_xor_sync(0xffffffffu, all_to, o));
         }
 
-        float o[NT][kT][4], mx[NT][2], sub[NT][2], sum[NT][2];
+        float o[NT][kT][4], sub[NT][2], sum[NT][2];   // sub: what scores lose before ex2
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -285,25 +312,26 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[nt][e] = -INFINITY;
-                sub[nt][e] = 0.f;
+                sub[nt][e] = -INFINITY;
                 sum[nt][e] = 0.f;
             }
         }
 
+        const uint8_t *buf = my_buf + (kStages - 1) * Sh::kGroupBytes;
+        int t0 = sq.lo + (grp0 - kWarps) * kGroup;
         for (int i = 0; i < steps; ++i) {
             cp_wait<kStages - 2>();
             __syncwarp();
             issue(i + kStages - 1);
-            const uint8_t *buf = my_buf + (i % kStages) * Sh::kGroupBytes;
-            const int t0 = sq.lo + (grp0 + i * kWarps) * kGroup;
+            buf = buf == my_buf + (kStages - 1) * Sh::kGroupBytes ? my_buf : buf + Sh::kGroupBytes;
+            t0 += kTile;
             const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
             // S^T
             float s[NT][4];
             {
                 uint32_t kw[2][kW];
-                uint32_t ks[2][kW / 2 > 0 ? (kW + 1) / 2 : 1];   // scale of each block, twice
+                __half2 ks[2][kW / 2];      // scale of each block, twice
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int row = place_of(g) + 8 * r;
@@ -312,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     if constexpr (D == 64) {
                         const uint2 w = *reinterpret_cast<const uint2 *>(p);
                         kw[r][0] = w.x; kw[r][1] = w.y;
-                        ks[r][0] = __byte_perm(e4m3x2_f16(*sp), 0, 0x1010);
+                        const uint32_t one = e4m3x2_f16(*sp);
+                        ks[r][0] = __low2half2(*reinterpret_cast<const __half2 *>(&one));
                     } else {
 #pragma unroll
                         for (int w4 = 0; w4 < kW / 4; ++w4) {
@@ -321,8 +350,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                             kw[r][4 * w4 + 2] = w.z; kw[r][4 * w4 + 3] = w.w;
                             const uint32_t two = e4m3x2_f16(
                                 *reinterpret_cast<const uint16_t *>(sp + 2 * w4));
-                            ks[r][2 * w4] = __byte_perm(two, 0, 0x1010);
-                            ks[r][2 * w4 + 1] = __byte_perm(two, 0, 0x3232);
+                            ks[r][2 * w4] =
+                                __low2half2(*reinterpret_cast<const __half2 *>(&two));
+                            ks[r][2 * w4 + 1] =
+                                __high2half2(*reinterpret_cast<const __half2 *>(&two));
                         }
                     }
                 }
@@ -357,60 +388,77 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
             }
 
-            // scores in log2 units, masked; running maximum
-            bool raise = false;
+            // Scores in log2 units less the row's `sub`, so that the row's largest number
+            // is about kLift.  One comparison finds those that call for more: above
+            // kLift + kRaise the maximum moves; below kLow probabilities lose bits.
+            float t[NT][4], rest[NT][4];
+            bool more = false, low = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[nt][e] *= mul[nt][e & 1];
+                    t[nt][e] = fmaf(s[nt][e], mul[nt][e & 1], -sub[nt][e & 1]);
                     if (!whole) {
                         const int at = t0 + place_of(g) + 8 * (e >> 1);
-                        if (at < from[nt][e & 1] || at >= to[nt][e & 1]) s[nt][e] = -INFINITY;
+                        if (at < from[nt][e & 1] || at >= to[nt][e & 1]) t[nt][e] = -INFINITY;
                     }
-                    raise = raise || s[nt][e] > mx[nt][e & 1] + kRaise;
+                    more = more || fabsf(t[nt][e] - kMid) > kHalf;
                 }
             }
-            if (__any_sync(0xffffffffu, raise)) {
+            const bool extra = __any_sync(0xffffffffu, more);
+            if (extra) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(s[nt][e], s[nt][e + 2]);
+                        // (an infinite t: the row's first score; its own score decides then)
+                        float y[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const bool out = t[nt][e + 2 * k] == -INFINITY;
+                            y[k] = out ? -INFINITY : s[nt][e + 2 * k] * mul[nt][e];
+                        }
+                        float m = fmaxf(y[0], y[1]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, mx[nt][e]);
-                        const float to_new = m == -INFINITY ? 0.f : m;
-                        const float f = ex2(mx[nt][e] - to_new);
-                        mx[nt][e] = m;
-                        sub[nt][e] = to_new - kLift;
-                        sum[nt][e] *= f;
+                        m -= kLift;
+                        if (m > sub[nt][e] + kRaise) {
+                            const float f = ex2(sub[nt][e] - m);
+                            sub[nt][e] = m;
+                            sum[nt][e] *= f;
 #pragma unroll
-                        for (int k = 0; k < kT; ++k) {
-                            o[nt][k][e] *= f;
-                            o[nt][k][e + 2] *= f;
+                            for (int k = 0; k < kT; ++k) {
+                                o[nt][k][e] *= f;
+                                o[nt][k][e + 2] *= f;
+                            }
                         }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (t[nt][e + 2 * k] != -INFINITY)
+                                t[nt][e + 2 * k] =
+                                    fmaf(s[nt][e + 2 * k], mul[nt][e], -sub[nt][e]);
                     }
             }
-            // Probabilities.  Those below kLow (`rest`) would lose bits as fp16 numbers:
-            // seldom there are any, and then they are added in a product of their own.
             uint32_t pf[kParts][NT][2];
-            float rest[NT][4];
-            bool low = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(s[nt][e] - sub[nt][e & 1]);
+                    p[e] = ex2(t[nt][e]);
                     sum[nt][e & 1] += p[e];
-                    rest[nt][e] = 0.f;
-                    if (p[e] < kLow) {
-                        rest[nt][e] = p[e];
-                        p[e] = 0.f;
+                }
+                if (extra) {      // the small ones later, in a product of their own
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        rest[nt][e] = 0.f;
+                        if (p[e] < kLow) {
+                            rest[nt][e] = p[e];
+                            p[e] = 0.f;
+                        }
+                        low = low || rest[nt][e] > 0.f;
                     }
-                    low = low || rest[nt][e] > 0.f;
                 }
                 operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
             }
@@ -496,7 +544,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     e2m1x8_f16(((vw[0][w] >> 4) & kEven) | (vw[1][w] & ~kEven), d1);
                     e2m1x8_f16((vw[2][w] & kEven) | ((vw[3][w] << 4) & ~kEven), e2);
                     e2m1x8_f16(((vw[2][w] >> 4) & kEven) | (vw[3][w] & ~kEven), d2);
-                    const uint32_t s1 = sc[w / 2 % kBlocks][0], s2 = sc[w / 2 % kBlocks][1];
+                    const __half2 s1 = *reinterpret_cast<const __half2 *>(&sc[w / 2 % kBlocks][0]);
+                    const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc[w / 2 % kBlocks][1]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t a0 = mul2(e1[k], s1), a1 = mul2(d1[k], s1);
@@ -521,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 }
             };
             product(std::true_type{}, 1.f);
-            if (__any_sync(0xffffffffu, low)) {
+            if (extra && __any_sync(0xffffffffu, low)) {
                 // what lies a factor kBand below the last product's range, until nothing is left
                 float factor = 1.f;
                 do {
@@ -555,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
                 sum[nt][e] = x;
-                if (g == 0) warp_ml[warp][8 * nt + 2 * t4 + e] = make_float2(mx[nt][e], x);
+                if (g == 0) warp_ml[warp][8 * nt + 2 * t4 + e] = make_float2(sub[nt][e], x);
             }
         __syncthreads();      // every warp is done with its ring as well
         float *merge = reinterpret_cast<float *>(ring);
@@ -567,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 float m = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r].x);
-                const float f = m == -INFINITY ? 1.f : ex2(mx[nt][e] - m);
+                const float f = m == -INFINITY ? 1.f : ex2(sub[nt][e] - m);
                 float *p = merge + (warp * Sh::kRows + r) * D + g * (D / 8);
 #pragma unroll
                 for (int k = 0; k < kT; ++k)
@@ -577,6 +626,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         __syncthreads();
         const bool complete = tile0 == 0 && tile1 == n_tiles;
         const long long slot = 2ll * blockIdx.x + (cur == beg ? 0 : 1);
+        if (threadIdx.x == 0 && tile0 == 0 && !complete) {
+            const long long end_tile = cur + n_tiles;    // CTA of its last tile: below
+            const int last = (int)((end_tile * ctas - 1) / plan.total);
+            a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, row0, rows};
+        }
         for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
             const int r = x / (D / 4), d = 4 * (x - r * (D / 4));
             float m = -INFINITY, l = 0.f;
@@ -598,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 if (a.lse && d == 0)
                     a.lse[(long long)(sq.first + j) * a.Hq + hq] =
-                        l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * 0.69314718055994531f;
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             } else {
                 store4(a.part_o + (slot * Sh::kRows + r) * D + d, v.x, v.y, v.z, v.w);
                 if (d == 0) a.part_ml[slot * Sh::kRows + r] = make_float2(m, l);
@@ -609,77 +663,70 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     }
 }
 
-// Adds the pieces of every (sequence, head, row tile) that a border between CTAs
-// cut: CTA (i, r) those of row r whose first border is border i + 1.
+// Adds the pieces of what was cut, in order: CTA (i, r) row r of the one whose
+// first piece CTA i of k_kv_attn had.
+constexpr int kJoinWarps = 4;
 template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kThreads) k_kv_join(const AttnArgs a, int grid) {
-    using P = Plan<kTile, kRows, kThreads>;
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
     constexpr int kVec = D / 32;
-    __shared__ P plan;
-    __shared__ float sums[kWarps][D];
-    __shared__ float2 ml_w[kWarps];
-    plan.build(a);
-    const long long ctas = min((long long)grid, plan.total);
-    const int i = blockIdx.x + 1, r = blockIdx.y;
-    if (i >= ctas) return;
-    const long long border = plan.total * i / ctas, before = plan.total * (i - 1) / ctas;
-    int b;
-    long long seq_start;
-    Seq sq;
-    plan.find(a, border, b, seq_start, sq);
-    const int n_tiles = P::tiles(sq), n_rt = P::row_tiles(a, sq);
-    const int seg = (int)((border - seq_start) / n_tiles);
-    const long long s0 = seq_start + (long long)seg * n_tiles, s1 = s0 + n_tiles;
-    const int h = seg / n_rt, row0 = (seg - h * n_rt) * kRows;
-    if (border == s0 || before > s0 || row0 + r >= sq.n * a.G) return;
-    int last = i;                       // last CTA with a piece
-    while (last + 1 < ctas && plan.total * (last + 1) / ctas < s1) ++last;
-    const int pieces = last - i + 2;
-    auto slot = [&](int k) {            // piece k: of CTA i - 1 + k
-        return k == 0 ? 2ll * (i - 1) + (before == s0 ? 0 : 1) : 2ll * (i - 1 + k);
+    __shared__ float sums[kJoinWarps][D];
+    __shared__ float2 warp_ml[kJoinWarps];
+    ptx::griddep_wait();
+    const Cut c = a.cuts[blockIdx.x];
+    const int r = blockIdx.y;
+    if (r >= c.rows || c.pieces == 0) return;
+    auto slot = [&](int k) {
+        return (k == 0 ? (long long)c.slot0 : 2ll * (blockIdx.x + k)) * kRows + r;
     };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float m = -INFINITY;
-    for (int k = threadIdx.x; k < pieces; k += kThreads)
-        m = fmaxf(m, a.part_ml[slot(k) * kRows + r].x);
+    for (int k = threadIdx.x; k < c.pieces; k += kJoinWarps * 32) m = fmaxf(m, a.part_ml[slot(k)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) ml_w[warp].x = m;
+    if (lane == 0) warp_ml[warp].x = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_w[w].x);
-    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, warp_ml[w].x);
     float v[kVec] = {}, l = 0.f;
-    for (int k = warp; k < pieces; k += kWarps) {
-        const float2 ml = a.part_ml[slot(k) * kRows + r];
+#pragma unroll 4
+    for (int k = warp; k < c.pieces; k += kJoinWarps) {
+        const float2 ml = a.part_ml[slot(k)];
         const float f = m == -INFINITY ? 1.f : ex2(ml.x - m);
-        const float *p = a.part_o + (slot(k) * kRows + r) * D + lane * kVec;
+        const float *p = a.part_o + slot(k) * D + lane * kVec;
         l += ml.y * f;
+        if constexpr (kVec == 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(p);
+            v[0] += x.x * f; v[1] += x.y * f;
+        } else {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] += p[e] * f;
+            for (int e = 0; e < kVec; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(p + e);
+                v[e] += x.x * f; v[e + 1] += x.y * f; v[e + 2] += x.z * f; v[e + 3] += x.w * f;
+            }
+        }
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
-    if (lane == 0) ml_w[warp].y = l;
+    if (lane == 0) warp_ml[warp].y = l;
     __syncthreads();
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) l += ml_w[w].y;
-    const int rr = row0 + r, j = rr / a.G, hq = h * a.G + rr - j * a.G;
-    const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
+    for (int w = 0; w < kJoinWarps; ++w) l += warp_ml[w].y;
+    const int rr = c.row0 + r, j = rr / a.G, hq = c.h * a.G + rr - j * a.G;
+    const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + c.h) : 1.f;
     const float inv = l == 0.f ? 0.f : gv / l;
-    T *p = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + hq * a.o_head;
-    for (int d = 4 * threadIdx.x; d < D; d += 4 * kThreads) {
+    T *p = static_cast<T *>(a.o) + (c.first + j) * a.o_tok + hq * a.o_head;
+    for (int d = 4 * threadIdx.x; d < D; d += 4 * kJoinWarps * 32) {
         float x[4] = {};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < kJoinWarps; ++w)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] += sums[w][d + e];
         store4(p + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
     }
     if (a.lse && threadIdx.x == 0)
-        a.lse[(long long)(sq.first + j) * a.Hq + hq] =
-            l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * 0.69314718055994531f;
+        a.lse[(long long)(c.first + j) * a.Hq + hq] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <typename T, int D, int NT, bool kSplit, int kStages, int kMinCtas>
@@ -708,9 +755,11 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     void *scratch = nullptr;
     const size_t po = (size_t)2 * grid * Sh::kRows * D * 4, pm = (size_t)2 * grid * Sh::kRows * 8;
     if (cut) {
-        if (scratch_alloc(&scratch, po + pm, st) != cudaSuccess) return GDN_ERR_CUDA;
+        if (scratch_alloc(&scratch, po + pm + grid * sizeof(Cut), st) != cudaSuccess)
+            return GDN_ERR_CUDA;
         a.part_o = static_cast<float *>(scratch);
         a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(scratch) + po);
+        a.cuts = reinterpret_cast<Cut *>(static_cast<uint8_t *>(scratch) + po + pm);
     }
     const int slot = timer_begin(st, "k_kv_attn");
     kern<<<grid, kThreads, Sh::kSmem, st>>>(a);
@@ -718,10 +767,20 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (cut) {
-        if (e == cudaSuccess && grid > 1) {
-            k_kv_join<T, D, Sh::kRows><<<dim3(grid - 1, Sh::kRows), kThreads, 0, st>>>(a, grid);
+        if (e == cudaSuccess && grid > 1 && a.max_new > 0) {
+            // launched while k_kv_attn runs: it waits for that to end before it reads
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t cfg{};
+            const long long rows = (long long)a.max_new * a.G;
+            cfg.gridDim = dim3(grid, (unsigned)(rows < Sh::kRows ? rows : Sh::kRows));
+            cfg.blockDim = dim3(kJoinWarps * 32);
+            cfg.stream = st;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, k_kv_join<T, D, Sh::kRows>, (const AttnArgs)a);
             count_launch();
-            e = cudaGetLastError();
         }
         const cudaError_t f = scratch_free(scratch, st);
         if (e == cudaSuccess) e = f;

@@ -19,8 +19,16 @@ struct AttnArgs {
     int window;                // 0: none
     bool causal;
     float *part_o;             // [2 * grid][rows][d], sums that a join still divides
-    float2 *part_ml;           // [2 * grid][rows]: maximum (log2 units) and sum
+    float2 *part_ml;           // [2 * grid][rows]: what scores lost (log2 units) and sum
+    struct Cut *cuts;          // [grid], nullptr where nothing is cut
     int *err;
+};
+
+// A (sequence, key/value head, row tile) that is cut, written by the CTA with its
+// first piece: pieces are slot0 of that CTA i, then slots 2 (i + 1), 2 (i + 2), ...
+struct Cut {
+    int pieces;                // 0: the CTA's last piece is whole
+    int slot0, first, h, row0, rows;
 };
 
 // Tokens of one sequence and what its rows see.  Row r of a (sequence,
@@ -122,6 +130,5 @@ struct Plan {
     }
 };
 
-// What the tensor-core path (many rows) takes; defined in gdn_kv_attn_tc.cu.
 }  // namespace kv
 }  // namespace gdn
