@@ -6,9 +6,10 @@
 // that the instructions that turn 4-bit numbers into fp16 operands: at 144 bytes
 // a (token, head) of d = 128 and 6.8 TB/s an SM has 3 issue slots per element.
 //
-// - A warp takes 16 tokens at a time, by itself: cp.async into its own ring of
-//   kStages groups (all four parts of a group lie contiguous in the page), no
-//   barrier between warps until a piece of work ends.
+// - A tile of 128 tokens is copied into a ring of shared memory by bulk copies
+//   (one per page and part of it), each warp issuing every eighth tile's; a warp
+//   takes 16 tokens of every tile, and no barrier joins the warps until a piece
+//   of work ends.
 // - Tokens are the M side of the products: S^T[16 x 8] = K[16 x d] Q^T[d x 8],
 //   O^T[d x 8] += V^T[d x 16] P^T[16 x 8], so 8 query rows of a key/value head
 //   cost one n = 8 tile and a single row no more.
@@ -45,18 +46,19 @@ constexpr int kTile = kWarps * kGroup;
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Copy of `bytes` (a multiple of 16, both sides 16-byte aligned) into shared
+// memory, counted on the mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst), "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -108,50 +110,33 @@ __device__ __forceinline__ void operand_of(const float (&p)[4], uint32_t (&hi)[2
 template <int D, int NT, bool kSplit, int kStages>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kGroupBytes = kGroup * D * 9 / 8;
-    static constexpr int kRing = kWarps * kStages * kGroupBytes;
-    static constexpr int kMerge = kWarps * kRows * D * 4;
-    static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kParts = kSplit ? 2 : 1;
+    // a stage: key codes, value codes, key scales, value scales of a tile
+    static constexpr int kVCode = kTile * D / 2, kKScale = kTile * D, kVScale = kTile * D * 17 / 16;
+    static constexpr int kStage = kTile * D * 9 / 8;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kMerge = kWarps * 8 * D * 4;          // 8 rows of every warp
+    static_assert(kMerge <= kRing, "the ring holds a merge");
+    static constexpr int kQueries = kParts * NT * (D / 16) * 32 * 8;
+    static constexpr int kSmem = kRing + kQueries;
+    static constexpr int kLead = kStages - 2;                  // tiles copied ahead
 };
 
-// A lane's share of copying groups of one head into the ring: 16 tokens' key
-// codes, value codes, key scales and value scales, each contiguous in the page,
-// in this order.  Pieces of 16 bytes: kCode of key codes, as many of value
-// codes, then D / 8 of scales.
-template <int D>
-struct Loader {
-    static constexpr int kCode = D / 2, kScale = D / 16;
-    const uint8_t *code, *scale;   // of page 0, row 0
-    uint32_t page_bytes, v_code;
-    bool scales;                   // whether this lane copies scales
-
-    __device__ __forceinline__ void init(const Kv &kv, int h, int lane) {
-        const int psz = kv.page_size();
-        page_bytes = kv.H * block_bytes(psz, D);
-        const uint8_t *blk = kv.pages + (long long)h * block_bytes(psz, D);
-        code = blk + 16 * lane;
-        v_code = psz * (D / 2);
-        scales = lane < 2 * kScale;
-        scale = blk + (lane < kScale ? k_scale_at(psz, D, 0) + 16 * lane
-                                     : v_scale_at(psz, D, 0) + 16 * (lane - kScale));
-    }
-    __device__ __forceinline__ void copy(uint32_t dst, int page, int row, int lane) const {
-        const uint8_t *c = code + (uint64_t)page * page_bytes + (uint32_t)(row * (D / 2));
-        const uint8_t *v = c + v_code;
-        const uint32_t d = dst + 16 * lane;
-        if constexpr (D == 64) {
-            cp_async16(d, c);
-            cp_async16(d + 16 * kCode, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCode / 32; ++i) {
-                cp_async16(d + 512 * i, c + 512 * i);
-                cp_async16(d + 16 * kCode + 512 * i, v + 512 * i);
-            }
+// The waits of a CTA: bounded, and over at once when one of them has given up
+// (the error is recorded, and the CTA runs to its end without computing).
+struct Waits {
+    volatile int *abort;
+    int *err;
+    uint32_t limit;
+    __device__ __forceinline__ bool on(uint64_t *bar, uint32_t parity) const {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        for (uint32_t i = 0; i < limit; ++i) {
+            if (*abort) return false;
+            if (ptx::mbar_try_wait(bar, parity)) return true;
         }
-        if (scales)
-            cp_async16(d + 32 * kCode,
-                       scale + (uint64_t)page * page_bytes + (uint32_t)(row * (D / 16)));
+        *abort = 1;
+        atomicCAS(err, 0, kErrTimeout);
+        return false;
     }
 };
 
@@ -166,33 +151,194 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
+// S^T of a warp's group (its first row at `codes` and `scales`): K, rows
+// place_of(g) and 8 more, times Q^T.
+template <int D, int NT, int kParts>
+__device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scales, int g, int t4,
+                                       const uint4 *queries, float (&s)[NT][4]) {
+    constexpr int kW = D / 32;      // 32-bit words of a lane's share of a row
+    uint32_t kw[2][kW];
+    __half2 ks[2][kW / 2];          // scale of each block, twice
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = place_of(g) + 8 * r;
+        const uint8_t *p = codes + row * (D / 2) + t4 * (D / 8);
+        const uint8_t *sp = scales + row * (D / 16) + t4 * (D / 64);
+        if constexpr (D == 64) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            kw[r][0] = w.x; kw[r][1] = w.y;
+            const uint32_t one = e4m3x2_f16(*sp);
+            ks[r][0] = __low2half2(*reinterpret_cast<const __half2 *>(&one));
+        } else {
+#pragma unroll
+            for (int w4 = 0; w4 < kW / 4; ++w4) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(p + 16 * w4);
+                kw[r][4 * w4] = w.x; kw[r][4 * w4 + 1] = w.y;
+                kw[r][4 * w4 + 2] = w.z; kw[r][4 * w4 + 3] = w.w;
+                const uint32_t two = e4m3x2_f16(*reinterpret_cast<const uint16_t *>(sp + 2 * w4));
+                ks[r][2 * w4] = __low2half2(*reinterpret_cast<const __half2 *>(&two));
+                ks[r][2 * w4 + 1] = __high2half2(*reinterpret_cast<const __half2 *>(&two));
+            }
+        }
+    }
+    float s2[NT][4];                // a second chain of products
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        uint32_t r0[4], r1[4];
+        e2m1x8_f16(kw[0][w], r0);
+        e2m1x8_f16(kw[1][w], r1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r0[e] = mul2(r0[e], ks[0][w / 2]);
+            r1[e] = mul2(r1[e], ks[1][w / 2]);
+        }
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 q = queries[((part * NT + nt) * kW + w) * 32];
+                mma16816(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
+                mma16816(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
+            }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
+}
+
+// A lane's numbers of V of one group: D / 8 elements of the tokens t4, 4 + (t4 ^ 1)
+// and those 8 further, with their scales.
+template <int D>
+struct VShare {
+    static constexpr int kWords = D / 64, kBlocks = D == 256 ? 2 : 1;
+    uint32_t w[4][kWords], sb[4];
+
+    __device__ static __forceinline__ int place(int j, int t4) {
+        return 4 * j + ((j & 1) ? t4 ^ 1 : t4);
+    }
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int g,
+                                         int t4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = place(j, t4);
+            const uint8_t *p = codes + row * (D / 2) + g * (D / 16);
+            const uint8_t *sp = scales + row * (D / 16) + g * D / 128;
+            if constexpr (D == 64) {
+                w[j][0] = *reinterpret_cast<const uint32_t *>(p);
+                sb[j] = *sp;
+            } else if constexpr (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                w[j][0] = x.x; w[j][1] = x.y;
+                sb[j] = *sp;
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
+                sb[j] = *reinterpret_cast<const uint16_t *>(sp);
+            }
+        }
+    }
+    // The scale of block k of the tokens 2 e and 2 e + 1 of the four.
+    __device__ __forceinline__ __half2 scale(int k, int e) const {
+        const uint32_t two =
+            e4m3x2_f16(__byte_perm(sb[2 * e], sb[2 * e + 1], k == 0 ? 0x0040 : 0x0051));
+        return *reinterpret_cast<const __half2 *>(&two);
+    }
+};
+
+// O^T += V^T P^T, or with kScaled O^T += factor * (V^T P^T).
+template <int D, int NT, int kParts, bool kScaled>
+__device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)[kParts][NT][2],
+                                        float factor, float (&o)[NT][D / 16][4]) {
+    __half2 sc[VShare<D>::kBlocks][2];
+#pragma unroll
+    for (int k = 0; k < VShare<D>::kBlocks; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sc[k][e] = v.scale(k, e);
+#pragma unroll
+    for (int w = 0; w < VShare<D>::kWords; ++w) {
+        constexpr uint32_t kEven = 0x0f0f0f0fu;
+        uint32_t e1[4], d1[4], e2[4], d2[4];   // even and odd elements of the two token pairs
+        e2m1x8_f16((v.w[0][w] & kEven) | ((v.w[1][w] << 4) & ~kEven), e1);
+        e2m1x8_f16(((v.w[0][w] >> 4) & kEven) | (v.w[1][w] & ~kEven), d1);
+        e2m1x8_f16((v.w[2][w] & kEven) | ((v.w[3][w] << 4) & ~kEven), e2);
+        e2m1x8_f16(((v.w[2][w] >> 4) & kEven) | (v.w[3][w] & ~kEven), d2);
+        const __half2 s1 = sc[w / 2 % VShare<D>::kBlocks][0], s2 = sc[w / 2 % VShare<D>::kBlocks][1];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = mul2(e1[k], s1), a1 = mul2(d1[k], s1);
+            const uint32_t a2 = mul2(e2[k], s2), a3 = mul2(d2[k], s2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float (&acc)[4] = o[nt][4 * w + k];
+                if constexpr (!kScaled) {
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+                        mma16816(acc, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
+                } else {
+                    float x[4] = {};
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+                        mma16816(x, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
+                }
+            }
+        }
+    }
+}
+
 template <typename T, int D, int NT, bool kSplit, int kStages, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
     using Sh = Shape<D, NT, kSplit, kStages>;
     using P = Plan<kTile, Sh::kRows, kThreads>;
-    constexpr int kW = D / 32;      // 32-bit words of a lane's share of a K row
-    constexpr int kV = D / 64;      // of a V row
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
-    constexpr int kParts = kSplit ? 2 : 1;
+    constexpr int kParts = Sh::kParts, kRows = Sh::kRows;
     // Least probability (lifted) whose fp16 parts keep all their bits, how far the
     // lifted maximum lies above it, and that range's middle and half in log2 units.
     constexpr float kLow = kSplit ? 0x1p-3f : 0x1p-14f, kBand = kSplit ? 0x1p18f : 0x1p29f;
     constexpr float kMid = kSplit ? 6.f : 0.5f, kHalf = kLift + kRaise - kMid;
-    extern __shared__ __align__(16) uint8_t ring[];
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ P plan;
-    __shared__ float2 warp_ml[kWarps][Sh::kRows];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int abort_flag;
+    __shared__ float2 warp_ml[kWarps][kRows];
+    __shared__ float row_mul[kRows];
+    __shared__ int row_from[kRows], row_to[kRows], all_seen[2];
+    uint4 *queries = reinterpret_cast<uint4 *>(smem + Sh::kRing);
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    plan.build(a);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, kWarps);
+        }
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    plan.build(a);                  // (its barriers cover the initialisation)
     const long long ctas = min((long long)gridDim.x, plan.total);
     if (a.cuts && threadIdx.x == 0) a.cuts[blockIdx.x].pieces = 0;
     if (blockIdx.x >= ctas) return;
     const long long beg = plan.total * blockIdx.x / ctas, end = plan.total * (blockIdx.x + 1) / ctas;
-    const uint32_t my_ring =
-        static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * kStages * Sh::kGroupBytes;
-    const uint8_t *my_buf = ring + warp * kStages * Sh::kGroupBytes;
+    const Waits waits{&abort_flag, a.err, a.wait_limit};
+    const uint32_t ring_at = ptx::smem_u32(smem);
 
+    // Copies: lane (run, part) of the issuing warp copies one part of a run of tokens
+    // that lie together, a page's or as many of it as make a tile.
+    const int run = min(a.kv.page_size(), kTile);
+    const int lane_run = lane >> 2, lane_part = lane & 3;
+    const int row_bytes = lane_part < 2 ? D / 2 : D / 16;
+    const uint32_t lane_dst = (lane_part == 0   ? 0
+                               : lane_part == 1 ? Sh::kVCode
+                               : lane_part == 2 ? Sh::kKScale
+                                                : Sh::kVScale) + lane_run * run * row_bytes;
+    uint32_t tiles_before = 0;      // of the earlier pieces: a tile's stage and phase
     int b;
     long long seq_start;
     Seq sq;
@@ -208,51 +354,49 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         const long long within = cur - seq_start;
         const int seg = (int)(within / n_tiles), tile0 = (int)(within - (long long)seg * n_tiles);
         const int tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
-        const int h = seg / n_rt, row0 = (seg - h * n_rt) * Sh::kRows;
-        const int rows = min(Sh::kRows, sq.n * a.G - row0);
+        const int h = seg / n_rt, row0 = (seg - h * n_rt) * kRows;
+        const int rows = min(kRows, sq.n * a.G - row0);
+        const int place0 = sq.lo + tile0 * kTile, n_copy = sq.span > 0 ? tile1 - tile0 : 0;
 
-        // groups of this piece, and this warp's among them
-        const int n_groups = (sq.span + kGroup - 1) / kGroup;
-        const int grp0 = tile0 * kWarps + warp, grp1 = min(tile1 * kWarps, n_groups);
-        const int steps = grp1 > grp0 ? (grp1 - grp0 + kWarps - 1) / kWarps : 0;
-        // page of the warp's step i: held by lane i % 32 of `pages`, the next 32 in `ahead`
+        // page of the lane's run of tile i, -1 if there is none to copy
         auto fetch = [&](int i) {
-            const int grp = grp0 + (i + lane) * kWarps;
-            return i + lane < steps ? a.kv.page_of(b, sq.lo + grp * kGroup, a.err) : -1;
+            const int at = place0 + i * kTile + lane_run * run;
+            return i < n_copy && lane_run * run < kTile && at < sq.len ? a.kv.page_of(b, at, a.err)
+                                                                       : -1;
         };
-        int pages = fetch(0), ahead = steps > 32 ? fetch(32) : -1;
-        Loader<D> loader;
-        loader.init(a.kv, h, lane);
-        uint32_t fill = my_ring;
-        auto issue = [&](int i) {   // whole warp, i in order
-            if (i < steps) {
-                if ((i & 31) == 0 && i > 0) {
-                    pages = ahead;
-                    if (i + 32 < steps) ahead = fetch(i + 32);
-                }
-                const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-                const int at = sq.lo + (grp0 + i * kWarps) * kGroup;
-                if (page >= 0) loader.copy(fill, page, at & (a.kv.page_size() - 1), lane);
-                fill = fill == my_ring + (kStages - 1) * Sh::kGroupBytes ? my_ring
-                                                                         : fill + Sh::kGroupBytes;
+        auto produce = [&](int i, int page) {    // one warp
+            const uint32_t n = tiles_before + i, stage = n % kStages;
+            if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
+            const uint32_t runs = __popc(__ballot_sync(0xffffffffu, page >= 0 && lane_part == 0));
+            if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
+            __syncwarp();
+            if (page >= 0) {
+                const int at = (place0 + i * kTile + lane_run * run) & (a.kv.page_size() - 1);
+                const int psz = a.kv.page_size();
+                const uint8_t *src = a.kv.pages + a.kv.block(page, h) + at * row_bytes +
+                                     (lane_part == 0   ? 0
+                                      : lane_part == 1 ? v_code_at(psz, D, 0)
+                                      : lane_part == 2 ? k_scale_at(psz, D, 0)
+                                                       : v_scale_at(psz, D, 0));
+                bulk_load(ring_at + stage * Sh::kStage + lane_dst, src, run * row_bytes,
+                          full + stage);
             }
-            cp_commit();
         };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        int next = warp;                          // the warp's next tile to copy, and its page
+        int next_page = fetch(next);
+        if (next < min(Sh::kLead, n_copy)) {
+            produce(next, next_page);
+            next += kWarps;
+            next_page = fetch(next);
+        }
 
-        // queries: lane's part of row 8 nt + g, as the B operand, scaled by a power
-        // of two that brings the row's largest number to [2^13, 2^14)
+        // Queries: warp nt, the lane's part of row 8 nt + g, as the B operand, scaled by
+        // a power of two that brings the row's largest number to [2^13, 2^14).
         const float gk = a.kv.head_scale ? __ldg(a.kv.head_scale + h) : 1.f;
         const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
-        uint32_t qf[kParts][NT][kT][2];
-        float mul[NT][2];
-        int from[NT][2], to[NT][2];
-        int all_from = 0, all_to = 0x7fffffff;     // places that every row sees
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + 8 * nt + g;
-            const bool there = 8 * nt + g < rows;
+        if (warp < NT) {
+            const int mine = 8 * warp + g, r = row0 + mine;
+            const bool there = mine < rows;
             const int j = there ? r / a.G : 0;
             const T *p = static_cast<const T *>(a.q) + (sq.first + j) * a.q_tok +
                          (long long)(h * a.G + (there ? r - j * a.G : 0)) * a.q_head + t4 * (D / 4);
@@ -272,37 +416,54 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t ex = max(27u, __float_as_uint(m) >> 23);
             const float up = __uint_as_float((267u - ex) << 23);
-            const float down = __uint_as_float((ex - 13u) << 23) * a.scale_log2 * gk;
 #pragma unroll
-            for (int s = 0; s < kT; ++s) {
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float u = x[4 * s + 2 * e] * up, w = x[4 * s + 2 * e + 1] * up;
-                    qf[0][nt][s][e] = pack_f16(u, w);
-                    if constexpr (kSplit) {
-                        const float2 hi =
-                            __half22float2(*reinterpret_cast<const __half2 *>(&qf[0][nt][s][e]));
-                        qf[1][nt][s][e] = pack_f16(u - hi.x, w - hi.y);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[8 * w + 2 * e] * up, v = x[8 * w + 2 * e + 1] * up;
+                    hi[e] = pack_f16(u, v);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
+                    lo[e] = pack_f16(u - f.x, v - f.y);
+                }
+                uint4 *q = queries + (warp * (D / 32) + w) * 32 + lane;
+                q[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if constexpr (kSplit) q[NT * (D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            int from = 0, to = sq.len;
+            if (there) sq.sees(a, j, from, to);
+            if (t4 == 0) {
+                row_mul[mine] = __uint_as_float((ex - 13u) << 23) * a.scale_log2 * gk;
+                row_from[mine] = from;
+                row_to[mine] = to;
+            }
+            if (NT == 1) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    from = max(from, __shfl_xor_sync(0xffffffffu, from, o));
+                    to = min(to, __shfl_xor_sync(0xffffffffu, to, o));
+                }
+                if (lane == 0) {
+                    all_seen[0] = from;
+                    all_seen[1] = to;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mul[nt][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * t4 + e));
-                const int rr = 8 * nt + 2 * t4 + e;
-                from[nt][e] = 0;
-                to[nt][e] = sq.len;
-                if (rr < rows) sq.sees(a, (row0 + rr) / a.G, from[nt][e], to[nt][e]);
-                all_from = max(all_from, from[nt][e]);
-                all_to = min(all_to, to[nt][e]);
+        }
+        __syncthreads();
+        if (NT > 1) {
+            if (threadIdx.x == 0) {
+                int from = 0, to = sq.len;
+                for (int r = 0; r < kRows; ++r) {
+                    from = max(from, row_from[r]);
+                    to = min(to, row_to[r]);
+                }
+                all_seen[0] = from;
+                all_seen[1] = to;
             }
+            __syncthreads();
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            all_from = max(all_from, __shfl_xor_sync(0xffffffffu, all_from, o));
-            all_to = min(all_to, __shfl_xor_sync(0xffffffffu, all_to, o));
-        }
-
+        const int all_from = all_seen[0], all_to = all_seen[1];   // places that every row sees
+        float mul[NT][2];
         float o[NT][kT][4], sub[NT][2], sum[NT][2];   // sub: what scores lose before ex2
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -312,113 +473,66 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                mul[nt][e] = row_mul[8 * nt + 2 * t4 + e];
                 sub[nt][e] = -INFINITY;
                 sum[nt][e] = 0.f;
             }
         }
 
-        const uint8_t *buf = my_buf + (kStages - 1) * Sh::kGroupBytes;
-        int t0 = sq.lo + (grp0 - kWarps) * kGroup;
-        for (int i = 0; i < steps; ++i) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            issue(i + kStages - 1);
-            buf = buf == my_buf + (kStages - 1) * Sh::kGroupBytes ? my_buf : buf + Sh::kGroupBytes;
-            t0 += kTile;
+        int t0 = place0 + warp * kGroup;
+        for (int i = 0; i < n_copy; ++i, t0 += kTile) {
+            if (next == i + Sh::kLead && next < n_copy) {
+                produce(next, next_page);
+                next += kWarps;
+                next_page = fetch(next);
+            }
+            const uint32_t n = tiles_before + i, stage = n % kStages;
+            const bool arrived = waits.on(full + stage, (n / kStages) & 1);
+            if (!arrived || t0 >= sq.len) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty + stage);
+                continue;
+            }
+            const uint8_t *buf = smem + stage * Sh::kStage + warp * (kGroup * D / 2);
+            const uint8_t *sbuf = smem + stage * Sh::kStage + Sh::kKScale + warp * (kGroup * D / 16);
             const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
-            // S^T
             float s[NT][4];
-            {
-                uint32_t kw[2][kW];
-                __half2 ks[2][kW / 2];      // scale of each block, twice
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = place_of(g) + 8 * r;
-                    const uint8_t *p = buf + row * (D / 2) + t4 * (D / 8);
-                    const uint8_t *sp = buf + 16 * D + row * (D / 16) + t4 * (D / 64);
-                    if constexpr (D == 64) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-                        kw[r][0] = w.x; kw[r][1] = w.y;
-                        const uint32_t one = e4m3x2_f16(*sp);
-                        ks[r][0] = __low2half2(*reinterpret_cast<const __half2 *>(&one));
-                    } else {
-#pragma unroll
-                        for (int w4 = 0; w4 < kW / 4; ++w4) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(p + 16 * w4);
-                            kw[r][4 * w4] = w.x; kw[r][4 * w4 + 1] = w.y;
-                            kw[r][4 * w4 + 2] = w.z; kw[r][4 * w4 + 3] = w.w;
-                            const uint32_t two = e4m3x2_f16(
-                                *reinterpret_cast<const uint16_t *>(sp + 2 * w4));
-                            ks[r][2 * w4] =
-                                __low2half2(*reinterpret_cast<const __half2 *>(&two));
-                            ks[r][2 * w4 + 1] =
-                                __high2half2(*reinterpret_cast<const __half2 *>(&two));
-                        }
-                    }
-                }
-                float s2[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kW; ++w) {
-                    uint32_t r0[4], r1[4];
-                    e2m1x8_f16(kw[0][w], r0);
-                    e2m1x8_f16(kw[1][w], r1);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r0[e] = mul2(r0[e], ks[0][w / 2]);
-                        r1[e] = mul2(r1[e], ks[1][w / 2]);
-                    }
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(s[nt], r0[0], r1[0], r0[1], r1[1], qf[part][nt][2 * w][0],
-                                     qf[part][nt][2 * w][1]);
-                            mma16816(s2[nt], r0[2], r1[2], r0[3], r1[3], qf[part][nt][2 * w + 1][0],
-                                     qf[part][nt][2 * w + 1][1]);
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
-            }
+            scores<D, NT, kParts>(buf, sbuf, g, t4, queries + lane, s);
+            VShare<D> v;
+            v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty + stage);
 
             // Scores in log2 units less the row's `sub`, so that the row's largest number
             // is about kLift.  One comparison finds those that call for more: above
             // kLift + kRaise the maximum moves; below kLow probabilities lose bits.
-            float t[NT][4], rest[NT][4];
-            bool more = false, low = false;
+            float t[NT][4];
+            bool more = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    t[nt][e] = fmaf(s[nt][e], mul[nt][e & 1], -sub[nt][e & 1]);
+                    float &y = t[nt][e];
+                    y = fmaf(s[nt][e], mul[nt][e & 1], -sub[nt][e & 1]);
                     if (!whole) {
-                        const int at = t0 + place_of(g) + 8 * (e >> 1);
-                        if (at < from[nt][e & 1] || at >= to[nt][e & 1]) t[nt][e] = -INFINITY;
+                        const int at = t0 + place_of(g) + 8 * (e >> 1), r = 8 * nt + 2 * t4 + (e & 1);
+                        if (at < row_from[r] || at >= row_to[r]) y = -INFINITY;
                     }
-                    more = more || fabsf(t[nt][e] - kMid) > kHalf;
+                    more = more || fabsf(y - kMid) > kHalf;
                 }
-            }
             const bool extra = __any_sync(0xffffffffu, more);
             if (extra) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        // (an infinite t: the row's first score; its own score decides then)
-                        float y[2];
+                        // (+infinity in t is a row's first score: its own value decides)
+                        float m = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const bool out = t[nt][e + 2 * k] == -INFINITY;
-                            y[k] = out ? -INFINITY : s[nt][e + 2 * k] * mul[nt][e];
-                        }
-                        float m = fmaxf(y[0], y[1]);
+                        for (int k = e; k < 4; k += 2)
+                            m = fmaxf(m, t[nt][k] == -INFINITY ? -INFINITY
+                                                               : s[nt][k] * mul[nt][e]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -434,13 +548,15 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (t[nt][e + 2 * k] != -INFINITY)
-                                t[nt][e + 2 * k] =
-                                    fmaf(s[nt][e + 2 * k], mul[nt][e], -sub[nt][e]);
+                        for (int k = e; k < 4; k += 2)
+                            if (t[nt][k] != -INFINITY)
+                                t[nt][k] = fmaf(s[nt][k], mul[nt][e], -sub[nt][e]);
                     }
             }
+
             uint32_t pf[kParts][NT][2];
+            float rest[NT][4];
+            bool low = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
@@ -462,48 +578,25 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 }
                 operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
             }
-
-            // O^T
-            uint32_t vw[4][kV], vs[4];       // lane's tokens t4, 4 + (t4 ^ 1), 8 more each
-            constexpr int kBlocks = D == 256 ? 2 : 1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 4 * j + ((j & 1) ? t4 ^ 1 : t4);
-                const uint8_t *p = buf + 8 * D + row * (D / 2) + g * (D / 16);
-                const uint8_t *sp = buf + 17 * D + row * (D / 16) + g * D / 128;
-                if constexpr (D == 64) {
-                    vw[j][0] = *reinterpret_cast<const uint32_t *>(p);
-                    vs[j] = *sp;
-                } else if constexpr (D == 128) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-                    vw[j][0] = w.x; vw[j][1] = w.y;
-                    vs[j] = *sp;
-                } else {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-                    vw[j][0] = w.x; vw[j][1] = w.y; vw[j][2] = w.z; vw[j][3] = w.w;
-                    vs[j] = *reinterpret_cast<const uint16_t *>(sp);
-                }
-            }
             if (!whole) {
-                // Places behind the sequence's end (or before what any row sees) may hold
-                // anything: their scales become 0.  A NaN that some rows see and others do
-                // not would reach all of them through 0 * NaN: it is taken out of the
-                // product and put into the rows that see it.
+                // Places behind the sequence's end may hold anything: their scales become 0.
+                // A NaN that some rows see and others do not would reach all of them through
+                // 0 * NaN: it is taken out of the product and put into the rows that see it.
+                constexpr int kBlocks = VShare<D>::kBlocks;
                 uint32_t nan[kBlocks] = {};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int off = 4 * j + ((j & 1) ? t4 ^ 1 : t4);
-                    if (t0 + off >= sq.len) vs[j] = 0;
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k)
-                        if (((vs[j] >> (8 * k)) & 0x7f) == 0x7f) {
-                            nan[k] |= 1u << off;
-                            vs[j] &= ~(0xffu << (8 * k));
-                        }
-                }
                 bool any = false;
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k) any = any || nan[k];
+                for (int j = 0; j < 4; ++j) {
+                    const int off = v.place(j, t4);
+                    if (t0 + off >= sq.len) v.sb[j] = 0;
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k)
+                        if (((v.sb[j] >> (8 * k)) & 0x7f) == 0x7f) {
+                            nan[k] |= 1u << off;
+                            any = true;
+                            v.sb[j] &= ~(0xffu << (8 * k));
+                        }
+                }
                 if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
                     for (int k = 0; k < kBlocks; ++k) {
@@ -513,8 +606,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int lo = min(16, max(0, from[nt][e] - t0));
-                                const int hi = min(16, max(0, to[nt][e] - t0));
+                                const int r = 8 * nt + 2 * t4 + e;
+                                const int lo = min(16, max(0, row_from[r] - t0));
+                                const int hi = min(16, max(0, row_to[r] - t0));
                                 const uint32_t seen = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
                                 if (nan[k] & seen) {
 #pragma unroll
@@ -527,51 +621,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     }
                 }
             }
-            uint32_t sc[kBlocks][2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t x = vs[2 * e], y = vs[2 * e + 1];
-                sc[0][e] = e4m3x2_f16(__byte_perm(x, y, 0x0040));
-                if constexpr (kBlocks == 2) sc[kBlocks - 1][e] = e4m3x2_f16(__byte_perm(x, y, 0x0051));
-            }
-            // O^T += V^T P^T, or O^T += factor * (V^T P^T)
-            auto product = [&](auto plain, float factor) {
-#pragma unroll
-                for (int w = 0; w < kV; ++w) {
-                    constexpr uint32_t kEven = 0x0f0f0f0fu;
-                    uint32_t e1[4], d1[4], e2[4], d2[4];   // even and odd elements of the two pairs
-                    e2m1x8_f16((vw[0][w] & kEven) | ((vw[1][w] << 4) & ~kEven), e1);
-                    e2m1x8_f16(((vw[0][w] >> 4) & kEven) | (vw[1][w] & ~kEven), d1);
-                    e2m1x8_f16((vw[2][w] & kEven) | ((vw[3][w] << 4) & ~kEven), e2);
-                    e2m1x8_f16(((vw[2][w] >> 4) & kEven) | (vw[3][w] & ~kEven), d2);
-                    const __half2 s1 = *reinterpret_cast<const __half2 *>(&sc[w / 2 % kBlocks][0]);
-                    const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc[w / 2 % kBlocks][1]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a0 = mul2(e1[k], s1), a1 = mul2(d1[k], s1);
-                        const uint32_t a2 = mul2(e2[k], s2), a3 = mul2(d2[k], s2);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float (&acc)[4] = o[nt][4 * w + k];
-                            if constexpr (plain.value) {
-#pragma unroll
-                                for (int part = 0; part < kParts; ++part)
-                                    mma16816(acc, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
-                            } else {
-                                float x[4] = {};
-#pragma unroll
-                                for (int part = 0; part < kParts; ++part)
-                                    mma16816(x, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
-                            }
-                        }
-                    }
-                }
-            };
-            product(std::true_type{}, 1.f);
+            product<D, NT, kParts, false>(v, pf, 1.f, o);
             if (extra && __any_sync(0xffffffffu, low)) {
-                // what lies a factor kBand below the last product's range, until nothing is left
+                // what lies a factor kBand below the last product's range, until nothing is
+                // left
                 float factor = 1.f;
                 do {
                     factor *= 1.f / kBand;
@@ -588,11 +641,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                         }
                         operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
                     }
-                    product(std::false_type{}, factor);
+                    product<D, NT, kParts, true>(v, pf, factor, o);
                 } while (__any_sync(0xffffffffu, low));
             }
         }
-        cp_wait<0>();
+        tiles_before += n_copy;
 
         // the warps' sums of this piece
 #pragma unroll
@@ -603,62 +656,69 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                sum[nt][e] = x;
                 if (g == 0) warp_ml[warp][8 * nt + 2 * t4 + e] = make_float2(sub[nt][e], x);
             }
-        __syncthreads();      // every warp is done with its ring as well
-        float *merge = reinterpret_cast<float *>(ring);
+        if (abort_flag && next >= kWarps && n_copy > 0) {
+            // a wait gave up: the last copy this warp issued is still waited for
+            const uint32_t n = tiles_before - n_copy + next - kWarps;
+            ptx::mbar_wait(full + n % kStages, (n / kStages) & 1, a.wait_limit);
+        }
+        __syncthreads();              // every warp is done with the ring as well
+        float *merge = reinterpret_cast<float *>(smem);
+        const bool complete = tile0 == 0 && tile1 == n_tiles;
+        const long long slot = 2ll * blockIdx.x + (cur == beg ? 0 : 1);
+        if (threadIdx.x == 0 && tile0 == 0 && !complete) {
+            const long long end_tile = cur + n_tiles;
+            const int last = (int)((end_tile * ctas - 1) / plan.total);   // CTA of its last tile
+            a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, row0, rows};
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            if (8 * nt >= rows) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + 2 * t4 + e;
+                const int r = 2 * t4 + e;
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r].x);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][8 * nt + r].x);
                 const float f = m == -INFINITY ? 1.f : ex2(sub[nt][e] - m);
-                float *p = merge + (warp * Sh::kRows + r) * D + g * (D / 8);
+                float *p = merge + (warp * 8 + r) * D + g * (D / 8);
 #pragma unroll
                 for (int k = 0; k < kT; ++k)
                     *reinterpret_cast<float2 *>(p + 2 * k) =
                         make_float2(o[nt][k][e] * f, o[nt][k][e + 2] * f);
             }
-        __syncthreads();
-        const bool complete = tile0 == 0 && tile1 == n_tiles;
-        const long long slot = 2ll * blockIdx.x + (cur == beg ? 0 : 1);
-        if (threadIdx.x == 0 && tile0 == 0 && !complete) {
-            const long long end_tile = cur + n_tiles;    // CTA of its last tile: below
-            const int last = (int)((end_tile * ctas - 1) / plan.total);
-            a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, row0, rows};
-        }
-        for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
-            const int r = x / (D / 4), d = 4 * (x - r * (D / 4));
-            float m = -INFINITY, l = 0.f;
+            __syncthreads();
+            for (int x = threadIdx.x; x < min(8, rows - 8 * nt) * (D / 4); x += kThreads) {
+                const int r8 = x / (D / 4), r = 8 * nt + r8, d = 4 * (x - r8 * (D / 4));
+                float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r].x);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = warp_ml[w][r];
-                l += ml.y * (m == -INFINITY ? 1.f : ex2(ml.x - m));
-                const float4 y =
-                    *reinterpret_cast<const float4 *>(merge + (w * Sh::kRows + r) * D + d);
-                v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 ml = warp_ml[w][r];
+                    l += ml.y * (m == -INFINITY ? 1.f : ex2(ml.x - m));
+                    const float4 y =
+                        *reinterpret_cast<const float4 *>(merge + (w * 8 + r8) * D + d);
+                    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+                }
+                if (complete) {
+                    const int rr = row0 + r, j = rr / a.G, hq = h * a.G + rr - j * a.G;
+                    const float inv = l == 0.f ? 0.f : gv / l;
+                    T *p = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + hq * a.o_head + d;
+                    store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (a.lse && d == 0)
+                        a.lse[(long long)(sq.first + j) * a.Hq + hq] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                } else {
+                    store4(a.part_o + (slot * kRows + r) * D + d, v.x, v.y, v.z, v.w);
+                    if (d == 0) a.part_ml[slot * kRows + r] = make_float2(m, l);
+                }
             }
-            if (complete) {
-                const int rr = row0 + r, j = rr / a.G, hq = h * a.G + rr - j * a.G;
-                const float inv = l == 0.f ? 0.f : gv / l;
-                T *p = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + hq * a.o_head + d;
-                store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                if (a.lse && d == 0)
-                    a.lse[(long long)(sq.first + j) * a.Hq + hq] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            } else {
-                store4(a.part_o + (slot * Sh::kRows + r) * D + d, v.x, v.y, v.z, v.w);
-                if (d == 0) a.part_ml[slot * Sh::kRows + r] = make_float2(m, l);
-            }
+            ptx::fence_proxy_async_smem();     // before copies go into the ring again
+            __syncthreads();
         }
-        __syncthreads();
         cur += tile1 - tile0;
     }
 }
@@ -747,7 +807,7 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     }, 0);
     if (resident < 1) return GDN_ERR_CUDA;
     const long long rt = ((long long)a.max_new * a.G + Sh::kRows - 1) / Sh::kRows;
-    const long long tiles = a.max_len / kTile + 1;
+    const long long tiles = a.max_len / kTile + 2;
     long long most = rt * a.kv.H * tiles;   // of one sequence; of all, without overflow:
     most = most > resident ? resident : most * a.kv.N;
     const int grid = (int)(most < resident ? (most < 1 ? 1 : most) : resident);
@@ -793,7 +853,7 @@ gdn_status pick(AttnArgs &a, cudaStream_t st) {
     switch (a.kv.d) {
         case 64: return launch<T, 64, 1, kSplit, 4, kSplit ? 1 : 2>(a, st);
         case 128: return launch<T, 128, 1, kSplit, 4, kSplit ? 1 : 2>(a, st);
-        default: return launch<T, 256, 1, kSplit, 3, 1>(a, st);
+        default: return launch<T, 256, 1, kSplit, 4, 1>(a, st);
     }
 }
 
@@ -834,6 +894,8 @@ extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn
     a.window = window;
     a.causal = (flags & GDN_ATTN_CAUSAL) != 0;
     a.err = gdn::device_error_word();
+    const long long limit = gdn::option(GDN_OPT_WAIT_LIMIT);
+    a.wait_limit = limit > 0 ? (uint32_t)(limit > 0x7fffffffLL ? 0x7fffffffLL : limit) : (1u << 22);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dt == GDN_BF16 ? pick<__nv_bfloat16, false>(a, st) : pick<float, true>(a, st);
 }

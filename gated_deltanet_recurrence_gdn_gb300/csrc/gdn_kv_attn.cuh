@@ -22,6 +22,7 @@ struct AttnArgs {
     float2 *part_ml;           // [2 * grid][rows]: what scores lost (log2 units) and sum
     struct Cut *cuts;          // [grid], nullptr where nothing is cut
     int *err;
+    uint32_t wait_limit;       // polls of a wait before it gives up
 };
 
 // A (sequence, key/value head, row tile) that is cut, written by the CTA with its
@@ -35,7 +36,8 @@ struct Cut {
 // key/value head) is query head h G + r % G of new token r / G.
 struct Seq {
     int first, n, len;
-    int lo;                    // first place that any row sees, rounded down to 16
+    int lo;                    // first place that any row sees, rounded down to a page or
+                               // to 128, whichever is less
     int span;                  // places [lo, lo + span) cover what any row sees
 
     __device__ __forceinline__ void get(const AttnArgs &a, int b) {
@@ -46,7 +48,7 @@ struct Seq {
             if (n > a.max_new) n = 0;
         }
         lo = 0;
-        if (a.window > 0) lo = max(0, len - n + 1 - a.window) & ~15;
+        if (a.window > 0) lo = max(0, len - n + 1 - a.window) & -min(a.kv.page_size(), 128);
         span = max(0, len - lo);
     }
     // Places [from, to) that new token j sees.
