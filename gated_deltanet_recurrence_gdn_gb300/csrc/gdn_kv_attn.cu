@@ -35,6 +35,9 @@
 #include "gdn_kv_attn.cuh"
 #include "tc_ptx.cuh"
 
+#define KU 2
+#define KS 3
+#define KX 0
 namespace gdn {
 namespace kv {
 namespace {
@@ -42,7 +45,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
-constexpr int kTile = kWarps * kGroup;
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -64,6 +66,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -77,6 +87,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+// Bits of a where `mask` is set, of b elsewhere.
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
+    return r;
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -107,8 +123,10 @@ __device__ __forceinline__ void operand_of(const float (&p)[4], uint32_t (&hi)[2
 }
 
 // kSplit: queries and probabilities as two fp16 numbers each (fp32 I/O).
-template <int D, int NT, bool kSplit, int kStages>
+// kU: groups of a warp in a tile.
+template <int D, int NT, bool kSplit, int kU, int kStages>
 struct Shape {
+    static constexpr int kTile = kWarps * kU * kGroup;
     static constexpr int kRows = 8 * NT;
     static constexpr int kParts = kSplit ? 2 : 1;
     // a stage: key codes, value codes, key scales, value scales of a tile
@@ -183,10 +201,6 @@ __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scal
     }
     float s2[NT][4];                // a second chain of products
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-#pragma unroll
     for (int w = 0; w < kW; ++w) {
         uint32_t r0[4], r1[4];
         e2m1x8_f16(kw[0][w], r0);
@@ -201,8 +215,13 @@ __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scal
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint4 q = queries[((part * NT + nt) * kW + w) * 32];
-                mma16816(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
-                mma16816(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
+                if (w == 0 && part == 0) {
+                    mma16816_zero(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
+                    mma16816_zero(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
+                } else {
+                    mma16816(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
+                    mma16816(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
+                }
             }
     }
 #pragma unroll
@@ -263,10 +282,10 @@ __device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)
     for (int w = 0; w < VShare<D>::kWords; ++w) {
         constexpr uint32_t kEven = 0x0f0f0f0fu;
         uint32_t e1[4], d1[4], e2[4], d2[4];   // even and odd elements of the two token pairs
-        e2m1x8_f16((v.w[0][w] & kEven) | ((v.w[1][w] << 4) & ~kEven), e1);
-        e2m1x8_f16(((v.w[0][w] >> 4) & kEven) | (v.w[1][w] & ~kEven), d1);
-        e2m1x8_f16((v.w[2][w] & kEven) | ((v.w[3][w] << 4) & ~kEven), e2);
-        e2m1x8_f16(((v.w[2][w] >> 4) & kEven) | (v.w[3][w] & ~kEven), d2);
+        e2m1x8_f16(select_bits(v.w[0][w], v.w[1][w] << 4, kEven), e1);
+        e2m1x8_f16(select_bits(v.w[0][w] >> 4, v.w[1][w], kEven), d1);
+        e2m1x8_f16(select_bits(v.w[2][w], v.w[3][w] << 4, kEven), e2);
+        e2m1x8_f16(select_bits(v.w[2][w] >> 4, v.w[3][w], kEven), d2);
         const __half2 s1 = sc[w / 2 % VShare<D>::kBlocks][0], s2 = sc[w / 2 % VShare<D>::kBlocks][1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -292,9 +311,10 @@ __device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)
     }
 }
 
-template <typename T, int D, int NT, bool kSplit, int kStages, int kMinCtas>
+template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
-    using Sh = Shape<D, NT, kSplit, kStages>;
+    using Sh = Shape<D, NT, kSplit, kU, kStages>;
+    constexpr int kTile = Sh::kTile;
     using P = Plan<kTile, Sh::kRows, kThreads>;
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
     constexpr int kParts = Sh::kParts, kRows = Sh::kRows;
@@ -331,13 +351,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
 
     // Copies: lane (run, part) of the issuing warp copies one part of a run of tokens
     // that lie together, a page's or as many of it as make a tile.
-    const int run = min(a.kv.page_size(), kTile);
+    const int run = min(a.kv.page_size(), 128);
     const int lane_run = lane >> 2, lane_part = lane & 3;
     const int row_bytes = lane_part < 2 ? D / 2 : D / 16;
-    const uint32_t lane_dst = (lane_part == 0   ? 0
-                               : lane_part == 1 ? Sh::kVCode
-                               : lane_part == 2 ? Sh::kKScale
-                                                : Sh::kVScale) + lane_run * run * row_bytes;
+    const uint32_t lane_dst = lane_part == 0   ? 0
+                              : lane_part == 1 ? Sh::kVCode
+                              : lane_part == 2 ? Sh::kKScale
+                                               : Sh::kVScale;
+    constexpr int kRuns = kTile / 16 / 8;         // of a lane, at the smallest pages
     uint32_t tiles_before = 0;      // of the earlier pieces: a tile's stage and phase
     int b;
     long long seq_start;
@@ -358,36 +379,44 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         const int rows = min(kRows, sq.n * a.G - row0);
         const int place0 = sq.lo + tile0 * kTile, n_copy = sq.span > 0 ? tile1 - tile0 : 0;
 
-        // page of the lane's run of tile i, -1 if there is none to copy
-        auto fetch = [&](int i) {
-            const int at = place0 + i * kTile + lane_run * run;
-            return i < n_copy && lane_run * run < kTile && at < sq.len ? a.kv.page_of(b, at, a.err)
+        // pages of the lane's runs (8 apart) of tile i, -1 if there is none to copy
+        auto fetch = [&](int i, int (&page)[kRuns]) {
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int in_tile = (lane_run + 8 * k) * run, at = place0 + i * kTile + in_tile;
+                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_of(b, at, a.err)
                                                                        : -1;
+            }
         };
-        auto produce = [&](int i, int page) {    // one warp
+        auto produce = [&](int i, const int (&page)[kRuns]) {    // one warp
             const uint32_t n = tiles_before + i, stage = n % kStages;
             if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
-            const uint32_t runs = __popc(__ballot_sync(0xffffffffu, page >= 0 && lane_part == 0));
+            uint32_t runs = 0;
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k)
+                runs += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && lane_part == 0));
             if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
             __syncwarp();
-            if (page >= 0) {
-                const int at = (place0 + i * kTile + lane_run * run) & (a.kv.page_size() - 1);
-                const int psz = a.kv.page_size();
-                const uint8_t *src = a.kv.pages + a.kv.block(page, h) + at * row_bytes +
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                if (page[k] < 0) continue;
+                const int psz = a.kv.page_size(), in_tile = (lane_run + 8 * k) * run;
+                const int at = (place0 + i * kTile + in_tile) & (psz - 1);
+                const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + at * row_bytes +
                                      (lane_part == 0   ? 0
                                       : lane_part == 1 ? v_code_at(psz, D, 0)
                                       : lane_part == 2 ? k_scale_at(psz, D, 0)
                                                        : v_scale_at(psz, D, 0));
-                bulk_load(ring_at + stage * Sh::kStage + lane_dst, src, run * row_bytes,
-                          full + stage);
+                bulk_load(ring_at + stage * Sh::kStage + lane_dst + in_tile * row_bytes, src,
+                          run * row_bytes, full + stage);
             }
         };
-        int next = warp;                          // the warp's next tile to copy, and its page
-        int next_page = fetch(next);
+        int next = warp, next_page[kRuns];        // the warp's next tile to copy, and its pages
+        fetch(next, next_page);
         if (next < min(Sh::kLead, n_copy)) {
             produce(next, next_page);
             next += kWarps;
-            next_page = fetch(next);
+            fetch(next, next_page);
         }
 
         // Queries: warp nt, the lane's part of row 8 nt + g, as the B operand, scaled by
@@ -479,30 +508,27 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             }
         }
 
-        int t0 = place0 + warp * kGroup;
-        for (int i = 0; i < n_copy; ++i, t0 += kTile) {
+        for (int i = 0; i < n_copy; ++i) {
             if (next == i + Sh::kLead && next < n_copy) {
                 produce(next, next_page);
                 next += kWarps;
-                next_page = fetch(next);
+                fetch(next, next_page);
             }
             const uint32_t n = tiles_before + i, stage = n % kStages;
             const bool arrived = waits.on(full + stage, (n / kStages) & 1);
-            if (!arrived || t0 >= sq.len) {
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(empty + stage);
-                continue;
-            }
-            const uint8_t *buf = smem + stage * Sh::kStage + warp * (kGroup * D / 2);
-            const uint8_t *sbuf = smem + stage * Sh::kStage + Sh::kKScale + warp * (kGroup * D / 16);
+            const uint8_t *buf = smem + stage * Sh::kStage + warp * (kU * kGroup * D / 2);
+            const uint8_t *sbuf =
+                smem + stage * Sh::kStage + Sh::kKScale + warp * (kU * kGroup * D / 16);
+            int t0 = place0 + i * kTile + warp * (kU * kGroup);
+#pragma unroll 1
+            for (int u = 0; u < kU; ++u, t0 += kGroup, buf += kGroup * D / 2, sbuf += kGroup * D / 16) {
+            if (!arrived || t0 >= sq.len) break;
             const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
             float s[NT][4];
             scores<D, NT, kParts>(buf, sbuf, g, t4, queries + lane, s);
             VShare<D> v;
             v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(empty + stage);
 
             // Scores in log2 units less the row's `sub`, so that the row's largest number
             // is about kLift.  One comparison finds those that call for more: above
@@ -519,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                         const int at = t0 + place_of(g) + 8 * (e >> 1), r = 8 * nt + 2 * t4 + (e & 1);
                         if (at < row_from[r] || at >= row_to[r]) y = -INFINITY;
                     }
-                    more = more || fabsf(y - kMid) > kHalf;
+                    more |= fabsf(y - kMid) > kHalf;
                 }
             const bool extra = __any_sync(0xffffffffu, more);
             if (extra) {
@@ -573,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                             rest[nt][e] = p[e];
                             p[e] = 0.f;
                         }
-                        low = low || rest[nt][e] > 0.f;
+                        low |= rest[nt][e] > 0.f;
                     }
                 }
                 operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
@@ -637,13 +663,16 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                             rest[nt][e] *= kBand;
                             p[e] = rest[nt][e] >= kLow ? rest[nt][e] : 0.f;
                             if (p[e] > 0.f) rest[nt][e] = 0.f;
-                            low = low || rest[nt][e] > 0.f;
+                            low |= rest[nt][e] > 0.f;
                         }
                         operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
                     }
                     product<D, NT, kParts, true>(v, pf, factor, o);
                 } while (__any_sync(0xffffffffu, low));
             }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty + stage);
         }
         tiles_before += n_copy;
 
@@ -789,10 +818,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
             l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <typename T, int D, int NT, bool kSplit, int kStages, int kMinCtas>
+template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinCtas>
 gdn_status launch(AttnArgs &a, cudaStream_t st) {
-    using Sh = Shape<D, NT, kSplit, kStages>;
-    auto kern = k_kv_attn<T, D, NT, kSplit, kStages, kMinCtas>;
+    using Sh = Shape<D, NT, kSplit, kU, kStages>;
+    auto kern = k_kv_attn<T, D, NT, kSplit, kU, kStages, kMinCtas>;
+    constexpr int kTile = Sh::kTile;
     static std::atomic<int> memo[kMaxDeviceMemo];
     // resident CTAs of the device, and the opt-in to the ring's shared memory
     const int resident = per_device(memo, [&](int dev) {
@@ -851,9 +881,9 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
 template <typename T, bool kSplit>
 gdn_status pick(AttnArgs &a, cudaStream_t st) {
     switch (a.kv.d) {
-        case 64: return launch<T, 64, 1, kSplit, 4, kSplit ? 1 : 2>(a, st);
-        case 128: return launch<T, 128, 1, kSplit, 4, kSplit ? 1 : 2>(a, st);
-        default: return launch<T, 256, 1, kSplit, 4, 1>(a, st);
+        case 64: return launch<T, 64, 1, kSplit, KU, KS, kSplit ? 1 : 2>(a, st);
+        case 128: return launch<T, 128, 1, kSplit, KU, KS, kSplit ? 1 : 2>(a, st);
+        default: return launch<T, 256, 1, kSplit, 1, 4, 1>(a, st);
     }
 }
 
