@@ -11,10 +11,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import _DT, _check, _i, _ptr, _stream, _vp, load
+from . import _DT, GdnError, _check, _i, _stream, _vp, load
 
 GDN_ROPE_ADJACENT = 1
 GDN_ROPE_INVERSE = 2
@@ -40,28 +41,40 @@ class _Kv(ctypes.Structure):
                 ("N", _i), ("max_pages", _i), ("n_tokens", _i), ("table_stride", _i64)]
 
 
+# The same structures packed into bytes, which costs a call less than filling a ctypes one (a
+# single token's call is bound by the host).
+_ROWS = struct.Struct("@Pqqqi4x")
+_ROTARY = struct.Struct("@PPPPqqiiiI")
+_KV = struct.Struct("@PPPPPiiiiiii4xq")
+assert (_ROWS.size, _ROTARY.size, _KV.size) == tuple(map(ctypes.sizeof, (_Rows, _Rotary, _Kv)))
+
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+_axes_kept: dict = {}      # axis numbers by their value, as C arrays
+
+
 def _rows3(name, t, heads, n, d, dtype):
     """[tokens, heads, d] rows."""
-    if not t.is_cuda or t.dtype != dtype or t.shape != (n, heads, d) or t.stride(2) != 1:
+    tok, head, one = t.stride()
+    if t.shape != (n, heads, d) or one != 1 or t.dtype != dtype or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor [tokens, heads, d] of the call's dtype, its last "
                          "dimension contiguous" % name)
     # (a dimension of one entry may have any stride)
-    return _Rows(t.data_ptr(), 0, t.stride(1) if heads > 1 else 0, t.stride(0) if n > 1 else 0,
-                 heads)
+    return _ROWS.pack(t.data_ptr(), 0, head if heads > 1 else 0, tok if n > 1 else 0, heads)
 
 
 def _rows4(name, t, like, heads):
-    """[B, heads, T, d] rows."""
+    """[B, heads, T, d] rows, like's but for the heads."""
     B, _, T, d = like.shape
-    if not t.is_cuda or t.dtype != like.dtype or t.shape != (B, heads, T, d) or t.stride(3) != 1:
+    if t.shape != (B, heads, T, d) or t.stride(3) != 1 or t.dtype != like.dtype or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor [B, heads, T, d] of the call's dtype, its last "
                          "dimension contiguous" % name)
-    return _Rows(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if heads > 1 else 0,
-                 t.stride(2) if T > 1 else 0, heads)
+    seq, head, tok, _ = t.stride()
+    return _ROWS.pack(t.data_ptr(), seq if B > 1 else 0, head if heads > 1 else 0,
+                      tok if T > 1 else 0, heads)
 
 
 def _int32(name, t, dims):
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != dims or \
+    if t.dim() != dims or t.dtype != _i32 or not t.is_cuda or \
             (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError("%s must be a %d-D int32 CUDA tensor, its last dimension contiguous"
                          % (name, dims))
@@ -69,29 +82,34 @@ def _int32(name, t, dims):
 
 def _rotary(cos, sin, pos, axes, flags, shape):
     """shape: the shape that one axis of `pos` has, or may have without its first part."""
-    if not cos.is_cuda or not sin.is_cuda or cos.dtype != torch.float32 or \
-            sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape or \
-            not cos.is_contiguous() or not sin.is_contiguous():
+    table = cos.shape
+    if cos.dim() != 2 or table != sin.shape or cos.dtype != _f32 or sin.dtype != _f32 or \
+            not cos.is_cuda or not sin.is_cuda or not cos.is_contiguous() or \
+            not sin.is_contiguous():
         raise ValueError("cos and sin must be contiguous fp32 CUDA tensors [positions, d_rot / 2]")
-    half = cos.shape[1]
     lead = 0 if axes is None else 1
     whole = pos.dim() == lead + len(shape)
     _int32("pos", pos, lead + (len(shape) if whole else 1))
-    if tuple(pos.shape[lead:]) != (shape if whole else shape[-1:]):
+    if pos.shape[lead:] != (shape if whole else shape[-1:]):
         raise ValueError("pos must hold a position per token%s" % (" on each axis" if lead else ""))
-    if axes is not None:
+    at = 0
+    if lead:
         axes = bytes(axes)
-        if len(axes) != half:
+        if len(axes) != table[1]:
             raise ValueError("axes must give the axis of each of the d_rot / 2 pairs")
-    return _Rotary(cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), axes,
-                   pos.stride(0) if lead else 0,
-                   pos.stride(lead) if whole and len(shape) == 2 else 0, cos.shape[0], 2 * half,
-                   pos.shape[0] if lead else 1, flags)
+        kept = _axes_kept.get(axes)
+        if kept is None:
+            kept = _axes_kept[axes] = ctypes.create_string_buffer(axes, max(1, len(axes)))
+        at = ctypes.addressof(kept)
+    return _ROTARY.pack(cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), at,
+                        pos.stride(0) if lead else 0,
+                        pos.stride(lead) if whole and len(shape) == 2 else 0, table[0],
+                        2 * table[1], pos.shape[0] if lead else 1, flags)
 
 
 def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d):
-    if not pages.is_cuda or pages.dtype != torch.uint8 or pages.dim() != 3 or \
-            not pages.is_contiguous():
+    """The packed gdn_kv, and the cache's heads and page size."""
+    if pages.dim() != 3 or pages.dtype != _u8 or not pages.is_cuda or not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 CUDA tensor [n_pages, heads, page bytes]")
     n_pages, heads, size = pages.shape
     page_size = size * 8 // (9 * d)
@@ -99,49 +117,39 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d):
         raise ValueError("a page of %d bytes does not hold rows of d = %d" % (size, d))
     _int32("page_table", page_table, 2)
     _int32("kv_len", kv_len, 1)
-    N = kv_len.shape[0]
-    if page_table.shape[0] != N:
+    N, (rows, max_pages) = kv_len.shape[0], page_table.shape
+    if rows != N:
         raise ValueError("page_table must have a row per sequence")
-    cu = None
+    cu = 0
     if cu_seqlens is not None:
         _int32("cu_seqlens", cu_seqlens, 1)
         if cu_seqlens.shape[0] != N + 1:
             raise ValueError("cu_seqlens must have one entry more than there are sequences")
         cu = cu_seqlens.data_ptr()
-    elif N == 0 or n_tokens % N:
-        if n_tokens:
-            raise ValueError("without cu_seqlens every sequence has the same number of tokens")
-    scale = None
+    elif n_tokens and (N == 0 or n_tokens % N):
+        raise ValueError("without cu_seqlens every sequence has the same number of tokens")
+    scale = 0
     if kv_scale is not None:
-        if not kv_scale.is_cuda or kv_scale.dtype != torch.float32 or \
-                kv_scale.shape != (2, heads) or not kv_scale.is_contiguous():
+        if kv_scale.shape != (2, heads) or kv_scale.dtype != _f32 or not kv_scale.is_cuda or \
+                not kv_scale.is_contiguous():
             raise ValueError("kv_scale must be a contiguous fp32 CUDA tensor [2, heads]")
         scale = kv_scale.data_ptr()
-    return _Kv(pages.data_ptr(), scale, page_table.data_ptr(), kv_len.data_ptr(), cu, n_pages,
-               page_size, heads, d, N, page_table.shape[1], n_tokens, page_table.stride(0))
+    return _KV.pack(pages.data_ptr(), scale, page_table.data_ptr(), kv_len.data_ptr(), cu, n_pages,
+                    page_size, heads, d, N, max_pages, n_tokens, page_table.stride(0)), \
+        heads, page_size
 
 
-class _on:
-    """The tensor's device made current, where it is not already."""
-
-    def __init__(self, device):
-        self.guard = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _finish(rc, what, check, device):
-    _check(rc, what)
+def _call(fn, what, t, check, *args):
+    """fn(*args, stream) on t's device and its current stream."""
+    at = t.get_device()
+    if torch._C._cuda_getDevice() != at:
+        with torch.cuda.device(at):
+            return _call(fn, what, t, check, *args)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(at))
+    if rc:
+        raise GdnError(rc, what)
     if check:
-        _check(load().gdn_sync_check(_stream(device)), what + " (device)")
+        _check(load().gdn_sync_check(_stream(t.device)), what + " (device)")
 
 
 def gdn_kv_page_bytes(page_size: int, d: int) -> int:
@@ -183,22 +191,17 @@ def gdn_rope_axes(sections, interleave=False):
 
 
 def _rope(q, k, cos, sin, pos, axes, flags, out, check, what):
-    lib = load()
     if q.dtype not in _DT or q.dim() != 4:
         raise ValueError("q must be [B, heads, T, d], bf16 or fp32")
     B, Hq, T, d = q.shape
     qo, ko = out if out is not None else (torch.empty_like(q),
                                           None if k is None else torch.empty_like(k))
-    rq, rqo = _rows4("q", q, q, Hq), _rows4("out[0]", qo, q, Hq)
     rk = rko = None
     if k is not None:
-        rk, rko = _rows4("k", k, q, k.shape[1]), _rows4("out[1]", ko, q, k.shape[1])
-    rot = _rotary(cos, sin, pos, axes, flags, (B, T))
-    with _on(q.device):
-        rc = lib.gdn_rope(ctypes.byref(rq), ctypes.byref(rqo), rk and ctypes.byref(rk),
-                          rko and ctypes.byref(rko), B, T, d, ctypes.byref(rot), _DT[q.dtype],
-                          _stream(q.device))
-        _finish(rc, what, check, q.device)
+        Hk = k.shape[1]
+        rk, rko = _rows4("k", k, q, Hk), _rows4("out[1]", ko, q, Hk)
+    _call(load().gdn_rope, what, q, check, _rows4("q", q, q, Hq), _rows4("out[0]", qo, q, Hq), rk,
+          rko, B, T, d, _rotary(cos, sin, pos, axes, flags, (B, T)), _DT[q.dtype])
     return qo, ko
 
 
@@ -229,25 +232,21 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     pages: the cache (gdn_kv_pages), written in place; page_table int32 [N, pages]; kv_len int32
     [N], the sequences' tokens with the new ones; cu_seqlens int32 [N + 1] or None for the same
     number of new tokens each; kv_scale fp32 [2, heads]: a further scale per head."""
-    lib = load()
     if k.dtype not in _DT or k.dim() != 3:
         raise ValueError("k must be [tokens, heads, d], bf16 or fp32")
-    n, heads, d = k.shape
-    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
-    rk, rv = _rows3("k", k, kv.heads, n, d, k.dtype), _rows3("v", v, kv.heads, n, d, k.dtype)
+    n, _, d = k.shape
+    dtype = k.dtype
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
     rq = rqo = rot = None
     if q is not None:
         if out is None:
             out = torch.empty_like(q)
-        rq = _rows3("q", q, q.shape[1], n, d, k.dtype)
-        rqo = _rows3("out", out, q.shape[1], n, d, k.dtype)
+        Hq = q.shape[1]
+        rq, rqo = _rows3("q", q, Hq, n, d, dtype), _rows3("out", out, Hq, n, d, dtype)
     if cos is not None:
         rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,))
-    with _on(k.device):
-        rc = lib.gdn_kv_append(ctypes.byref(kv), ctypes.byref(rk), ctypes.byref(rv),
-                               rq and ctypes.byref(rq), rqo and ctypes.byref(rqo),
-                               rot and ctypes.byref(rot), _DT[k.dtype], _stream(k.device))
-        _finish(rc, "gdn_kv_append", check, k.device)
+    _call(load().gdn_kv_append, "gdn_kv_append", k, check, kv, _rows3("k", k, heads, n, d, dtype),
+          _rows3("v", v, heads, n, d, dtype), rq, rqo, rot, _DT[dtype])
     return out if q is not None else None
 
 
@@ -255,17 +254,15 @@ def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_s
                 dtype=torch.bfloat16, out=None, check=False):
     """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
     they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
-    lib = load()
-    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d)
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d)
     if out is None:
-        k, v = torch.empty((2, n_tokens, kv.heads, d), dtype=dtype, device=pages.device).unbind(0)
+        k = torch.empty((n_tokens, heads, d), dtype=dtype, device=pages.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
-    rk, rv = (_rows3("out", t, kv.heads, n_tokens, d, dtype) for t in (k, v))
-    with _on(pages.device):
-        rc = lib.gdn_kv_read(ctypes.byref(kv), ctypes.byref(rk), ctypes.byref(rv), _DT[dtype],
-                             _stream(pages.device))
-        _finish(rc, "gdn_kv_read", check, pages.device)
+    _call(load().gdn_kv_read, "gdn_kv_read", pages, check, kv,
+          _rows3("out", k, heads, n_tokens, d, dtype), _rows3("out", v, heads, n_tokens, d, dtype),
+          _DT[dtype])
     return k, v
 
 
@@ -279,22 +276,20 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
     kv_len and on a sequence's tokens in this call, known on the host (default: what the page
     table and q can hold); they plan the launch.  scale: default d^-1/2.  window: a token sees
     the last `window` places up to its own (0: all)."""
-    lib = load()
     if q.dtype not in _DT or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
     n, Hq, d = q.shape
-    kv = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
+    dtype = q.dtype
+    kv, _, page_size = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
     if out is None:
         out = torch.empty_like(q)
-    rq, ro = _rows3("q", q, Hq, n, d, q.dtype), _rows3("out", out, Hq, n, d, q.dtype)
-    lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty((n, Hq), dtype=_f32, device=q.device) if return_lse else None
     if max_len is None:
-        max_len = kv.max_pages * kv.page_size
+        max_len = page_table.shape[1] * page_size
     if max_new is None:
-        max_new = n if cu_seqlens is not None else n // max(kv.N, 1)
-    with _on(q.device):
-        rc = lib.gdn_kv_attn(ctypes.byref(kv), ctypes.byref(rq), ctypes.byref(ro), _ptr(lse),
-                             max_len, max_new, d ** -0.5 if scale is None else scale, window,
-                             GDN_ATTN_CAUSAL if causal else 0, _DT[q.dtype], _stream(q.device))
-        _finish(rc, "gdn_kv_attn", check, q.device)
+        max_new = n if cu_seqlens is not None else n // max(kv_len.shape[0], 1)
+    _call(load().gdn_kv_attn, "gdn_kv_attn", q, check, kv, _rows3("q", q, Hq, n, d, dtype),
+          _rows3("out", out, Hq, n, d, dtype), None if lse is None else lse.data_ptr(), max_len,
+          max_new, d ** -0.5 if scale is None else scale, window,
+          GDN_ATTN_CAUSAL if causal else 0, _DT[dtype])
     return (out, lse) if return_lse else out
