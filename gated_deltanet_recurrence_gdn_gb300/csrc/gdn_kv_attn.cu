@@ -29,11 +29,7 @@
 // - A CTA's tiles are a contiguous share of all tiles (Plan, gdn_kv_attn.cuh);
 //   pieces of a cut (sequence, head) go to scratch as fp32 sums and k_kv_join
 //   adds them in a fixed order.
-#include <cmath>
-#include <type_traits>
-
 #include "gdn_kv_attn.cuh"
-#include "tc_ptx.cuh"
 
 #define KU 2
 #define KS 3
@@ -45,6 +41,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
+constexpr int kMany = 32;                     // rows of a key/value head: then tcgen05 products
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -79,27 +76,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
 // Bits of a where `mask` is set, of b elsewhere.
 __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // Place within its group of 16 of S^T's row g (rows g + 8: 8 more).  Rows 2 i and
 // 2 i + 1 are places i and 4 + (i ^ 1): the four lanes that share a V operand
 // register's tokens then read four neighbouring rows, and the two rows that a
@@ -139,35 +121,6 @@ struct Shape {
     static constexpr int kSmem = kRing + kQueries;
     static constexpr int kLead = kStages - 2;                  // tiles copied ahead
 };
-
-// The waits of a CTA: bounded, and over at once when one of them has given up
-// (the error is recorded, and the CTA runs to its end without computing).
-struct Waits {
-    volatile int *abort;
-    int *err;
-    uint32_t limit;
-    __device__ __forceinline__ bool on(uint64_t *bar, uint32_t parity) const {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        for (uint32_t i = 0; i < limit; ++i) {
-            if (*abort) return false;
-            if (ptx::mbar_try_wait(bar, parity)) return true;
-        }
-        *abort = 1;
-        atomicCAS(err, 0, kErrTimeout);
-        return false;
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d);
-template <>
-__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
-    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(a, b), pack2(c, d));
-}
 
 // S^T of a warp's group (its first row at `codes` and `scales`): K, rows
 // place_of(g) and 8 more, times Q^T.
@@ -315,7 +268,7 @@ template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinC
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
     using Sh = Shape<D, NT, kSplit, kU, kStages>;
     constexpr int kTile = Sh::kTile;
-    using P = Plan<kTile, Sh::kRows, kThreads>;
+    using W = Walk<kTile, Sh::kRows, kThreads>;
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
     constexpr int kParts = Sh::kParts, kRows = Sh::kRows;
     // Least probability (lifted) whose fp16 parts keep all their bits, how far the
@@ -323,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     constexpr float kLow = kSplit ? 0x1p-3f : 0x1p-14f, kBand = kSplit ? 0x1p18f : 0x1p29f;
     constexpr float kMid = kSplit ? 6.f : 0.5f, kHalf = kLift + kRaise - kMid;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ P plan;
+    __shared__ typename W::P plan;
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ int abort_flag;
     __shared__ float2 warp_ml[kWarps][kRows];
@@ -360,31 +313,19 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                                                : Sh::kVScale;
     constexpr int kRuns = kTile / 16 / 8;         // of a lane, at the smallest pages
     uint32_t tiles_before = 0;      // of the earlier pieces: a tile's stage and phase
-    int b;
-    long long seq_start;
-    Seq sq;
-    plan.find(a, beg, b, seq_start, sq);
-    for (long long cur = beg; cur < end;) {
-        int n_tiles = P::tiles(sq), n_rt = P::row_tiles(a, sq);
-        while (cur >= seq_start + (long long)n_rt * a.kv.H * n_tiles) {
-            seq_start += (long long)n_rt * a.kv.H * n_tiles;
-            sq.get(a, ++b);
-            n_tiles = P::tiles(sq);
-            n_rt = P::row_tiles(a, sq);
-        }
-        const long long within = cur - seq_start;
-        const int seg = (int)(within / n_tiles), tile0 = (int)(within - (long long)seg * n_tiles);
-        const int tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
-        const int h = seg / n_rt, row0 = (seg - h * n_rt) * kRows;
-        const int rows = min(kRows, sq.n * a.G - row0);
-        const int place0 = sq.lo + tile0 * kTile, n_copy = sq.span > 0 ? tile1 - tile0 : 0;
+    W w;
+    w.start(a, plan, beg, end);
+    do {
+        const Seq sq = w.sq;
+        const int h = w.h, row0 = w.row0(), rows = w.rows(a);
+        const int place0 = w.place0(), n_copy = w.count();
 
         // pages of the lane's runs (8 apart) of tile i, -1 if there is none to copy
         auto fetch = [&](int i, int (&page)[kRuns]) {
 #pragma unroll
             for (int k = 0; k < kRuns; ++k) {
                 const int in_tile = (lane_run + 8 * k) * run, at = place0 + i * kTile + in_tile;
-                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_of(b, at, a.err)
+                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_of(w.b, at, a.err)
                                                                        : -1;
             }
         };
@@ -443,26 +384,26 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             }
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t ex = max(27u, __float_as_uint(m) >> 23);
-            const float up = __uint_as_float((267u - ex) << 23);
+            float down;
+            const float up = row_up(m, down);
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
+            for (int k = 0; k < D / 32; ++k) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float u = x[8 * w + 2 * e] * up, v = x[8 * w + 2 * e + 1] * up;
+                    const float u = x[8 * k + 2 * e] * up, v = x[8 * k + 2 * e + 1] * up;
                     hi[e] = pack_f16(u, v);
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
                     lo[e] = pack_f16(u - f.x, v - f.y);
                 }
-                uint4 *q = queries + (warp * (D / 32) + w) * 32 + lane;
+                uint4 *q = queries + (warp * (D / 32) + k) * 32 + lane;
                 q[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 if constexpr (kSplit) q[NT * (D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             int from = 0, to = sq.len;
             if (there) sq.sees(a, j, from, to);
             if (t4 == 0) {
-                row_mul[mine] = __uint_as_float((ex - 13u) << 23) * a.scale_log2 * gk;
+                row_mul[mine] = down * a.scale_log2 * gk;
                 row_from[mine] = from;
                 row_to[mine] = to;
             }
@@ -694,10 +635,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         }
         __syncthreads();              // every warp is done with the ring as well
         float *merge = reinterpret_cast<float *>(smem);
-        const bool complete = tile0 == 0 && tile1 == n_tiles;
-        const long long slot = 2ll * blockIdx.x + (cur == beg ? 0 : 1);
-        if (threadIdx.x == 0 && tile0 == 0 && !complete) {
-            const long long end_tile = cur + n_tiles;
+        const bool complete = w.complete();
+        const long long slot = 2ll * blockIdx.x + (w.cur == beg ? 0 : 1);
+        if (threadIdx.x == 0 && w.tile0 == 0 && !complete) {
+            const long long end_tile = w.cur + w.n_tiles;
             const int last = (int)((end_tile * ctas - 1) / plan.total);   // CTA of its last tile
             a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, row0, rows};
         }
@@ -709,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 const int r = 2 * t4 + e;
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][8 * nt + r].x);
+                for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][8 * nt + r].x);
                 const float f = m == -INFINITY ? 1.f : ex2(sub[nt][e] - m);
                 float *p = merge + (warp * 8 + r) * D + g * (D / 8);
 #pragma unroll
@@ -722,14 +663,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 const int r8 = x / (D / 4), r = 8 * nt + r8, d = 4 * (x - r8 * (D / 4));
                 float m = -INFINITY, l = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r].x);
+                for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][r].x);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 ml = warp_ml[w][r];
+                for (int k = 0; k < kWarps; ++k) {
+                    const float2 ml = warp_ml[k][r];
                     l += ml.y * (m == -INFINITY ? 1.f : ex2(ml.x - m));
                     const float4 y =
-                        *reinterpret_cast<const float4 *>(merge + (w * 8 + r8) * D + d);
+                        *reinterpret_cast<const float4 *>(merge + (k * 8 + r8) * D + d);
                     v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
                 }
                 if (complete) {
@@ -737,9 +678,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     const float inv = l == 0.f ? 0.f : gv / l;
                     T *p = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + hq * a.o_head + d;
                     store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                    if (a.lse && d == 0)
-                        a.lse[(long long)(sq.first + j) * a.Hq + hq] =
-                            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    if (a.lse && d == 0) a.lse[(long long)(sq.first + j) * a.Hq + hq] = lse_of(m, l);
                 } else {
                     store4(a.part_o + (slot * kRows + r) * D + d, v.x, v.y, v.z, v.w);
                     if (d == 0) a.part_ml[slot * kRows + r] = make_float2(m, l);
@@ -748,74 +687,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             ptx::fence_proxy_async_smem();     // before copies go into the ring again
             __syncthreads();
         }
-        cur += tile1 - tile0;
-    }
-}
-
-// Adds the pieces of what was cut, in order: CTA (i, r) row r of the one whose
-// first piece CTA i of k_kv_attn had.
-constexpr int kJoinWarps = 4;
-template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
-    constexpr int kVec = D / 32;
-    __shared__ float sums[kJoinWarps][D];
-    __shared__ float2 warp_ml[kJoinWarps];
-    ptx::griddep_wait();
-    const Cut c = a.cuts[blockIdx.x];
-    const int r = blockIdx.y;
-    if (r >= c.rows || c.pieces == 0) return;
-    auto slot = [&](int k) {
-        return (k == 0 ? (long long)c.slot0 : 2ll * (blockIdx.x + k)) * kRows + r;
-    };
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY;
-    for (int k = threadIdx.x; k < c.pieces; k += kJoinWarps * 32) m = fmaxf(m, a.part_ml[slot(k)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) warp_ml[warp].x = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, warp_ml[w].x);
-    float v[kVec] = {}, l = 0.f;
-#pragma unroll 4
-    for (int k = warp; k < c.pieces; k += kJoinWarps) {
-        const float2 ml = a.part_ml[slot(k)];
-        const float f = m == -INFINITY ? 1.f : ex2(ml.x - m);
-        const float *p = a.part_o + slot(k) * D + lane * kVec;
-        l += ml.y * f;
-        if constexpr (kVec == 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(p);
-            v[0] += x.x * f; v[1] += x.y * f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; e += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(p + e);
-                v[e] += x.x * f; v[e + 1] += x.y * f; v[e + 2] += x.z * f; v[e + 3] += x.w * f;
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
-    if (lane == 0) warp_ml[warp].y = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l += warp_ml[w].y;
-    const int rr = c.row0 + r, j = rr / a.G, hq = c.h * a.G + rr - j * a.G;
-    const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + c.h) : 1.f;
-    const float inv = l == 0.f ? 0.f : gv / l;
-    T *p = static_cast<T *>(a.o) + (c.first + j) * a.o_tok + hq * a.o_head;
-    for (int d = 4 * threadIdx.x; d < D; d += 4 * kJoinWarps * 32) {
-        float x[4] = {};
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] += sums[w][d + e];
-        store4(p + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(long long)(c.first + j) * a.Hq + hq] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    } while (w.next(a));
 }
 
 template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinCtas>
@@ -843,35 +715,14 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     const int grid = (int)(most < resident ? (most < 1 ? 1 : most) : resident);
     const bool cut = a.max_len > kTile;     // else no piece of work has two tiles
     void *scratch = nullptr;
-    const size_t po = (size_t)2 * grid * Sh::kRows * D * 4, pm = (size_t)2 * grid * Sh::kRows * 8;
-    if (cut) {
-        if (scratch_alloc(&scratch, po + pm + grid * sizeof(Cut), st) != cudaSuccess)
-            return GDN_ERR_CUDA;
-        a.part_o = static_cast<float *>(scratch);
-        a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(scratch) + po);
-        a.cuts = reinterpret_cast<Cut *>(static_cast<uint8_t *>(scratch) + po + pm);
-    }
+    if (cut && alloc_pieces<D, Sh::kRows>(a, grid, &scratch, st) != cudaSuccess) return GDN_ERR_CUDA;
     const int slot = timer_begin(st, "k_kv_attn");
     kern<<<grid, kThreads, Sh::kSmem, st>>>(a);
     timer_end(slot, st);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (cut) {
-        if (e == cudaSuccess && grid > 1 && a.max_new > 0) {
-            // launched while k_kv_attn runs: it waits for that to end before it reads
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr.val.programmaticStreamSerializationAllowed = 1;
-            cudaLaunchConfig_t cfg{};
-            const long long rows = (long long)a.max_new * a.G;
-            cfg.gridDim = dim3(grid, (unsigned)(rows < Sh::kRows ? rows : Sh::kRows));
-            cfg.blockDim = dim3(kJoinWarps * 32);
-            cfg.stream = st;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, k_kv_join<T, D, Sh::kRows>, (const AttnArgs)a);
-            count_launch();
-        }
+        if (e == cudaSuccess) e = launch_join<T, D, Sh::kRows, kJoinWarps>(a, grid, st);
         const cudaError_t f = scratch_free(scratch, st);
         if (e == cudaSuccess) e = f;
     }
@@ -927,5 +778,7 @@ extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn
     const long long limit = gdn::option(GDN_OPT_WAIT_LIMIT);
     a.wait_limit = limit > 0 ? (uint32_t)(limit > 0x7fffffffLL ? 0x7fffffffLL : limit) : (1u << 22);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dt == GDN_BF16 ? pick<__nv_bfloat16, false>(a, st) : pick<float, true>(a, st);
+    if (dt == GDN_F32) return pick<float, true>(a, st);
+    if (a.kv.d <= 128 && (long long)a.max_new * a.G > kMany) return attn_many(a, st);
+    return pick<__nv_bfloat16, false>(a, st);
 }

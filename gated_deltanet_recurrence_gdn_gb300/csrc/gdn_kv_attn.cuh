@@ -2,7 +2,10 @@
 // call's arguments, what each row sees, and the division of the work.
 #pragma once
 
+#include <cmath>
+
 #include "gdn_kv.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace kv {
@@ -36,9 +39,6 @@ struct Cut {
 // key/value head) is query head h G + r % G of new token r / G.
 struct Seq {
     int first, n, len;
-    int lo;                    // first place that any row sees, rounded down to a page or
-                               // to 128, whichever is less
-    int span;                  // places [lo, lo + span) cover what any row sees
 
     __device__ __forceinline__ void get(const AttnArgs &a, int b) {
         a.kv.tokens(b, first, n, len, a.err);
@@ -47,9 +47,6 @@ struct Seq {
             if (len > a.max_len) len = 0;
             if (n > a.max_new) n = 0;
         }
-        lo = 0;
-        if (a.window > 0) lo = max(0, len - n + 1 - a.window) & -min(a.kv.page_size(), 128);
-        span = max(0, len - lo);
     }
     // Places [from, to) that new token j sees.
     __device__ __forceinline__ void sees(const AttnArgs &a, int j, int &from, int &to) const {
@@ -61,7 +58,7 @@ struct Seq {
 
 // The work of a call is a list of tiles of `kTile` places: of every sequence in
 // turn, of its key/value heads, of the head's row tiles (kRows rows each), of
-// what the sequence's rows see (one tile where they see nothing: its rows are
+// what the row tile's rows see (one tile where they see nothing: its rows are
 // written as zero).  CTA i of `grid` takes the tiles [total i / g, total (i + 1)
 // / g), g = min(grid, total): every CTA has the same number of tiles to within
 // one whatever the lengths, and a (sequence, head, row tile) is cut only where
@@ -71,14 +68,32 @@ struct Plan {
     long long prefix[kThreads];   // tiles before the sequences of each thread's share
     long long total;
 
-    __device__ static __forceinline__ int tiles(const Seq &s) {
-        return max(1, (s.span + kTile - 1) / kTile);
-    }
     __device__ static __forceinline__ int row_tiles(const AttnArgs &a, const Seq &s) {
         return (int)(((long long)s.n * a.G + kRows - 1) / kRows);
     }
-    __device__ static __forceinline__ long long weight(const AttnArgs &a, const Seq &s) {
-        return (long long)row_tiles(a, s) * a.kv.H * tiles(s);
+    // Places [lo, lo + span) cover what any row of row tile rt sees; lo is rounded
+    // down to a page or to 128, whichever is less.
+    __device__ static __forceinline__ void range(const AttnArgs &a, const Seq &s, int rt, int &lo,
+                                                 int &span) {
+        int none, to;
+        s.sees(a, (int)((long long)rt * kRows / a.G), lo, none);
+        s.sees(a, min(s.n - 1, (int)(((long long)rt * kRows + kRows - 1) / a.G)), none, to);
+        lo &= -min(a.kv.page_size(), 128);
+        span = max(0, to - lo);
+    }
+    __device__ static __forceinline__ int tiles(int span) {
+        return max(1, (span + kTile - 1) / kTile);
+    }
+    // Tiles of one key/value head of the sequence.
+    __device__ static long long head_tiles(const AttnArgs &a, const Seq &s) {
+        const int n = row_tiles(a, s);
+        long long sum = 0;
+        for (int rt = 0; rt < n; ++rt) {
+            int lo, span;
+            range(a, s, rt, lo, span);
+            sum += tiles(span);
+        }
+        return sum;
     }
     // Whole CTA; `this` in shared memory.
     __device__ void build(const AttnArgs &a) {
@@ -91,7 +106,7 @@ struct Plan {
             if (b < a.kv.N) {
                 Seq s;
                 s.get(a, b);
-                mine += weight(a, s);
+                mine += a.kv.H * head_tiles(a, s);
             }
         }
         long long x = mine;
@@ -112,25 +127,226 @@ struct Plan {
         if (threadIdx.x == 0) total = all;
         __syncthreads();
     }
-    // The sequence that tile `at` belongs to, and the tiles before that sequence.
-    __device__ void find(const AttnArgs &a, long long at, int &b, long long &start, Seq &s) const {
-        int lo = 0, hi = kThreads;
-        while (hi - lo > 1) {
-            const int m = (lo + hi) >> 1;
-            if (prefix[m] <= at) lo = m;
-            else hi = m;
+};
+
+// One CTA's walk over its pieces: the part of its tiles that belongs to one
+// (sequence, head, row tile).
+template <int kTile, int kRows, int kThreads>
+struct Walk {
+    using P = Plan<kTile, kRows, kThreads>;
+    Seq sq;
+    int b, h, rt, n_rt, lo, span, n_tiles;
+    int tile0, tile1;             // the piece: tiles [tile0, tile1) of n_tiles
+    long long cur, end;           // first tile of the piece, end of the CTA's tiles
+
+    __device__ __forceinline__ int row0() const { return rt * kRows; }
+    __device__ __forceinline__ int rows(const AttnArgs &a) const {
+        return min(kRows, sq.n * a.G - rt * kRows);
+    }
+    __device__ __forceinline__ bool complete() const { return tile0 == 0 && tile1 == n_tiles; }
+    __device__ __forceinline__ int place0() const { return lo + tile0 * kTile; }
+    // Tiles of the piece that hold anything.
+    __device__ __forceinline__ int count() const { return span > 0 ? tile1 - tile0 : 0; }
+
+    __device__ __forceinline__ void piece(const AttnArgs &a, int from) {
+        P::range(a, sq, rt, lo, span);
+        n_tiles = P::tiles(span);
+        tile0 = from;
+        tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
+    }
+    __device__ void start(const AttnArgs &a, const P &plan, long long at, long long until) {
+        cur = at;
+        end = until;
+        int i = 0, j = kThreads;
+        while (j - i > 1) {
+            const int m = (i + j) >> 1;
+            if (plan.prefix[m] <= at) i = m;
+            else j = m;
         }
-        const int share = (a.kv.N + kThreads - 1) / kThreads;
-        b = lo * share;
-        start = prefix[lo];
+        b = i * ((a.kv.N + kThreads - 1) / kThreads);
+        long long left = at - plan.prefix[i], per_head;
         for (;; ++b) {
-            s.get(a, b);
-            const long long w = weight(a, s);
-            if (at < start + w) return;
-            start += w;
+            sq.get(a, b);
+            per_head = P::head_tiles(a, sq);
+            if (left < per_head * a.kv.H) break;
+            left -= per_head * a.kv.H;
         }
+        h = (int)(left / per_head);
+        left -= h * per_head;
+        n_rt = P::row_tiles(a, sq);
+        for (rt = 0;; ++rt) {
+            P::range(a, sq, rt, lo, span);
+            const int n = P::tiles(span);
+            if (left < n) break;
+            left -= n;
+        }
+        piece(a, (int)left);
+    }
+    // The next piece; false at the end of the CTA's tiles.
+    __device__ __forceinline__ bool next(const AttnArgs &a) {
+        cur += tile1 - tile0;
+        if (cur >= end) return false;
+        if (++rt == n_rt) {
+            rt = 0;
+            if (++h == a.kv.H) {
+                h = 0;
+                do {
+                    sq.get(a, ++b);
+                    n_rt = P::row_tiles(a, sq);
+                } while (n_rt == 0);
+            }
+        }
+        piece(a, 0);
+        return true;
     }
 };
+
+// The waits of a CTA: bounded, and over at once when one of them has given up
+// (the error is recorded, and the CTA runs to its end without computing).
+struct Waits {
+    volatile int *abort;
+    int *err;
+    uint32_t limit;
+    __device__ __forceinline__ bool on(uint64_t *bar, uint32_t parity) const {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        for (uint32_t i = 0; i < limit; ++i) {
+            if (*abort) return false;
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        }
+        *abort = 1;
+        atomicCAS(err, 0, kErrTimeout);
+        return false;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// The power of two that brings a row whose largest magnitude is m to [2^13, 2^14)
+// (fp16's upper range; rows below 2^-100 stay smaller), and what undoes it.
+__device__ __forceinline__ float row_up(float m, float &down) {
+    const uint32_t ex = max(27u, __float_as_uint(m) >> 23);
+    down = __uint_as_float((ex - 13u) << 23);
+    return __uint_as_float((267u - ex) << 23);
+}
+
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(a, b), pack2(c, d));
+}
+// A row's logarithm of the sum of its exponentials, from what its scores lost.
+__device__ __forceinline__ float lse_of(float sub, float sum) {
+    return sum == 0.f ? -INFINITY : (sub + log2f(sum)) * 0.69314718055994531f;
+}
+
+// Adds the pieces of what was cut, in order.  CTA (i, y): kJoinWarps / kStripes
+// rows of the one whose first piece CTA i of the attention kernel had; kStripes
+// warps share a row's pieces (many pieces of few rows, or the other way round).
+constexpr int kJoinWarps = 4;
+template <typename T, int D, int kRows, int kStripes>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
+    constexpr int kVec = D / 32, kCtaRows = kJoinWarps / kStripes;
+    __shared__ float sums[kJoinWarps][D];
+    __shared__ float2 warp_ml[kJoinWarps];
+    ptx::griddep_wait();
+    const Cut c = a.cuts[blockIdx.x];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int local = warp / kStripes, stripe = warp - local * kStripes;
+    if (blockIdx.y * kCtaRows >= c.rows || c.pieces == 0) return;
+    const int r = min((int)blockIdx.y * kCtaRows + local, c.rows - 1);   // (the last row again)
+    auto slot = [&](int k) {
+        return (k == 0 ? (long long)c.slot0 : 2ll * (blockIdx.x + k)) * kRows + r;
+    };
+    float m = -INFINITY;
+    for (int k = lane; k < c.pieces; k += 32) m = fmaxf(m, a.part_ml[slot(k)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float v[kVec] = {}, l = 0.f;
+#pragma unroll 4
+    for (int k = stripe; k < c.pieces; k += kStripes) {
+        const float2 ml = a.part_ml[slot(k)];
+        const float f = m == -INFINITY ? 1.f : ex2(ml.x - m);
+        const float *p = a.part_o + slot(k) * D + lane * kVec;
+        l += ml.y * f;
+        if constexpr (kVec == 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(p);
+            v[0] += x.x * f; v[1] += x.y * f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(p + e);
+                v[e] += x.x * f; v[e + 1] += x.y * f; v[e + 2] += x.z * f; v[e + 3] += x.w * f;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
+    if (lane == 0) warp_ml[warp].y = l;
+    __syncthreads();
+    if (stripe != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kStripes; ++w) l += warp_ml[warp + w].y;
+    const int rr = c.row0 + r, j = rr / a.G, hq = c.h * a.G + rr - j * a.G;
+    const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + c.h) : 1.f;
+    const float inv = l == 0.f ? 0.f : gv / l;
+    T *p = static_cast<T *>(a.o) + (c.first + j) * a.o_tok + hq * a.o_head;
+    for (int d = 4 * lane; d < D; d += 128) {
+        float x[4] = {};
+#pragma unroll
+        for (int w = 0; w < kStripes; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += sums[warp + w][d + e];
+        store4(p + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[(long long)(c.first + j) * a.Hq + hq] = lse_of(m, l);
+}
+
+// Scratch for the pieces of a launch of `grid` CTAs with kRows rows, into `a`.
+template <int D, int kRows>
+inline cudaError_t alloc_pieces(AttnArgs &a, int grid, void **scratch, cudaStream_t st) {
+    const size_t po = (size_t)2 * grid * kRows * D * 4, pm = (size_t)2 * grid * kRows * 8;
+    const cudaError_t e = scratch_alloc(scratch, po + pm + grid * sizeof(Cut), st);
+    if (e != cudaSuccess) return e;
+    a.part_o = static_cast<float *>(*scratch);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(*scratch) + po);
+    a.cuts = reinterpret_cast<Cut *>(static_cast<uint8_t *>(*scratch) + po + pm);
+    return cudaSuccess;
+}
+// The join after such a launch: started while that runs, it waits for its end.
+template <typename T, int D, int kRows, int kStripes>
+inline cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t st) {
+    const long long most = (long long)a.max_new * a.G;
+    const int rows = (int)(most < kRows ? most : kRows), per = kJoinWarps / kStripes;
+    if (grid < 2 || rows < 1) return cudaSuccess;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, (rows + per - 1) / per);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, k_kv_join<T, D, kRows, kStripes>, a);
+}
+
+// Many rows (gdn_kv_attn_tc.cu): bf16 rows, d = 64 or 128.
+gdn_status attn_many(AttnArgs &a, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace gdn

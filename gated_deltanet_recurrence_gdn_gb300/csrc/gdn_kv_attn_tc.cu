@@ -1,0 +1,568 @@
+// gdn_kv_attn_tc.cu -- attention over the 4-bit paged cache for many rows (a
+// chunk of a prompt): tcgen05 products, bf16 rows, d = 64 or 128.
+//
+// A CTA takes 256 rows of a (sequence, key/value head), row r being query head
+// r % G of token r / G, as two tiles of 128, over 128 tokens at a time:
+//     S = Q K^T (TMEM),  P = 2^(S - sub) (fp16, into S's columns),  O += P V (TMEM).
+// Four roles, 16 warps:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, a thread a row: no exchange
+//                    between threads, the row's sum and `sub` in registers;
+//   warps 8-11       turn the next 128 tokens' 4-bit numbers into fp16 operand
+//                    tiles (128-byte swizzle), a thread a token, its codes
+//                    loaded straight into registers one tile ahead;
+//   warp 12          issues the products: QK of the next tokens right after PV of
+//                    these, one row tile after the other, so that the softmax of
+//                    one runs while the tensor cores work for the other.
+// The products bound it (2 x 2 x 128^3 multiply-adds a tile at d = 128), and next
+// to them the exponentials; turning a tile into fp16 costs 1/4 of that time in
+// issue slots because 256 rows share it.
+//
+// e2m1 * e4m3 is exact in fp16, queries are scaled by a power of two per row, and
+// probabilities are fp16 numbers.  `sub` is set so that the first scores' maximum
+// is 2^kLift; it moves only when a tile's sum passes 2^15, which any number near
+// fp16's end brings about, so no maximum is taken otherwise.  A weight keeps its
+// 11 bits down to 2^-22 of the row's largest.
+#include "gdn_kv_attn.cuh"
+
+namespace gdn {
+namespace kv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 128;                  // tokens
+constexpr int kRowTile = 128;
+constexpr int kRows = 2 * kRowTile;
+constexpr int kThreads = 512;
+constexpr int kConvert = 256;               // first thread of the converting warps
+constexpr int kIssuer = 384;                // the issuing thread
+// Registers a thread of each role; together no more than the launch's 512 x 128.
+constexpr int kSoftmaxRegs = 168, kConvertRegs = 96, kIssuerRegs = 64;
+static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssuerRegs <= 512 * 128, "registers");
+constexpr float kLift = 8.f;                // log2 of the first maximum's probability
+constexpr float kMostSum = 32768.f;         // of a tile: above it `sub` moves
+
+// mbarriers
+enum : int {
+    B_K_FULL = 0,             // [2] converted keys; 4 warps
+    B_K_FREE = 2,             // [2] their products are done
+    B_V_FULL = 4,             // [2]
+    B_V_FREE = 6,             // [2]
+    B_Q_FULL = 8,             // [2] a row tile's queries; 4 warps
+    B_S_FULL = 10,            // [2] scores of a row tile
+    B_P_FULL = 12,            // [2] probabilities; 4 warps
+    B_O_FULL = 14,            // [2] a row tile's PV is done
+    B_DRAIN = 16,
+    B_COUNT = 17
+};
+
+template <int D>
+struct Lay {
+    static constexpr int kOperand = 128 * D * 2;                 // Q row tile, K tile, V tile
+    static constexpr int OFF_Q = 0;                              // [2]
+    static constexpr int OFF_K = 2 * kOperand;                   // [2]
+    static constexpr int OFF_V = 4 * kOperand;                   // [2]
+    static constexpr int SIZE = 6 * kOperand + 1024;             // (aligned up to 1024)
+    static constexpr uint32_t TM_S = 0, TM_O = 256;              // TMEM columns, 128 a row tile
+};
+
+__device__ __forceinline__ uint32_t idesc_f16(int N, bool b_mn) {
+    // kind::f16 with fp16 A and B, fp32 accumulation, M = 128
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " GDN_OPS32 ";" ::"r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                 "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+                 "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+                 "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+// 16-byte chunk c (8 numbers) of row `row` of an operand tile: 64-column blocks
+// of 128 rows of 128 bytes, 128-byte swizzled.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int c) {
+    return tile + (c >> 3) * 16384 + sw128_offset(row, c & 7);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One token's codes and scales of K or V of a head, in registers.
+template <int D>
+struct Token {
+    uint4 w[D / 32];
+    uint32_t s[D / 64];       // D / 16 scale bytes
+    __device__ __forceinline__ void load(const uint8_t *code, const uint8_t *scale) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(code) + i);
+        if constexpr (D == 128) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(scale));
+            s[0] = x.x; s[1] = x.y;
+        } else {
+            s[0] = __ldg(reinterpret_cast<const uint32_t *>(scale));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) s[i] = 0;
+    }
+    // Zeroes the scales that are NaN; the mask of their blocks.
+    __device__ __forceinline__ uint32_t take_nan() {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            if (((s[i / 4] >> (8 * (i & 3))) & 0x7f) == 0x7f) {
+                bad |= 1u << i;
+                s[i / 4] &= ~(0xffu << (8 * (i & 3)));
+            }
+        return bad;
+    }
+    // Its D numbers as fp16 into row `row` of an operand tile.
+    __device__ __forceinline__ void convert(uint32_t tile, int row) const {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {     // 32 numbers: two blocks
+            const uint32_t two = e4m3x2_f16(s[i / 2] >> (16 * (i & 1)));
+            const __half2 h = *reinterpret_cast<const __half2 *>(&two);
+            const __half2 lo = __low2half2(h), hi = __high2half2(h);
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t r[4];
+                e2m1x8_f16(x[k], r);
+                const __half2 f = k < 2 ? lo : hi;
+                st_shared16(chunk_at(tile, row, 4 * i + k), mul2(r[0], f), mul2(r[1], f),
+                            mul2(r[2], f), mul2(r[3], f));
+            }
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
+    using L = Lay<D>;
+    using W = Walk<kTile, kRows, kThreads>;
+    using T = __nv_bfloat16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ typename W::P plan;
+    __shared__ uint64_t bar[B_COUNT];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    // NaN blocks of V of the last four tiles' tokens (a tile's are read before the
+    // fourth next is converted), and whether a warp found any
+    __shared__ uint8_t nan_of[4][kTile];
+    __shared__ uint32_t nan_any[4][4];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == kIssuer / 32) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < B_COUNT; ++i) {
+            const bool warps = i < B_K_FREE || i == B_V_FULL || i == B_V_FULL + 1 ||
+                               i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL ||
+                               i == B_P_FULL + 1;
+            mbar_init(bar + i, warps ? 4 : 1);
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    plan.build(a);                  // (its barriers cover the initialisation)
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const long long ctas = min((long long)gridDim.x, plan.total);
+    if (a.cuts && tid == 0) a.cuts[blockIdx.x].pieces = 0;
+    const Waits waits{&abort_flag, a.err, a.wait_limit};
+    const long long beg = plan.total * blockIdx.x / max(ctas, 1ll);
+    const long long end = plan.total * (blockIdx.x + 1) / max(ctas, 1ll);
+
+    if (blockIdx.x < ctas) {
+        W w;
+        if (tid < kConvert) {
+            // ------------------------------------------------------------ softmax
+            regs_more<kSoftmaxRegs>();
+            const int m = tid >> 7, row = tid & 127;
+            const uint32_t lanes = (uint32_t)(row & 96) << 16;       // the warp's TMEM lanes
+            const uint32_t tS = tmem + L::TM_S + 128 * m + lanes, tO = tmem + L::TM_O + 128 * m + lanes;
+            const uint32_t tile_q = base + L::OFF_Q + m * L::kOperand;
+            uint32_t done = 0;           // this row tile's token tiles so far
+            uint32_t all = 0;            // the CTA's token tiles so far
+            w.start(a, plan, beg, end);
+            do {
+                const Seq sq = w.sq;
+                const int h = w.h, rows = w.rows(a), count = w.count(), place0 = w.place0();
+                const int mine = m * kRowTile + row, r = w.row0() + mine;
+                const bool there = mine < rows;
+                const int j = there ? r / a.G : 0, hq = h * a.G + (there ? r - j * a.G : 0);
+                const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
+                int from = 0, to = sq.len;
+                if (there) sq.sees(a, j, from, to);
+                float sub = 0.f, sum = 0.f;
+                bool started = false;       // whether `sub` is set
+                uint32_t nan = 0;           // blocks of d in which the row sees a NaN
+                const bool active = m * kRowTile < rows;
+                if (active && count > 0) {
+                    float mul;
+                    {   // the row's queries, into the operand tile
+                        const T *p = static_cast<const T *>(a.q) + (sq.first + j) * a.q_tok +
+                                     (long long)hq * a.q_head;
+                        uint4 x[D / 8];
+                        float most = 0.f;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            x[i] = there ? __ldg(reinterpret_cast<const uint4 *>(p) + i)
+                                         : make_uint4(0, 0, 0, 0);
+                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                most = fmaxf(most, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
+                                                         fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+                        }
+                        float down;
+                        const float up = row_up(most, down);
+                        mul = down * a.scale_log2 *
+                              (a.kv.head_scale ? __ldg(a.kv.head_scale + h) : 1.f);
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
+                                                __uint_as_float(u[e] & 0xffff0000u) * up);
+                            st_shared16(chunk_at(tile_q, row, i), y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + B_Q_FULL + m);
+
+                    for (int i = 0; i < count; ++i, ++done) {
+                        const int t0 = place0 + i * kTile;
+                        const bool ok = waits.on(bar + B_S_FULL + m, done & 1);
+                        tc_fence_after();
+                        // (every lane of a warp takes part in what follows, whatever it sees)
+                        const bool whole = __all_sync(0xffffffffu, t0 >= from && t0 + kTile <= to);
+                        uint32_t pk[64];
+                        float part = 0.f;
+                        auto probabilities = [&]() {
+                            float p4[4] = {};
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t x[32];
+                                tmem_ld32(tS + 32 * c, x);
+                                tmem_wait32(x);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    float t[2];
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        t[k] = fmaf(__uint_as_float(x[e + k]), mul, -sub);
+                                        if (!whole) {
+                                            const int at = t0 + 32 * c + e + k;
+                                            if (at < from || at >= to) t[k] = -INFINITY;
+                                        }
+                                        t[k] = ex2(t[k]);
+                                        p4[(e + k) & 3] += t[k];
+                                    }
+                                    pk[16 * c + e / 2] = pack_f16(t[0], t[1]);
+                                }
+                            }
+                            part = (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                        };
+                        if (ok) {
+                            if (__all_sync(0xffffffffu, started)) probabilities();
+                            else part = INFINITY;
+                            const bool move = !started || part > kMostSum;
+                            if (__any_sync(0xffffffffu, move)) {
+                                // the row's maximum of these scores, and `sub` by it
+                                float top = -INFINITY;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t x[32];
+                                    tmem_ld32(tS + 32 * c, x);
+                                    tmem_wait32(x);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) {
+                                        const int at = t0 + 32 * c + e;
+                                        const float y = __uint_as_float(x[e]) * mul;
+                                        if (at >= from && at < to) top = fmaxf(top, y);
+                                    }
+                                }
+                                float f = 1.f;
+                                if (move && top > -INFINITY) {
+                                    const float to_new = top - kLift;
+                                    if (!started) {
+                                        sub = to_new;
+                                        started = true;
+                                    } else if (to_new > sub) {
+                                        f = ex2(sub - to_new);
+                                        sub = to_new;
+                                    }
+                                }
+                                sum *= f;
+                                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                                    waits.on(bar + B_O_FULL + m, (done - 1) & 1);
+                                    tc_fence_after();
+#pragma unroll
+                                    for (int c = 0; c < D / 32; ++c) {
+                                        uint32_t x[32];
+                                        tmem_ld32(tO + 32 * c, x);
+                                        tmem_wait32(x);
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e)
+                                            x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                                        tmem_st32(tO + 32 * c, x);
+                                    }
+                                    tmem_st_wait();
+                                }
+                                probabilities();
+                            }
+                            sum += part;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t x[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = pk[32 * c + e];
+                                tmem_st32(tS + 32 * c, x);
+                            }
+                            tmem_st_wait();
+                            const uint32_t *any = nan_any[(all + i) & 3];
+                            if (any[0] | any[1] | any[2] | any[3]) {
+                                const uint8_t *of = nan_of[(all + i) & 3];
+                                for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e)
+                                    nan |= of[e];
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar + B_P_FULL + m);
+                    }
+                    waits.on(bar + B_O_FULL + m, (done - 1) & 1);
+                    tc_fence_after();
+                }
+                all += count;
+
+                // the piece's result
+                const bool complete = w.complete();
+                const long long slot = 2ll * blockIdx.x + (w.cur == beg ? 0 : 1);
+                if (tid == 0 && w.tile0 == 0 && !complete) {
+                    const int last = (int)(((w.cur + w.n_tiles) * ctas - 1) / plan.total);
+                    a.cuts[blockIdx.x] =
+                        Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, w.row0(), rows};
+                }
+                if (active) {
+                    const float scale = complete ? (sum == 0.f ? 0.f : gv / sum) : 1.f;
+                    const float lost = started ? sub : -INFINITY;
+                    T *po = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + (long long)hq * a.o_head;
+                    float *pp = a.part_o + (slot * kRows + mine) * D;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[32];
+                        if (count > 0) {
+                            tmem_ld32(tO + 32 * c, x);
+                            tmem_wait32(x);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                v[k] = count > 0 ? __uint_as_float(x[e + k]) * scale : 0.f;
+                                if ((nan >> (2 * c + e / 16)) & 1) v[k] = NAN;
+                            }
+                            if (!there) continue;
+                            if (complete) store8(po + 32 * c + e, v);
+                            else store8(pp + 32 * c + e, v);
+                        }
+                    }
+                    if (there) {
+                        if (!complete) a.part_ml[slot * kRows + mine] = make_float2(lost, sum);
+                        else if (a.lse)
+                            a.lse[(long long)(sq.first + j) * a.Hq + hq] = lse_of(lost, sum);
+                    }
+                }
+            } while (w.next(a));
+        } else if (tid < kIssuer) {
+            // --------------------------------------------------------- conversion
+            regs_less<kConvertRegs>();
+            const int tok = tid - kConvert;
+            uint32_t n = 0;               // the CTA's token tiles so far
+            w.start(a, plan, beg, end);
+            do {
+                const int count = w.count(), place0 = w.place0(), len = w.sq.len, h = w.h;
+                const int psz = a.kv.page_size();
+                auto page_at = [&](int i) {
+                    const int at = place0 + i * kTile + tok;
+                    return i < count && at < len ? a.kv.page_of(w.b, at, a.err) : -1;
+                };
+                Token<D> k, v;
+                auto load = [&](Token<D> &x, int i, int page, bool key) {
+                    if (page < 0) {
+                        x.clear();
+                        return;
+                    }
+                    const int row = (place0 + i * kTile + tok) & (psz - 1);
+                    const uint8_t *blk = a.kv.pages + a.kv.block(page, h);
+                    x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
+                           blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
+                };
+                int page = page_at(0), next_page = page_at(1);
+                load(k, 0, page, true);
+                load(v, 0, page, false);
+                for (int i = 0; i < count; ++i, ++n) {
+                    const int buf = n & 1;
+                    const uint32_t reuse = ((n >> 1) + 1) & 1;
+                    const uint32_t bad = v.take_nan();
+                    const bool k_ok = n < 2 || waits.on(bar + B_K_FREE + buf, reuse);
+                    nan_of[n & 3][tok] = (uint8_t)bad;
+                    const uint32_t found = __ballot_sync(0xffffffffu, bad != 0);
+                    if (lane == 0) nan_any[n & 3][warp & 3] = found;
+                    if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, tok);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + B_K_FULL + buf);
+                    page = next_page;
+                    next_page = page_at(i + 2);
+                    load(k, i + 1, page, true);
+                    const bool v_ok = n < 2 || waits.on(bar + B_V_FREE + buf, reuse);
+                    if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, tok);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + B_V_FULL + buf);
+                    load(v, i + 1, page, false);
+                }
+            } while (w.next(a));
+        } else {
+          regs_less<kIssuerRegs>();
+          if (tid == kIssuer) {
+            // ------------------------------------------------------------- products
+            const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B);
+            const uint64_t dK = make_sdesc(base + L::OFF_K, 16, 1024, kSwizzle128B);
+            const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
+            const uint32_t id_qk = idesc_f16(kTile, false), id_pv = idesc_f16(D, true);
+            uint32_t n = 0, done[2] = {}, pieces[2] = {};
+            bool alive = true;
+            auto qk = [&](int m, int buf) {
+                if (alive) {
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
+                        mma_bf16(tmem + L::TM_S + 128 * m, dQ + ((m * L::kOperand + off) >> 4),
+                                 dK + ((buf * L::kOperand + off) >> 4), id_qk, s > 0);
+                    }
+                }
+                mma_commit(bar + B_S_FULL + m);
+            };
+            w.start(a, plan, beg, end);
+            do {
+                const int count = w.count(), mt = w.rows(a) > kRowTile ? 2 : 1;
+                if (count == 0) continue;
+                for (int m = 0; m < mt; ++m)
+                    alive &= waits.on(bar + B_Q_FULL + m, pieces[m]++ & 1);
+                alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
+                tc_fence_after();
+                for (int m = 0; m < mt; ++m) qk(m, n & 1);
+                mma_commit(bar + B_K_FREE + (n & 1));
+                for (int i = 0; i < count; ++i, ++n) {
+                    const int buf = n & 1;
+                    const bool more = i + 1 < count;
+                    if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
+                    alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
+                    for (int m = 0; m < mt; ++m) {
+                        alive &= waits.on(bar + B_P_FULL + m, done[m]++ & 1);
+                        tc_fence_after();
+                        if (alive) {
+#pragma unroll
+                            for (int s = 0; s < kTile / 16; ++s)
+                                mma_ts(tmem + L::TM_O + 128 * m, tmem + L::TM_S + 128 * m + 8 * s,
+                                       dV + ((buf * L::kOperand + s * 2048) >> 4), id_pv,
+                                       i > 0 || s > 0);
+                        }
+                        mma_commit(bar + B_O_FULL + m);
+                        if (more) qk(m, buf ^ 1);
+                    }
+                    mma_commit(bar + B_V_FREE + buf);
+                    if (more) mma_commit(bar + B_K_FREE + (buf ^ 1));
+                }
+            } while (w.next(a));
+            // before tensor memory is given back, whatever happened
+            mma_commit(bar + B_DRAIN);
+            mbar_wait(bar + B_DRAIN, 0, a.wait_limit);
+          }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssuer / 32) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+gdn_status launch(AttnArgs &a, cudaStream_t st) {
+    auto kern = k_kv_attn_tc<D>;
+    static std::atomic<int> memo[kMaxDeviceMemo];
+    const int sms = per_device(memo, [&](int dev) {
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SIZE) !=
+                cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return -1;
+        return n;
+    }, 0);
+    if (sms < 1) return GDN_ERR_CUDA;
+    const long long rt = ((long long)a.max_new * a.G + kRows - 1) / kRows;
+    long long most = rt * a.kv.H * (a.max_len / kTile + 2);     // of one sequence
+    most = most > sms ? sms : most * a.kv.N;
+    const int grid = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
+    void *scratch = nullptr;
+    if (alloc_pieces<D, kRows>(a, grid, &scratch, st) != cudaSuccess) return GDN_ERR_CUDA;
+    const int slot = timer_begin(st, "k_kv_attn_tc");
+    kern<<<grid, kThreads, Lay<D>::SIZE, st>>>(a);
+    timer_end(slot, st);
+    count_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D, kRows, 1>(a, grid, st);
+    const cudaError_t f = scratch_free(scratch, st);
+    if (e == cudaSuccess) e = f;
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+gdn_status attn_many(AttnArgs &a, cudaStream_t st) {
+    return a.kv.d == 64 ? launch<64>(a, st) : launch<128>(a, st);
+}
+
+}  // namespace kv
+}  // namespace gdn
