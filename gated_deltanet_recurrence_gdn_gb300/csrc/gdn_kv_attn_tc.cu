@@ -22,6 +22,8 @@
 // is 2^kLift; it moves only when a tile's sum passes 2^15, which any number near
 // fp16's end brings about, so no maximum is taken otherwise.  A weight keeps its
 // 11 bits down to 2^-22 of the row's largest.
+#include <type_traits>
+
 #include "gdn_kv_attn.cuh"
 
 namespace gdn {
@@ -236,13 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     {   // the row's queries, into the operand tile
                         const T *p = static_cast<const T *>(a.q) + (sq.first + j) * a.q_tok +
                                      (long long)hq * a.q_head;
-                        uint4 x[D / 8];
-                        float most = 0.f;
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            x[i] = there ? __ldg(reinterpret_cast<const uint4 *>(p) + i)
+                        auto piece = [&](int i) {
+                            return there ? __ldg(reinterpret_cast<const uint4 *>(p) + i)
                                          : make_uint4(0, 0, 0, 0);
-                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        };
+                        float most = 0.f;
+#pragma unroll 4
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 x = piece(i);
+                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 most = fmaxf(most, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
@@ -252,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         const float up = row_up(most, down);
                         mul = down * a.scale_log2 *
                               (a.kv.head_scale ? __ldg(a.kv.head_scale + h) : 1.f);
-#pragma unroll
+#pragma unroll 4
                         for (int i = 0; i < D / 8; ++i) {
-                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            const uint4 x = piece(i);
+                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                             uint32_t y[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         const bool whole = __all_sync(0xffffffffu, t0 >= from && t0 + kTile <= to);
                         uint32_t pk[64];
                         float part = 0.f;
-                        auto probabilities = [&]() {
+                        auto numbers = [&](auto masked) {
                             float p4[4] = {};
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
 #pragma unroll
                                     for (int k = 0; k < 2; ++k) {
                                         t[k] = fmaf(__uint_as_float(x[e + k]), mul, -sub);
-                                        if (!whole) {
+                                        if constexpr (masked.value) {
                                             const int at = t0 + 32 * c + e + k;
                                             if (at < from || at >= to) t[k] = -INFINITY;
                                         }
@@ -299,6 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                                 }
                             }
                             part = (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                        };
+                        auto probabilities = [&]() {
+                            if (whole) numbers(std::false_type{});
+                            else numbers(std::true_type{});
                         };
                         if (ok) {
                             if (__all_sync(0xffffffffu, started)) probabilities();
