@@ -167,6 +167,103 @@ struct Token {
     }
 };
 
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// Products of row tile m with the token tile in `buf`.  Every lane of the issuing
+// warp comes here, so that the descriptors stay in uniform registers; one issues.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tmem, uint64_t dQ, uint64_t dK, int m, int buf,
+                                         bool alive, uint64_t *bar) {
+    using L = Lay<D>;
+    const uint32_t id = idesc_f16(kTile, false), d = tmem + L::TM_S + 128 * m;
+    const uint64_t q = dQ + ((m * L::kOperand) >> 4), k = dK + ((buf * L::kOperand) >> 4);
+    if (elect_one()) {
+        if (alive) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
+                mma_bf16(d, q + off, k + off, id, s > 0);
+            }
+        }
+        mma_commit(bar + B_S_FULL + m);
+    }
+    __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t dV, int m, int buf, bool add,
+                                         bool alive, uint64_t *bar) {
+    using L = Lay<D>;
+    const uint32_t id = idesc_f16(D, true), d = tmem + L::TM_O + 128 * m;
+    const uint32_t p = tmem + L::TM_S + 128 * m;
+    const uint64_t v = dV + ((buf * L::kOperand) >> 4);
+    if (elect_one()) {
+        if (alive) {
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+                mma_ts(d, p + 8 * s, v + ((s * 2048) >> 4), id, add || s > 0);
+        }
+        mma_commit(bar + B_O_FULL + m);
+    }
+    __syncwarp();
+}
+
+template <int D, typename W>
+__device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &plan, W &w,
+                                      long long beg, long long end, uint32_t base, uint32_t tmem,
+                                      uint64_t *bar, const Waits &waits) {
+    using L = Lay<D>;
+    const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B);
+    const uint64_t dK = make_sdesc(base + L::OFF_K, 16, 1024, kSwizzle128B);
+    const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
+    uint32_t n = 0, done[2] = {}, pieces[2] = {};
+    bool alive = true;
+    auto commit = [&](int b) {
+        if (elect_one()) mma_commit(bar + b);
+        __syncwarp();
+    };
+    w.start(a, plan, beg, end);
+    do {
+        const int count = w.count();
+        const bool two = w.rows(a) > kRowTile;
+        if (count == 0) continue;
+        alive &= waits.on(bar + B_Q_FULL, pieces[0]++ & 1);
+        if (two) alive &= waits.on(bar + B_Q_FULL + 1, pieces[1]++ & 1);
+        alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
+        alive = __all_sync(0xffffffffu, alive);
+        tc_fence_after();
+        issue_qk<D>(tmem, dQ, dK, 0, n & 1, alive, bar);
+        if (two) issue_qk<D>(tmem, dQ, dK, 1, n & 1, alive, bar);
+        commit(B_K_FREE + (n & 1));
+        for (int i = 0; i < count; ++i, ++n) {
+            const int buf = n & 1;
+            const bool more = i + 1 < count;
+            if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
+            alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (m == 1 && !two) break;
+                alive &= waits.on(bar + B_P_FULL + m, done[m]++ & 1);
+                alive = __all_sync(0xffffffffu, alive);
+                tc_fence_after();
+                issue_pv<D>(tmem, dV, m, buf, i > 0, alive, bar);
+                if (more) issue_qk<D>(tmem, dQ, dK, m, buf ^ 1, alive, bar);
+            }
+            commit(B_V_FREE + buf);
+            if (more) commit(B_K_FREE + (buf ^ 1));
+        }
+    } while (w.next(a));
+    // before tensor memory is given back, whatever happened
+    commit(B_DRAIN);
+    mbar_wait(bar + B_DRAIN, 0, a.wait_limit);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     using L = Lay<D>;
@@ -473,62 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 }
             } while (w.next(a));
         } else {
-          regs_less<kIssuerRegs>();
-          if (tid == kIssuer) {
-            // ------------------------------------------------------------- products
-            const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B);
-            const uint64_t dK = make_sdesc(base + L::OFF_K, 16, 1024, kSwizzle128B);
-            const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
-            const uint32_t id_qk = idesc_f16(kTile, false), id_pv = idesc_f16(D, true);
-            uint32_t n = 0, done[2] = {}, pieces[2] = {};
-            bool alive = true;
-            auto qk = [&](int m, int buf) {
-                if (alive) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-                        mma_bf16(tmem + L::TM_S + 128 * m, dQ + ((m * L::kOperand + off) >> 4),
-                                 dK + ((buf * L::kOperand + off) >> 4), id_qk, s > 0);
-                    }
-                }
-                mma_commit(bar + B_S_FULL + m);
-            };
-            w.start(a, plan, beg, end);
-            do {
-                const int count = w.count(), mt = w.rows(a) > kRowTile ? 2 : 1;
-                if (count == 0) continue;
-                for (int m = 0; m < mt; ++m)
-                    alive &= waits.on(bar + B_Q_FULL + m, pieces[m]++ & 1);
-                alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
-                tc_fence_after();
-                for (int m = 0; m < mt; ++m) qk(m, n & 1);
-                mma_commit(bar + B_K_FREE + (n & 1));
-                for (int i = 0; i < count; ++i, ++n) {
-                    const int buf = n & 1;
-                    const bool more = i + 1 < count;
-                    if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
-                    alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
-                    for (int m = 0; m < mt; ++m) {
-                        alive &= waits.on(bar + B_P_FULL + m, done[m]++ & 1);
-                        tc_fence_after();
-                        if (alive) {
-#pragma unroll
-                            for (int s = 0; s < kTile / 16; ++s)
-                                mma_ts(tmem + L::TM_O + 128 * m, tmem + L::TM_S + 128 * m + 8 * s,
-                                       dV + ((buf * L::kOperand + s * 2048) >> 4), id_pv,
-                                       i > 0 || s > 0);
-                        }
-                        mma_commit(bar + B_O_FULL + m);
-                        if (more) qk(m, buf ^ 1);
-                    }
-                    mma_commit(bar + B_V_FREE + buf);
-                    if (more) mma_commit(bar + B_K_FREE + (buf ^ 1));
-                }
-            } while (w.next(a));
-            // before tensor memory is given back, whatever happened
-            mma_commit(bar + B_DRAIN);
-            mbar_wait(bar + B_DRAIN, 0, a.wait_limit);
-          }
+            regs_less<kIssuerRegs>();
+            if (warp == kIssuer / 32) issue<D>(a, plan, w, beg, end, base, tmem, bar, waits);
         }
     }
     tc_fence_before();
