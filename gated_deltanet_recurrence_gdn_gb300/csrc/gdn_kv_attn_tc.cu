@@ -33,6 +33,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;                  // tokens
+constexpr int kHalf = kTile / 2;
 constexpr int kRowTile = 128;
 constexpr int kRows = 2 * kRowTile;
 constexpr int kThreads = 512;
@@ -52,10 +53,10 @@ enum : int {
     B_V_FREE = 6,             // [2]
     B_Q_FULL = 8,             // [2] a row tile's queries; 4 warps
     B_S_FULL = 10,            // [2] scores of a row tile
-    B_P_FULL = 12,            // [2] probabilities; 4 warps
-    B_O_FULL = 14,            // [2] a row tile's PV is done
-    B_DRAIN = 16,
-    B_COUNT = 17
+    B_P_FULL = 12,            // [2][2] probabilities of each half of a tile; 4 warps
+    B_O_FULL = 16,            // [2][2] their PV is done
+    B_DRAIN = 20,
+    B_COUNT = 21
 };
 
 template <int D>
@@ -113,6 +114,31 @@ __device__ __forceinline__ void regs_more() {
 template <int N>
 __device__ __forceinline__ void regs_less() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Pairs of fp32 numbers in one register pair.
+__device__ __forceinline__ uint64_t pack64(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack64(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack64(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // One token's codes and scales of K or V of a head, in registers.
@@ -197,19 +223,19 @@ __device__ __forceinline__ void issue_qk(uint32_t tmem, uint64_t dQ, uint64_t dK
     __syncwarp();
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t dV, int m, int buf, bool add,
-                                         bool alive, uint64_t *bar) {
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t dV, int m, int buf, int half,
+                                         bool add, bool alive, uint64_t *bar) {
     using L = Lay<D>;
     const uint32_t id = idesc_f16(D, true), d = tmem + L::TM_O + 128 * m;
-    const uint32_t p = tmem + L::TM_S + 128 * m;
-    const uint64_t v = dV + ((buf * L::kOperand) >> 4);
+    const uint32_t p = tmem + L::TM_S + 128 * m + half * (kHalf / 2);
+    const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
     if (elect_one()) {
         if (alive) {
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
+            for (int s = 0; s < kHalf / 16; ++s)
                 mma_ts(d, p + 8 * s, v + ((s * 2048) >> 4), id, add || s > 0);
         }
-        mma_commit(bar + B_O_FULL + m);
+        mma_commit(bar + B_O_FULL + 2 * m + half);
     }
     __syncwarp();
 }
@@ -249,10 +275,14 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 if (m == 1 && !two) break;
-                alive &= waits.on(bar + B_P_FULL + m, done[m]++ & 1);
-                alive = __all_sync(0xffffffffu, alive);
-                tc_fence_after();
-                issue_pv<D>(tmem, dV, m, buf, i > 0, alive, bar);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    alive &= waits.on(bar + B_P_FULL + 2 * m + half, done[m] & 1);
+                    alive = __all_sync(0xffffffffu, alive);
+                    tc_fence_after();
+                    issue_pv<D>(tmem, dV, m, buf, half, i > 0 || half > 0, alive, bar);
+                }
+                ++done[m];
                 if (more) issue_qk<D>(tmem, dQ, dK, m, buf ^ 1, alive, bar);
             }
             commit(B_V_FREE + buf);
@@ -288,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
             const bool warps = i < B_K_FREE || i == B_V_FULL || i == B_V_FULL + 1 ||
-                               i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL ||
-                               i == B_P_FULL + 1;
+                               i == B_Q_FULL || i == B_Q_FULL + 1 ||
+                               (i >= B_P_FULL && i < B_O_FULL);
             mbar_init(bar + i, warps ? 4 : 1);
         }
         abort_flag = 0;
@@ -375,106 +405,113 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         tc_fence_after();
                         // (every lane of a warp takes part in what follows, whatever it sees)
                         const bool whole = __all_sync(0xffffffffu, t0 >= from && t0 + kTile <= to);
-                        uint32_t pk[64];
-                        float part = 0.f;
-                        auto numbers = [&](auto masked) {
-                            float p4[4] = {};
+                        const uint32_t *any = nan_any[(all + i) & 3];
+                        if (ok && (any[0] | any[1] | any[2] | any[3])) {
+                            const uint8_t *of = nan_of[(all + i) & 3];
+                            for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e) nan |= of[e];
+                        }
+                        // half a tile at a time: its products start while the rest is formed
+                        for (int half = 0; half < 2; ++half) {
+                            const int h0 = t0 + half * kHalf;       // first place
+                            const uint32_t tH = tS + half * kHalf;
+                            uint32_t pk[kHalf / 2];
+                            float part = 0.f;
+                            auto numbers = [&](auto masked) {
+                                const uint64_t mul2 = pack64(mul, mul), sub2 = pack64(-sub, -sub);
+                                uint64_t p2[2] = {};
+                                uint32_t x[2][32];
+                                tmem_ld32(tH, x[0]);
+                                tmem_ld32(tH + 32, x[1]);
+                                tmem_wait32(x[0]);
+                                tmem_wait32(x[1]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32(tS + 32 * c, x);
-                                tmem_wait32(x);
+                                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    float t[2];
-#pragma unroll
-                                    for (int k = 0; k < 2; ++k) {
-                                        t[k] = fmaf(__uint_as_float(x[e + k]), mul, -sub);
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const uint64_t t2 =
+                                            fma_f32x2(pack64(x[c][e], x[c][e + 1]), mul2, sub2);
+                                        float t[2];
+                                        unpack64(t2, t[0], t[1]);
                                         if constexpr (masked.value) {
-                                            const int at = t0 + 32 * c + e + k;
-                                            if (at < from || at >= to) t[k] = -INFINITY;
+                                            const int at = h0 + 32 * c + e;
+                                            if (at < from || at >= to) t[0] = -INFINITY;
+                                            if (at + 1 < from || at + 1 >= to) t[1] = -INFINITY;
                                         }
-                                        t[k] = ex2(t[k]);
-                                        p4[(e + k) & 3] += t[k];
+                                        t[0] = ex2(t[0]);
+                                        t[1] = ex2(t[1]);
+                                        p2[(e >> 1) & 1] =
+                                            add_f32x2(p2[(e >> 1) & 1], pack64(t[0], t[1]));
+                                        pk[16 * c + e / 2] = pack_f16(t[0], t[1]);
                                     }
-                                    pk[16 * c + e / 2] = pack_f16(t[0], t[1]);
-                                }
-                            }
-                            part = (p4[0] + p4[1]) + (p4[2] + p4[3]);
-                        };
-                        auto probabilities = [&]() {
-                            if (whole) numbers(std::false_type{});
-                            else numbers(std::true_type{});
-                        };
-                        if (ok) {
-                            if (__all_sync(0xffffffffu, started)) probabilities();
-                            else part = INFINITY;
-                            const bool move = !started || part > kMostSum;
-                            if (__any_sync(0xffffffffu, move)) {
-                                // the row's maximum of these scores, and `sub` by it
-                                float top = -INFINITY;
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    uint32_t x[32];
-                                    tmem_ld32(tS + 32 * c, x);
-                                    tmem_wait32(x);
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) {
-                                        const int at = t0 + 32 * c + e;
-                                        const float y = __uint_as_float(x[e]) * mul;
-                                        if (at >= from && at < to) top = fmaxf(top, y);
-                                    }
-                                }
-                                float f = 1.f;
-                                if (move && top > -INFINITY) {
-                                    const float to_new = top - kLift;
-                                    if (!started) {
-                                        sub = to_new;
-                                        started = true;
-                                    } else if (to_new > sub) {
-                                        f = ex2(sub - to_new);
-                                        sub = to_new;
-                                    }
-                                }
-                                sum *= f;
-                                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                                    waits.on(bar + B_O_FULL + m, (done - 1) & 1);
-                                    tc_fence_after();
-#pragma unroll
-                                    for (int c = 0; c < D / 32; ++c) {
+                                float y[4];
+                                unpack64(p2[0], y[0], y[1]);
+                                unpack64(p2[1], y[2], y[3]);
+                                part = (y[0] + y[1]) + (y[2] + y[3]);
+                            };
+                            auto probabilities = [&]() {
+                                if (whole) numbers(std::false_type{});
+                                else numbers(std::true_type{});
+                            };
+                            if (ok) {
+                                if (__all_sync(0xffffffffu, started)) probabilities();
+                                else part = INFINITY;
+                                const bool move = !started || part > kMostSum;
+                                if (__any_sync(0xffffffffu, move)) {
+                                    // the row's maximum of these scores, and `sub` by it
+                                    float top = -INFINITY;
+#pragma unroll 1
+                                    for (int c = 0; c < kHalf; c += 32) {
                                         uint32_t x[32];
-                                        tmem_ld32(tO + 32 * c, x);
+                                        tmem_ld32(tH + c, x);
                                         tmem_wait32(x);
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e)
-                                            x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                                        tmem_st32(tO + 32 * c, x);
+                                        for (int e = 0; e < 32; ++e) {
+                                            const int at = h0 + c + e;
+                                            const float y = __uint_as_float(x[e]) * mul;
+                                            if (at >= from && at < to) top = fmaxf(top, y);
+                                        }
                                     }
-                                    tmem_st_wait();
+                                    float f = 1.f;
+                                    if (move && top > -INFINITY) {
+                                        const float to_new = top - kLift;
+                                        if (!started) {
+                                            sub = to_new;
+                                            started = true;
+                                        } else if (to_new > sub) {
+                                            f = ex2(sub - to_new);
+                                            sub = to_new;
+                                        }
+                                    }
+                                    sum *= f;
+                                    if ((i > 0 || half > 0) && __any_sync(0xffffffffu, f != 1.f)) {
+                                        // (the half before this one; of tile i - 1 before its first)
+                                        waits.on(bar + B_O_FULL + 2 * m + (half ^ 1),
+                                                 (done - (half ^ 1)) & 1);
+                                        tc_fence_after();
+#pragma unroll 1
+                                        for (int c = 0; c < D; c += 32) {
+                                            uint32_t x[32];
+                                            tmem_ld32(tO + c, x);
+                                            tmem_wait32(x);
+#pragma unroll
+                                            for (int e = 0; e < 32; ++e)
+                                                x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                                            tmem_st32(tO + c, x);
+                                        }
+                                        tmem_st_wait();
+                                    }
+                                    probabilities();
                                 }
-                                probabilities();
+                                sum += part;
+                                tmem_st32(tS + half * (kHalf / 2), pk);
+                                tmem_st_wait();
                             }
-                            sum += part;
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t x[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = pk[32 * c + e];
-                                tmem_st32(tS + 32 * c, x);
-                            }
-                            tmem_st_wait();
-                            const uint32_t *any = nan_any[(all + i) & 3];
-                            if (any[0] | any[1] | any[2] | any[3]) {
-                                const uint8_t *of = nan_of[(all + i) & 3];
-                                for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e)
-                                    nan |= of[e];
-                            }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar + B_P_FULL + 2 * m + half);
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar + B_P_FULL + m);
                     }
-                    waits.on(bar + B_O_FULL + m, (done - 1) & 1);
+                    waits.on(bar + B_O_FULL + 2 * m + 1, (done - 1) & 1);
                     tc_fence_after();
                 }
                 all += count;
