@@ -69,7 +69,7 @@ struct Lay {
     static constexpr uint32_t TM_S = 0, TM_O = 256;              // TMEM columns, 128 a row tile
 };
 
-__device__ __forceinline__ uint32_t idesc_f16(int N, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
     // kind::f16 with fp16 A and B, fp32 accumulation, M = 128
     return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
@@ -202,95 +202,88 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Products of row tile m with the token tile in `buf`.  Every lane of the issuing
-// warp comes here, so that the descriptors stay in uniform registers; one issues.
-template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t tmem, uint64_t dQ, uint64_t dK, int m, int buf,
-                                         bool alive, uint64_t *bar) {
-    using L = Lay<D>;
-    const uint32_t id = idesc_f16(kTile, false), d = tmem + L::TM_S + 128 * m;
-    const uint64_t q = dQ + ((m * L::kOperand) >> 4), k = dK + ((buf * L::kOperand) >> 4);
-    if (elect_one()) {
-        if (alive) {
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
-                mma_bf16(d, q + off, k + off, id, s > 0);
-            }
-        }
-        mma_commit(bar + B_S_FULL + m);
-    }
-    __syncwarp();
-}
-template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t dV, int m, int buf, int half,
-                                         bool add, bool alive, uint64_t *bar) {
-    using L = Lay<D>;
-    const uint32_t id = idesc_f16(D, true), d = tmem + L::TM_O + 128 * m;
-    const uint32_t p = tmem + L::TM_S + 128 * m + half * (kHalf / 2);
-    const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
-    if (elect_one()) {
-        if (alive) {
-#pragma unroll
-            for (int s = 0; s < kHalf / 16; ++s)
-                mma_ts(d, p + 8 * s, v + ((s * 2048) >> 4), id, add || s > 0);
-        }
-        mma_commit(bar + B_O_FULL + 2 * m + half);
-    }
-    __syncwarp();
-}
-
+// The issuing warp.  Every lane walks along, so that the descriptors stay in
+// uniform registers, and an elected one issues.  Its loops are kept rolled: this
+// warp runs each instruction once a tile, and fetches what is long from far away.
 template <int D, typename W>
 __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &plan, W &w,
                                       long long beg, long long end, uint32_t base, uint32_t tmem,
                                       uint64_t *bar, const Waits &waits) {
     using L = Lay<D>;
+    constexpr uint32_t id_qk = idesc_f16(kTile, false), id_pv = idesc_f16(D, true);
     const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B);
     const uint64_t dK = make_sdesc(base + L::OFF_K, 16, 1024, kSwizzle128B);
     const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
-    uint32_t n = 0, done[2] = {}, pieces[2] = {};
+    uint32_t n = 0, done = 0, pieces = 0;      // bits m: parities of row tile m
     bool alive = true;
-    auto commit = [&](int b) {
-        if (elect_one()) mma_commit(bar + b);
+    // Q K^T of row tile m with the token tile in `buf`; the last row tile's frees the keys
+    auto scores = [&](int m, int buf, bool last) {
+        if (elect_one()) {
+            if (alive) {
+#pragma unroll 1
+                for (int s = 0; s < D / 64; ++s) {
+                    const uint64_t q = dQ + ((m * L::kOperand + s * 16384) >> 4);
+                    const uint64_t k = dK + ((buf * L::kOperand + s * 16384) >> 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mma_bf16(tmem + L::TM_S + 128 * m, q + 2 * e, k + 2 * e, id_qk,
+                                 (s | e) != 0);
+                }
+            }
+            mma_commit(bar + B_S_FULL + m);
+            if (last) mma_commit(bar + B_K_FREE + buf);
+        }
         __syncwarp();
     };
     w.start(a, plan, beg, end);
     do {
-        const int count = w.count();
-        const bool two = w.rows(a) > kRowTile;
+        const int count = w.count(), mt = w.rows(a) > kRowTile ? 2 : 1;
         if (count == 0) continue;
-        alive &= waits.on(bar + B_Q_FULL, pieces[0]++ & 1);
-        if (two) alive &= waits.on(bar + B_Q_FULL + 1, pieces[1]++ & 1);
+#pragma unroll 1
+        for (int m = 0; m < mt; ++m) {
+            alive &= waits.on(bar + B_Q_FULL + m, (pieces >> m) & 1);
+            pieces ^= 1u << m;
+        }
         alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
         alive = __all_sync(0xffffffffu, alive);
         tc_fence_after();
-        issue_qk<D>(tmem, dQ, dK, 0, n & 1, alive, bar);
-        if (two) issue_qk<D>(tmem, dQ, dK, 1, n & 1, alive, bar);
-        commit(B_K_FREE + (n & 1));
+#pragma unroll 1
+        for (int m = 0; m < mt; ++m) scores(m, n & 1, m + 1 == mt);
+#pragma unroll 1
         for (int i = 0; i < count; ++i, ++n) {
             const int buf = n & 1;
             const bool more = i + 1 < count;
             if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
             alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if (m == 1 && !two) break;
-#pragma unroll
+#pragma unroll 1
+            for (int m = 0; m < mt; ++m) {
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    alive &= waits.on(bar + B_P_FULL + 2 * m + half, done[m] & 1);
+                    alive &= waits.on(bar + B_P_FULL + 2 * m + half, (done >> m) & 1);
                     alive = __all_sync(0xffffffffu, alive);
                     tc_fence_after();
-                    issue_pv<D>(tmem, dV, m, buf, half, i > 0 || half > 0, alive, bar);
+                    if (elect_one()) {
+                        if (alive) {
+                            const uint32_t p = tmem + L::TM_S + 128 * m + half * (kHalf / 2);
+                            const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
+#pragma unroll
+                            for (int s = 0; s < kHalf / 16; ++s)
+                                mma_ts(tmem + L::TM_O + 128 * m, p + 8 * s, v + s * (2048 >> 4),
+                                       id_pv, (i | half | s) != 0);
+                        }
+                        mma_commit(bar + B_O_FULL + 2 * m + half);
+                        if (half + 1 == 2 && m + 1 == mt) mma_commit(bar + B_V_FREE + buf);
+                    }
+                    __syncwarp();
                 }
-                ++done[m];
-                if (more) issue_qk<D>(tmem, dQ, dK, m, buf ^ 1, alive, bar);
+                done ^= 1u << m;
+                if (more) scores(m, buf ^ 1, m + 1 == mt);
             }
-            commit(B_V_FREE + buf);
-            if (more) commit(B_K_FREE + (buf ^ 1));
         }
     } while (w.next(a));
     // before tensor memory is given back, whatever happened
-    commit(B_DRAIN);
+    if (elect_one()) mma_commit(bar + B_DRAIN);
+    __syncwarp();
     mbar_wait(bar + B_DRAIN, 0, a.wait_limit);
 }
 
