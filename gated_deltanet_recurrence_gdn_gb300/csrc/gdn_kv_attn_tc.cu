@@ -10,9 +10,10 @@
 //   warps 8-11       turn the next 128 tokens' 4-bit numbers into fp16 operand
 //                    tiles (128-byte swizzle), a thread a token, its codes
 //                    loaded straight into registers one tile ahead;
-//   warp 12          issues the products: QK of the next tokens right after PV of
-//                    these, one row tile after the other, so that the softmax of
-//                    one runs while the tensor cores work for the other.
+//   warps 12, 13     issue the products of row tile 0 and 1.  Scores and
+//                    probabilities go by halves of 64 tokens with columns of their
+//                    own: while the softmax works on one half, PV of the other and
+//                    QK of the next tile's follow.
 // The products bound it (2 x 2 x 128^3 multiply-adds a tile at d = 128), and next
 // to them the exponentials; turning a tile into fp16 costs 1/4 of that time in
 // issue slots because 256 rows share it.
@@ -38,7 +39,7 @@ constexpr int kRowTile = 128;
 constexpr int kRows = 2 * kRowTile;
 constexpr int kThreads = 512;
 constexpr int kConvert = 256;               // first thread of the converting warps
-constexpr int kIssuer = 384;                // the issuing thread
+constexpr int kIssuer = 384;                // first thread of the issuing warps
 // Registers a thread of each role; together no more than the launch's 512 x 128.
 constexpr int kSoftmaxRegs = 168, kConvertRegs = 96, kIssuerRegs = 64;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssuerRegs <= 512 * 128, "registers");
@@ -48,15 +49,15 @@ constexpr float kMostSum = 32768.f;         // of a tile: above it `sub` moves
 // mbarriers
 enum : int {
     B_K_FULL = 0,             // [2] converted keys; 4 warps
-    B_K_FREE = 2,             // [2] their products are done
+    B_K_FREE = 2,             // [2] their products are done; 2 issuing warps
     B_V_FULL = 4,             // [2]
     B_V_FREE = 6,             // [2]
     B_Q_FULL = 8,             // [2] a row tile's queries; 4 warps
-    B_S_FULL = 10,            // [2] scores of a row tile
-    B_P_FULL = 12,            // [2][2] probabilities of each half of a tile; 4 warps
-    B_O_FULL = 16,            // [2][2] their PV is done
-    B_DRAIN = 20,
-    B_COUNT = 21
+    B_S_FULL = 10,            // [2][2] scores of a row tile with each half of the tokens
+    B_P_FULL = 14,            // [2][2] probabilities; 4 warps
+    B_O_FULL = 18,            // [2][2] their PV is done
+    B_DRAIN = 22,             // [2]
+    B_COUNT = 24
 };
 
 template <int D>
@@ -202,89 +203,98 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// The issuing warp.  Every lane walks along, so that the descriptors stay in
-// uniform registers, and an elected one issues.  Its loops are kept rolled: this
-// warp runs each instruction once a tile, and fetches what is long from far away.
+// The issuing warp of row tile m.  Every lane walks along, so that the descriptors
+// stay in uniform registers, and an elected one issues; while one of the two warps
+// waits, the other keeps the tensor cores fed (their queue is a few products
+// deep).  The loops are kept rolled: a warp runs each instruction once a tile, and
+// fetches what is long from far away.
 template <int D, typename W>
 __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &plan, W &w,
                                       long long beg, long long end, uint32_t base, uint32_t tmem,
-                                      uint64_t *bar, const Waits &waits) {
+                                      uint64_t *bar, const Waits &waits, int m) {
     using L = Lay<D>;
-    constexpr uint32_t id_qk = idesc_f16(kTile, false), id_pv = idesc_f16(D, true);
-    const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B);
+    constexpr uint32_t id_qk = idesc_f16(kHalf, false), id_pv = idesc_f16(D, true);
+    const uint64_t dQ = make_sdesc(base + L::OFF_Q, 16, 1024, kSwizzle128B) +
+                        ((m * L::kOperand) >> 4);
     const uint64_t dK = make_sdesc(base + L::OFF_K, 16, 1024, kSwizzle128B);
     const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
-    uint32_t n = 0, done = 0, pieces = 0;      // bits m: parities of row tile m
+    const uint32_t tS = tmem + L::TM_S + 128 * m, tO = tmem + L::TM_O + 128 * m;
+    uint32_t n = 0, done = 0, pieces = 0;
     bool alive = true;
-    // Q K^T of row tile m with the token tile in `buf`; the last row tile's frees the keys
-    auto scores = [&](int m, int buf, bool last) {
+    // Q K^T with half of the token tile in `buf`; the second half's frees the keys
+    auto scores = [&](int half, int buf) {
         if (elect_one()) {
             if (alive) {
 #pragma unroll 1
                 for (int s = 0; s < D / 64; ++s) {
-                    const uint64_t q = dQ + ((m * L::kOperand + s * 16384) >> 4);
-                    const uint64_t k = dK + ((buf * L::kOperand + s * 16384) >> 4);
+                    const uint64_t q = dQ + ((s * 16384) >> 4);
+                    const uint64_t k =
+                        dK + ((buf * L::kOperand + s * 16384 + half * kHalf * 128) >> 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mma_bf16(tmem + L::TM_S + 128 * m, q + 2 * e, k + 2 * e, id_qk,
-                                 (s | e) != 0);
+                        mma_bf16(tS + kHalf * half, q + 2 * e, k + 2 * e, id_qk, (s | e) != 0);
                 }
             }
-            mma_commit(bar + B_S_FULL + m);
-            if (last) mma_commit(bar + B_K_FREE + buf);
+            mma_commit(bar + B_S_FULL + 2 * m + half);
+            if (half == 1) mma_commit(bar + B_K_FREE + buf);
         }
         __syncwarp();
     };
     w.start(a, plan, beg, end);
     do {
-        const int count = w.count(), mt = w.rows(a) > kRowTile ? 2 : 1;
+        const int count = w.count();
         if (count == 0) continue;
+        if (w.rows(a) <= m * kRowTile) {
+            // no rows: the tiles go by, in step with the other warp's
 #pragma unroll 1
-        for (int m = 0; m < mt; ++m) {
-            alive &= waits.on(bar + B_Q_FULL + m, (pieces >> m) & 1);
-            pieces ^= 1u << m;
+            for (int i = 0; i < count; ++i, ++n) {
+                waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
+                waits.on(bar + B_V_FULL + (n & 1), (n >> 1) & 1);
+                if (elect_one()) {
+                    mbar_arrive(bar + B_K_FREE + (n & 1));
+                    mbar_arrive(bar + B_V_FREE + (n & 1));
+                }
+                __syncwarp();
+            }
+            continue;
         }
+        alive &= waits.on(bar + B_Q_FULL + m, pieces++ & 1);
         alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
         alive = __all_sync(0xffffffffu, alive);
         tc_fence_after();
+        scores(0, n & 1);
+        scores(1, n & 1);
 #pragma unroll 1
-        for (int m = 0; m < mt; ++m) scores(m, n & 1, m + 1 == mt);
-#pragma unroll 1
-        for (int i = 0; i < count; ++i, ++n) {
+        for (int i = 0; i < count; ++i, ++n, ++done) {
             const int buf = n & 1;
             const bool more = i + 1 < count;
             if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
             alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
 #pragma unroll 1
-            for (int m = 0; m < mt; ++m) {
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    alive &= waits.on(bar + B_P_FULL + 2 * m + half, (done >> m) & 1);
-                    alive = __all_sync(0xffffffffu, alive);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (alive) {
-                            const uint32_t p = tmem + L::TM_S + 128 * m + half * (kHalf / 2);
-                            const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
+            for (int half = 0; half < 2; ++half) {
+                alive &= waits.on(bar + B_P_FULL + 2 * m + half, done & 1);
+                alive = __all_sync(0xffffffffu, alive);
+                tc_fence_after();
+                if (elect_one()) {
+                    if (alive) {
+                        const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
 #pragma unroll
-                            for (int s = 0; s < kHalf / 16; ++s)
-                                mma_ts(tmem + L::TM_O + 128 * m, p + 8 * s, v + s * (2048 >> 4),
-                                       id_pv, (i | half | s) != 0);
-                        }
-                        mma_commit(bar + B_O_FULL + 2 * m + half);
-                        if (half + 1 == 2 && m + 1 == mt) mma_commit(bar + B_V_FREE + buf);
+                        for (int s = 0; s < kHalf / 16; ++s)
+                            mma_ts(tO, tS + kHalf * half + 8 * s, v + s * (2048 >> 4), id_pv,
+                                   (i | half | s) != 0);
                     }
-                    __syncwarp();
+                    mma_commit(bar + B_O_FULL + 2 * m + half);
+                    if (half == 1) mma_commit(bar + B_V_FREE + buf);
                 }
-                done ^= 1u << m;
-                if (more) scores(m, buf ^ 1, m + 1 == mt);
+                __syncwarp();
+                if (more) scores(half, buf ^ 1);
             }
         }
     } while (w.next(a));
     // before tensor memory is given back, whatever happened
-    if (elect_one()) mma_commit(bar + B_DRAIN);
+    if (elect_one()) mma_commit(bar + B_DRAIN + m);
     __syncwarp();
-    mbar_wait(bar + B_DRAIN, 0, a.wait_limit);
+    mbar_wait(bar + B_DRAIN + m, 0, a.wait_limit);
 }
 
 template <int D>
@@ -313,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
             const bool warps = i < B_K_FREE || i == B_V_FULL || i == B_V_FULL + 1 ||
                                i == B_Q_FULL || i == B_Q_FULL + 1 ||
                                (i >= B_P_FULL && i < B_O_FULL);
-            mbar_init(bar + i, warps ? 4 : 1);
+            const bool free = (i >= B_K_FREE && i < B_V_FULL) || (i >= B_V_FREE && i < B_Q_FULL);
+            mbar_init(bar + i, warps ? 4 : free ? 2 : 1);
         }
         abort_flag = 0;
         fence_mbar_init();
@@ -394,19 +405,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
 
                     for (int i = 0; i < count; ++i, ++done) {
                         const int t0 = place0 + i * kTile;
-                        const bool ok = waits.on(bar + B_S_FULL + m, done & 1);
-                        tc_fence_after();
                         // (every lane of a warp takes part in what follows, whatever it sees)
                         const bool whole = __all_sync(0xffffffffu, t0 >= from && t0 + kTile <= to);
-                        const uint32_t *any = nan_any[(all + i) & 3];
-                        if (ok && (any[0] | any[1] | any[2] | any[3])) {
-                            const uint8_t *of = nan_of[(all + i) & 3];
-                            for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e) nan |= of[e];
-                        }
-                        // half a tile at a time: its products start while the rest is formed
+                        // Half a tile at a time, in columns of its own: while one half's numbers are
+                        // formed, the tensor cores finish the other's and score the next tile's.
                         for (int half = 0; half < 2; ++half) {
                             const int h0 = t0 + half * kHalf;       // first place
                             const uint32_t tH = tS + half * kHalf;
+                            const bool ok = waits.on(bar + B_S_FULL + 2 * m + half, done & 1);
+                            tc_fence_after();
+                            const uint32_t *any = nan_any[(all + i) & 3];
+                            if (half == 0 && ok && (any[0] | any[1] | any[2] | any[3])) {
+                                const uint8_t *of = nan_of[(all + i) & 3];
+                                for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e)
+                                    nan |= of[e];
+                            }
                             uint32_t pk[kHalf / 2];
                             float part = 0.f;
                             auto numbers = [&](auto masked) {
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                                     probabilities();
                                 }
                                 sum += part;
-                                tmem_st32(tS + half * (kHalf / 2), pk);
+                                tmem_st32(tH, pk);
                                 tmem_st_wait();
                             }
                             tc_fence_before();
@@ -601,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
             } while (w.next(a));
         } else {
             regs_less<kIssuerRegs>();
-            if (warp == kIssuer / 32) issue<D>(a, plan, w, beg, end, base, tmem, bar, waits);
+            if (warp < kIssuer / 32 + 2)
+                issue<D>(a, plan, w, beg, end, base, tmem, bar, waits, warp - kIssuer / 32);
         }
     }
     tc_fence_before();
