@@ -55,8 +55,8 @@ __device__ __forceinline__ void put_unit(uint8_t *code_row, uint8_t *scale_row, 
 // blockIdx.y takes heads_per of the Hq + 2 H items (query, key, value heads).
 // Every lane of a warp runs the same items (the scale is taken across lanes);
 // lanes past the last token only take part in that.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int kFly>
+__global__ void __launch_bounds__(kThreads, 4)
 k_kv_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Rows<T> qo, int Hq,
             int heads_per, bool rotate, const __grid_constant__ Rotary rot, int *err) {
     const int units = kv.d / 16;                     // 4, 8 or 16: divides a warp
@@ -66,6 +66,22 @@ k_kv_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Rows
     const int t = there ? t0 : kv.n_tokens - 1;
     const Unit un = unit_of(rot, u);
     const Unit whole{16 * u, 16 * u + 8, false};
+    const int i0 = blockIdx.y * heads_per, i1 = min(i0 + heads_per, Hq + 2 * kv.H);
+    Run<T> x[kFly], y[kFly];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+            if (i + f < i1) {
+                const int h = i + f;
+                const T *p = h < Hq          ? q.at(0, h, t)
+                             : h < Hq + kv.H ? k.at(0, h - Hq, t)
+                                             : v.at(0, h - Hq - kv.H, t);
+                const Unit &w = h < Hq + kv.H ? un : whole;
+                x[f].load(p + w.lo);
+                y[f].load(p + w.hi);
+            }
+    };
+    load(i0);
     float c[8], s[8];
     if (rotate && un.turned) unit_angles(rot, u, 0, t, c, s, err);
     const int b = kv.seq_of(t);
@@ -78,34 +94,33 @@ k_kv_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Rows
     const int row = place & (kv.page_size() - 1), psz = kv.page_size();
     uint8_t *base = kv.pages + kv.block(live ? page : 0, 0);
     const int step = block_bytes(psz, kv.d);
-    const int i0 = blockIdx.y * heads_per, i1 = min(i0 + heads_per, Hq + 2 * kv.H);
-    for (int i = i0; i < i1; ++i) {
-        float x[8], y[8];
-        if (i < Hq) {
-            const T *p = q.at(0, i, t);
-            load8(p + un.lo, x);
-            load8(p + un.hi, y);
-            if (rotate && un.turned) turn(rot.adjacent, c, s, x, y);
-            if (there) {
-                T *o = qo.at(0, i, t);
-                store8(o + un.lo, x);
-                store8(o + un.hi, y);
+    for (int i = i0; i < i1;) {
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            if (i + f >= i1) break;
+            float a[8], e[8];
+            x[f].get(a);
+            y[f].get(e);
+            if (i + f < Hq + kv.H && rotate && un.turned) turn(rot.adjacent, c, s, a, e);
+            if (i + f < Hq) {
+                if (there) {
+                    T *o = qo.at(0, i + f, t);
+                    store8(o + un.lo, a);
+                    store8(o + un.hi, e);
+                }
+            } else {
+                const bool key = i + f < Hq + kv.H;
+                const int h = key ? i + f - Hq : i + f - Hq - kv.H;
+                const float inv =
+                    kv.head_scale ? __frcp_rn(__ldg(kv.head_scale + (key ? 0 : kv.H) + h)) : 1.f;
+                uint8_t *blk = base + (long long)h * step;
+                put_unit(blk + (key ? k_code_at(psz, kv.d, row) : v_code_at(psz, kv.d, row)),
+                         blk + (key ? k_scale_at(psz, kv.d, row) : v_scale_at(psz, kv.d, row)),
+                         key ? un : whole, key && un.turned && !rot.adjacent, live, inv, a, e);
             }
-        } else {
-            const bool key = i < Hq + kv.H;
-            const int h = key ? i - Hq : i - Hq - kv.H;
-            const Unit w = key ? un : whole;
-            const T *p = key ? k.at(0, h, t) : v.at(0, h, t);
-            load8(p + w.lo, x);
-            load8(p + w.hi, y);
-            if (key && rotate && un.turned) turn(rot.adjacent, c, s, x, y);
-            const float inv =
-                kv.head_scale ? __frcp_rn(__ldg(kv.head_scale + (key ? 0 : kv.H) + h)) : 1.f;
-            uint8_t *blk = base + (long long)h * step;
-            put_unit(blk + (key ? k_code_at(psz, kv.d, row) : v_code_at(psz, kv.d, row)),
-                     blk + (key ? k_scale_at(psz, kv.d, row) : v_scale_at(psz, kv.d, row)), w,
-                     key && un.turned && !rot.adjacent, live, inv, x, y);
         }
+        i += kFly;
+        load(i);
     }
 }
 
@@ -159,21 +174,21 @@ k_kv_read(const Kv kv, Rows<T> k, Rows<T> v, int heads_per, int *err) {
     }
 }
 
-// Heads a CTA walks over, so that few tokens still make about 4 CTAs an SM.
+// Heads a CTA walks over, so that few tokens still make about 16 CTAs an SM.
 int heads_per_cta(long long gx, int items) {
-    const long long want = (152 * 4 + gx - 1) / gx;
+    const long long want = (152 * 16 + gx - 1) / gx;
     const int split = (int)(want < items ? want : items);
     return (items + split - 1) / split;
 }
 
-template <typename T>
+template <typename T, int kFly>
 cudaError_t launch_append(const Kv &kv, const gdn_rows *k, const gdn_rows *v, const gdn_rows *q,
                           const gdn_rows *qo, bool rotate, const Rotary &rot, cudaStream_t st) {
     const int per = kThreads / (kv.d / 16), Hq = q ? q->heads : 0, items = Hq + 2 * kv.H;
     const int gx = (kv.n_tokens + per - 1) / per, heads_per = heads_per_cta(gx, items);
     const dim3 grid(gx, (items + heads_per - 1) / heads_per);
     const int slot = timer_begin(st, "k_kv_append");
-    k_kv_append<T><<<grid, kThreads, 0, st>>>(kv, rows_of<const T>(k), rows_of<const T>(v),
+    k_kv_append<T, kFly><<<grid, kThreads, 0, st>>>(kv, rows_of<const T>(k), rows_of<const T>(v),
                                               rows_of<const T>(q), rows_of<T>(qo), Hq, heads_per,
                                               rotate, rot, device_error_word());
     timer_end(slot, st);
@@ -250,8 +265,8 @@ gdn_status gdn_kv_append(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v,
     if (rot && (rc = check_rotary(rot, kv->d, true, &r)) != GDN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        dt == GDN_BF16 ? launch_append<__nv_bfloat16>(dev, k, v, q, q_out, rot != nullptr, r, st)
-                       : launch_append<float>(dev, k, v, q, q_out, rot != nullptr, r, st);
+        dt == GDN_BF16 ? launch_append<__nv_bfloat16, 2>(dev, k, v, q, q_out, rot != nullptr, r, st)
+                       : launch_append<float, 1>(dev, k, v, q, q_out, rot != nullptr, r, st);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
