@@ -217,13 +217,20 @@ struct Kv {
     __device__ __forceinline__ long long block(int page, int h) const {
         return ((long long)page * H + h) * block_bytes(1 << page_shift, d);
     }
-    // Page of place p of sequence b, -1 with the error recorded if it is outside
-    // the pool.
-    __device__ __forceinline__ int page_of(int b, int p, int *err) const {
-        const int g = __ldg(page_table + b * table_stride + (p >> page_shift));
+    // Page of place p of sequence b as the table has it, and the same checked: -1 with
+    // the error recorded if it is outside the pool.  (Apart, so that a look-up made
+    // ahead is not waited for where it is made; kNoPage passes through as -1.)
+    static constexpr int kNoPage = -0x7fffffff;
+    __device__ __forceinline__ int page_raw(int b, int p) const {
+        return __ldg(page_table + b * table_stride + (p >> page_shift));
+    }
+    __device__ __forceinline__ int page_checked(int g, int *err) const {
         if ((unsigned)g < (unsigned)n_pages) return g;
-        atomicCAS(err, 0, kErrBadIndex);
+        if (g != kNoPage) atomicCAS(err, 0, kErrBadIndex);
         return -1;
+    }
+    __device__ __forceinline__ int page_of(int b, int p, int *err) const {
+        return page_checked(page_raw(b, p), err);
     }
     // Tokens [first, first + n) and length of sequence b.  Offsets or lengths
     // out of range are recorded, and the sequence then counts as having none.

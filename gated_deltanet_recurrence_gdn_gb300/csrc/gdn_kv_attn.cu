@@ -41,7 +41,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
-constexpr int kMany = 32;                     // rows of a key/value head: then tcgen05 products
+constexpr int kMany = 16;                     // rows of a key/value head: then tcgen05 products
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -325,11 +325,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
 #pragma unroll
             for (int k = 0; k < kRuns; ++k) {
                 const int in_tile = (lane_run + 8 * k) * run, at = place0 + i * kTile + in_tile;
-                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_of(w.b, at, a.err)
-                                                                       : -1;
+                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_raw(w.b, at)
+                                                                       : Kv::kNoPage;
             }
         };
-        auto produce = [&](int i, const int (&page)[kRuns]) {    // one warp
+        auto produce = [&](int i, const int (&raw)[kRuns]) {    // one warp
+            int page[kRuns];
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) page[k] = a.kv.page_checked(raw[k], a.err);
             const uint32_t n = tiles_before + i, stage = n % kStages;
             if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
             uint32_t runs = 0;

@@ -573,10 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 const int psz = a.kv.page_size();
                 auto page_at = [&](int i) {
                     const int at = place0 + i * kTile + tok;
-                    return i < count && at < len ? a.kv.page_of(w.b, at, a.err) : -1;
+                    return i < count && at < len ? a.kv.page_raw(w.b, at) : Kv::kNoPage;
                 };
                 Token<D> k, v;
-                auto load = [&](Token<D> &x, int i, int page, bool key) {
+                auto load = [&](Token<D> &x, int i, int raw, bool key) {
+                    const int page = a.kv.page_checked(raw, a.err);
                     if (page < 0) {
                         x.clear();
                         return;
