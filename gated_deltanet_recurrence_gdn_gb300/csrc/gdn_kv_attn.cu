@@ -6,10 +6,12 @@
 // that the instructions that turn 4-bit numbers into fp16 operands: at 144 bytes
 // a (token, head) of d = 128 and 6.8 TB/s an SM has 3 issue slots per element.
 //
-// - A tile of 128 tokens is copied into a ring of shared memory by bulk copies
-//   (one per page and part of it), each warp issuing every eighth tile's; a warp
-//   takes 16 tokens of every tile, and no barrier joins the warps until a piece
-//   of work ends.
+// - A tile (256 tokens; 128 at d = 256) is copied into a ring of shared memory by
+//   bulk copies, one per page and part of it, each warp issuing every eighth
+//   tile's; a warp takes its 16 or 32 tokens of every tile, and no barrier joins
+//   the warps until a piece of work ends.  The next piece's first tile and its
+//   place in the work are fetched with the last tile of the piece before it
+//   (64 ragged sequences below: 178 us without that).
 // - Tokens are the M side of the products: S^T[16 x 8] = K[16 x d] Q^T[d x 8],
 //   O^T[d x 8] += V^T[d x 16] P^T[16 x 8], so 8 query rows of a key/value head
 //   cost one n = 8 tile and a single row no more.
@@ -19,21 +21,28 @@
 //   nibbles of two tokens are merged before the conversion (4 instructions per
 //   16 numbers).  e2m1 -> fp16 is the hardware conversion (64 a clock an SM);
 //   times the block's e4m3 scale it is exact in fp16.
+// - Rows are scaled by a power of two and rounded to fp16 (fp32 rows to two fp16
+//   numbers, 22 bits).  bf16 rows keep all their 8 bits.
 // - The running maximum of a row moves only when a score passes it by more than
 //   kRaise (log2 units), so the output's registers are seldom rescaled.
-//   Probabilities are carried times 2^kLift, which fills fp16's range: at most
-//   2^15, and a weight keeps its bits down to 2^-28 of the row's largest (2^-17
-//   as two numbers).  Smaller ones are multiplied up into that range and added
-//   by a product of their own, so that they count where the largest weights
-//   meet zeros.
+//   Probabilities are rounded to fp16, the products' type, times 2^kLift, which
+//   fills that type's range: at most 2^15, and a weight keeps its bits down to
+//   2^-28 of the row's largest (2^-17 as two numbers).  Smaller ones are
+//   multiplied up into that range and added by a product of their own, so that
+//   they count where the largest weights meet zeros.  Sums are fp32.
 // - A CTA's tiles are a contiguous share of all tiles (Plan, gdn_kv_attn.cuh);
 //   pieces of a cut (sequence, head) go to scratch as fp32 sums and k_kv_join
 //   adds them in a fixed order.
+//
+// Measured, join included (bf16, d = 128, one token a sequence, pages read cold):
+//   256 sequences of 8000 to 8192, 8 heads:    473 us, 5.0 TB/s (2.39 GB);
+//   64 ragged ones of 128 to 16384, 8 heads:   167 us, 4.0 TB/s (665 MB);
+//   one of 131072, 4 heads:                     35 us, 2.2 TB/s (75 MB).
+// Issue slots bound the first (about 340 instructions per 16 tokens and warp, 65 %
+// of the slots taken, DRAM at 74 %); the last one spends 10 us in starting up,
+// finding its pages and the join.
 #include "gdn_kv_attn.cuh"
 
-#define KU 2
-#define KS 3
-#define KX 0
 namespace gdn {
 namespace kv {
 namespace {
@@ -41,7 +50,10 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
-constexpr int kMany = 16;                     // rows of a key/value head: then tcgen05 products
+// Rows of a key/value head above which the products go to tcgen05 (gdn_kv_attn_tc.cu),
+// whose time does not depend on them up to 128: there 490 us for 64 ragged sequences, here
+// 165 for every 8 rows (one pass more over the cache), so 330 for 16 and 495 for 24.
+constexpr int kMany = 16;
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -105,28 +117,30 @@ __device__ __forceinline__ void operand_of(const float (&p)[4], uint32_t (&hi)[2
 }
 
 // kSplit: queries and probabilities as two fp16 numbers each (fp32 I/O).
-// kU: groups of a warp in a tile.
-template <int D, int NT, bool kSplit, int kU, int kStages>
+// kU: groups of a warp in a tile.  Two groups and three stages leave room for two
+// CTAs an SM (bf16, d <= 128); two stages took 522 us where three took 462.
+template <int D, bool kSplit, int kU, int kStages>
 struct Shape {
     static constexpr int kTile = kWarps * kU * kGroup;
-    static constexpr int kRows = 8 * NT;
+    static constexpr int kRows = 8;
     static constexpr int kParts = kSplit ? 2 : 1;
     // a stage: key codes, value codes, key scales, value scales of a tile
     static constexpr int kVCode = kTile * D / 2, kKScale = kTile * D, kVScale = kTile * D * 17 / 16;
     static constexpr int kStage = kTile * D * 9 / 8;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kMerge = kWarps * 8 * D * 4;          // 8 rows of every warp
-    static_assert(kMerge <= kRing, "the ring holds a merge");
-    static constexpr int kQueries = kParts * NT * (D / 16) * 32 * 8;
+    static constexpr int kQueries = kParts * (D / 16) * 32 * 8;
+    // rows of every warp that are merged at a time, in one stage
+    static constexpr int kMergeRows = kWarps * 8 * D * 4 <= kStage ? 8 : 4;
+    static_assert(kWarps * kMergeRows * D * 4 <= kStage, "a stage holds a merge");
     static constexpr int kSmem = kRing + kQueries;
     static constexpr int kLead = kStages - 2;                  // tiles copied ahead
 };
 
 // S^T of a warp's group (its first row at `codes` and `scales`): K, rows
 // place_of(g) and 8 more, times Q^T.
-template <int D, int NT, int kParts>
+template <int D, int kParts>
 __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scales, int g, int t4,
-                                       const uint4 *queries, float (&s)[NT][4]) {
+                                       const uint4 *queries, float (&s)[4]) {
     constexpr int kW = D / 32;      // 32-bit words of a lane's share of a row
     uint32_t kw[2][kW];
     __half2 ks[2][kW / 2];          // scale of each block, twice
@@ -152,7 +166,7 @@ __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scal
             }
         }
     }
-    float s2[NT][4];                // a second chain of products
+    float s2[4];                    // a second chain of products
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
         uint32_t r0[4], r1[4];
@@ -164,23 +178,19 @@ __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scal
             r1[e] = mul2(r1[e], ks[1][w / 2]);
         }
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint4 q = queries[((part * NT + nt) * kW + w) * 32];
-                if (w == 0 && part == 0) {
-                    mma16816_zero(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
-                    mma16816_zero(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
-                } else {
-                    mma16816(s[nt], r0[0], r1[0], r0[1], r1[1], q.x, q.y);
-                    mma16816(s2[nt], r0[2], r1[2], r0[3], r1[3], q.z, q.w);
-                }
+        for (int part = 0; part < kParts; ++part) {
+            const uint4 q = queries[(part * kW + w) * 32];
+            if (w == 0 && part == 0) {
+                mma16816_zero(s, r0[0], r1[0], r0[1], r1[1], q.x, q.y);
+                mma16816_zero(s2, r0[2], r1[2], r0[3], r1[3], q.z, q.w);
+            } else {
+                mma16816(s, r0[0], r1[0], r0[1], r1[1], q.x, q.y);
+                mma16816(s2, r0[2], r1[2], r0[3], r1[3], q.z, q.w);
             }
+        }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
+    for (int e = 0; e < 4; ++e) s[e] += s2[e];
 }
 
 // A lane's numbers of V of one group: D / 8 elements of the tokens t4, 4 + (t4 ^ 1)
@@ -223,9 +233,9 @@ struct VShare {
 };
 
 // O^T += V^T P^T, or with kScaled O^T += factor * (V^T P^T).
-template <int D, int NT, int kParts, bool kScaled>
-__device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)[kParts][NT][2],
-                                        float factor, float (&o)[NT][D / 16][4]) {
+template <int D, int kParts, bool kScaled>
+__device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)[kParts][2],
+                                        float factor, float (&o)[D / 16][4]) {
     __half2 sc[VShare<D>::kBlocks][2];
 #pragma unroll
     for (int k = 0; k < VShare<D>::kBlocks; ++k)
@@ -244,29 +254,26 @@ __device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)
         for (int k = 0; k < 4; ++k) {
             const uint32_t a0 = mul2(e1[k], s1), a1 = mul2(d1[k], s1);
             const uint32_t a2 = mul2(e2[k], s2), a3 = mul2(d2[k], s2);
+            float (&acc)[4] = o[4 * w + k];
+            if constexpr (!kScaled) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float (&acc)[4] = o[nt][4 * w + k];
-                if constexpr (!kScaled) {
+                for (int part = 0; part < kParts; ++part)
+                    mma16816(acc, a0, a1, a2, a3, pf[part][0], pf[part][1]);
+            } else {
+                float x[4] = {};
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-                        mma16816(acc, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
-                } else {
-                    float x[4] = {};
+                for (int part = 0; part < kParts; ++part)
+                    mma16816(x, a0, a1, a2, a3, pf[part][0], pf[part][1]);
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-                        mma16816(x, a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
-                }
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
             }
         }
     }
 }
 
-template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
-    using Sh = Shape<D, NT, kSplit, kU, kStages>;
+    using Sh = Shape<D, kSplit, kU, kStages>;
     constexpr int kTile = Sh::kTile;
     using W = Walk<kTile, Sh::kRows, kThreads>;
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
@@ -281,6 +288,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     __shared__ int abort_flag;
     __shared__ float2 warp_ml[kWarps][kRows];
     __shared__ float row_mul[kRows];
+    __shared__ W walk[2];           // the piece at work and the one after it
+    __shared__ bool walk_more;      // there is one
     __shared__ int row_from[kRows], row_to[kRows], all_seen[2];
     uint4 *queries = reinterpret_cast<uint4 *>(smem + Sh::kRing);
 
@@ -312,358 +321,385 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                               : lane_part == 2 ? Sh::kKScale
                                                : Sh::kVScale;
     constexpr int kRuns = kTile / 16 / 8;         // of a lane, at the smallest pages
-    uint32_t tiles_before = 0;      // of the earlier pieces: a tile's stage and phase
-    W w;
-    w.start(a, plan, beg, end);
-    do {
-        const Seq sq = w.sq;
-        const int h = w.h, row0 = w.row0(), rows = w.rows(a);
-        const int place0 = w.place0(), n_copy = w.count();
+    // pages of the lane's runs (8 apart) of the tile at `place`, as the table has them
+    auto fetch = [&](bool there, int b, int place, int len, int (&raw)[kRuns]) {
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            const int in_tile = (lane_run + 8 * k) * run, at = place + in_tile;
+            raw[k] = there && in_tile < kTile && at < len ? a.kv.page_raw(b, at) : Kv::kNoPage;
+        }
+    };
+    // copies the CTA's tile n, whose first place is `place` (one warp)
+    int last_made = -1;                           // the last one that this warp copied
+    auto produce = [&](uint32_t n, int place, int h, const int (&raw)[kRuns]) {
+        int page[kRuns];
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) page[k] = a.kv.page_checked(raw[k], a.err);
+        const uint32_t stage = n % kStages;
+        if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
+        uint32_t runs = 0;
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k)
+            runs += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && lane_part == 0));
+        last_made = n;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            if (page[k] < 0) continue;
+            const int psz = a.kv.page_size(), in_tile = (lane_run + 8 * k) * run;
+            const int at = (place + in_tile) & (psz - 1);
+            const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + at * row_bytes +
+                                 (lane_part == 0   ? 0
+                                  : lane_part == 1 ? v_code_at(psz, D, 0)
+                                  : lane_part == 2 ? k_scale_at(psz, D, 0)
+                                                   : v_scale_at(psz, D, 0));
+            bulk_load(ring_at + stage * Sh::kStage + lane_dst + in_tile * row_bytes, src,
+                      run * row_bytes, full + stage);
+        }
+    };
 
-        // pages of the lane's runs (8 apart) of tile i, -1 if there is none to copy
-        auto fetch = [&](int i, int (&page)[kRuns]) {
+    // Queries of a piece, by warp 0: the lane's part of row g, loaded ...
+    auto row_of = [&](const W &w, bool &there, int &j) {
+        const int r = w.row0() + g;
+        there = g < w.rows(a);
+        j = there ? r / a.G : 0;
+        return there ? r - j * a.G : 0;
+    };
+    auto load_queries = [&](const W &w, Run<T> (&x)[D / 32]) {
+        bool there;
+        int j;
+        const int i = row_of(w, there, j);
+        const T *p = static_cast<const T *>(a.q) + (w.sq.first + j) * a.q_tok +
+                     (long long)(w.h * a.G + i) * a.q_head + t4 * (D / 4);
 #pragma unroll
-            for (int k = 0; k < kRuns; ++k) {
-                const int in_tile = (lane_run + 8 * k) * run, at = place0 + i * kTile + in_tile;
-                page[k] = i < n_copy && in_tile < kTile && at < sq.len ? a.kv.page_raw(w.b, at)
-                                                                       : Kv::kNoPage;
+        for (int k = 0; k < D / 32; ++k) {
+            x[k] = Run<T>{};
+            if (there) x[k].load(p + 8 * k);
+        }
+    };
+    // ... and as the B operand, scaled by a power of two that brings the row's largest
+    // number to [2^13, 2^14), with what the rows see.
+    auto put_queries = [&](const W &w, const Run<T> (&x)[D / 32]) {
+        bool there;
+        int j;
+        row_of(w, there, j);
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            float v[8];
+            x[k].get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+        }
+        if (!there) m = 0.f;
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        float down;
+        const float up = row_up(m, down);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            float v[8];
+            x[k].get(v);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float u = there ? v[2 * e] * up : 0.f, y = there ? v[2 * e + 1] * up : 0.f;
+                hi[e] = pack_f16(u, y);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
+                lo[e] = pack_f16(u - f.x, y - f.y);
             }
+            uint4 *q = queries + k * 32 + lane;
+            q[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (kSplit) q[(D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        int from = 0, to = w.sq.len;
+        if (there) w.sq.sees(a, j, from, to);
+        if (t4 == 0) {
+            const float gk = a.kv.head_scale ? __ldg(a.kv.head_scale + w.h) : 1.f;
+            row_mul[g] = down * a.scale_log2 * gk;
+            row_from[g] = from;
+            row_to[g] = to;
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            from = max(from, __shfl_xor_sync(0xffffffffu, from, o));
+            to = min(to, __shfl_xor_sync(0xffffffffu, to, o));
+        }
+        if (lane == 0) {
+            all_seen[0] = from;
+            all_seen[1] = to;
+        }
+    };
+
+    {
+        W w;
+        w.start(a, plan, beg, end);
+        if (threadIdx.x == 0) walk[0] = w;
+    }
+    __syncthreads();
+    Run<T> raw_q[D / 32];
+    if (warp == 0) load_queries(walk[0], raw_q);
+    // Tile n of the CTA (over all its pieces) is copied by warp n % kWarps; a piece's
+    // first tile already while the last tile of the piece before it is worked on.
+    uint32_t tiles_before = 0;      // of the earlier pieces
+    uint32_t stage = 0, phase = 0;  // of the tile at work
+    int made = 0;                   // tiles of this piece that are on their way already
+    for (int piece = 0;; piece ^= 1) {
+        const int n_copy = walk[piece].count(), place0 = walk[piece].place0();
+        const int len = walk[piece].sq.len;
+        int next = (warp - (int)tiles_before) & (kWarps - 1);   // the warp's next tile to copy
+        if (next < made) next += kWarps;
+        int next_page[kRuns];
+        auto fetch_next = [&]() {
+            fetch(next < n_copy, walk[piece].b, place0 + next * kTile, len, next_page);
         };
-        auto produce = [&](int i, const int (&raw)[kRuns]) {    // one warp
-            int page[kRuns];
-#pragma unroll
-            for (int k = 0; k < kRuns; ++k) page[k] = a.kv.page_checked(raw[k], a.err);
-            const uint32_t n = tiles_before + i, stage = n % kStages;
-            if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
-            uint32_t runs = 0;
-#pragma unroll
-            for (int k = 0; k < kRuns; ++k)
-                runs += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && lane_part == 0));
-            if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < kRuns; ++k) {
-                if (page[k] < 0) continue;
-                const int psz = a.kv.page_size(), in_tile = (lane_run + 8 * k) * run;
-                const int at = (place0 + i * kTile + in_tile) & (psz - 1);
-                const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + at * row_bytes +
-                                     (lane_part == 0   ? 0
-                                      : lane_part == 1 ? v_code_at(psz, D, 0)
-                                      : lane_part == 2 ? k_scale_at(psz, D, 0)
-                                                       : v_scale_at(psz, D, 0));
-                bulk_load(ring_at + stage * Sh::kStage + lane_dst + in_tile * row_bytes, src,
-                          run * row_bytes, full + stage);
-            }
-        };
-        int next = warp, next_page[kRuns];        // the warp's next tile to copy, and its pages
-        fetch(next, next_page);
-        if (next < min(Sh::kLead, n_copy)) {
-            produce(next, next_page);
+        auto produce_next = [&]() {
+            produce(tiles_before + next, place0 + next * kTile, walk[piece].h, next_page);
             next += kWarps;
-            fetch(next, next_page);
-        }
-
-        // Queries: warp nt, the lane's part of row 8 nt + g, as the B operand, scaled by
-        // a power of two that brings the row's largest number to [2^13, 2^14).
-        const float gk = a.kv.head_scale ? __ldg(a.kv.head_scale + h) : 1.f;
-        const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
-        if (warp < NT) {
-            const int mine = 8 * warp + g, r = row0 + mine;
-            const bool there = mine < rows;
-            const int j = there ? r / a.G : 0;
-            const T *p = static_cast<const T *>(a.q) + (sq.first + j) * a.q_tok +
-                         (long long)(h * a.G + (there ? r - j * a.G : 0)) * a.q_head + t4 * (D / 4);
-            float x[D / 4];
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float v[8];
-                if (there) load8(p + 8 * i, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[8 * i + e] = there ? v[e] : 0.f;
-                    m = fmaxf(m, fabsf(x[8 * i + e]));
-                }
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            float down;
-            const float up = row_up(m, down);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u = x[8 * k + 2 * e] * up, v = x[8 * k + 2 * e + 1] * up;
-                    hi[e] = pack_f16(u, v);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
-                    lo[e] = pack_f16(u - f.x, v - f.y);
-                }
-                uint4 *q = queries + (warp * (D / 32) + k) * 32 + lane;
-                q[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if constexpr (kSplit) q[NT * (D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-            int from = 0, to = sq.len;
-            if (there) sq.sees(a, j, from, to);
-            if (t4 == 0) {
-                row_mul[mine] = down * a.scale_log2 * gk;
-                row_from[mine] = from;
-                row_to[mine] = to;
-            }
-            if (NT == 1) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    from = max(from, __shfl_xor_sync(0xffffffffu, from, o));
-                    to = min(to, __shfl_xor_sync(0xffffffffu, to, o));
-                }
-                if (lane == 0) {
-                    all_seen[0] = from;
-                    all_seen[1] = to;
-                }
-            }
-        }
+            fetch_next();
+        };
+        fetch_next();
+        if (next < min(Sh::kLead, n_copy)) produce_next();
+        if (warp == 0) put_queries(walk[piece], raw_q);
         __syncthreads();
-        if (NT > 1) {
-            if (threadIdx.x == 0) {
-                int from = 0, to = sq.len;
-                for (int r = 0; r < kRows; ++r) {
-                    from = max(from, row_from[r]);
-                    to = min(to, row_to[r]);
-                }
-                all_seen[0] = from;
-                all_seen[1] = to;
-            }
-            __syncthreads();
-        }
         const int all_from = all_seen[0], all_to = all_seen[1];   // places that every row sees
-        float mul[NT][2];
-        float o[NT][kT][4], sub[NT][2], sum[NT][2];   // sub: what scores lose before ex2
+        float mul[2], o[kT][4], sub[2], sum[2];   // sub: what scores lose before ex2
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int i = 0; i < kT; ++i)
 #pragma unroll
-            for (int i = 0; i < kT; ++i)
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mul[nt][e] = row_mul[8 * nt + 2 * t4 + e];
-                sub[nt][e] = -INFINITY;
-                sum[nt][e] = 0.f;
-            }
+        for (int e = 0; e < 2; ++e) {
+            mul[e] = row_mul[2 * t4 + e];
+            sub[e] = -INFINITY;
+            sum[e] = 0.f;
         }
-
-        for (int i = 0; i < n_copy; ++i) {
-            if (next == i + Sh::kLead && next < n_copy) {
-                produce(next, next_page);
-                next += kWarps;
-                fetch(next, next_page);
+        // The first tile of the piece after this one, copied by warp `after`: its pages are
+        // looked up before this piece's last tile is worked on and copied behind it.
+        const int after = (tiles_before + n_copy) & (kWarps - 1);
+        auto look_after = [&]() {
+            W x = walk[piece];
+            const bool more = x.next(a);
+            if (lane == 0) {
+                walk[piece ^ 1] = x;
+                walk_more = more;
             }
-            const uint32_t n = tiles_before + i, stage = n % kStages;
-            const bool arrived = waits.on(full + stage, (n / kStages) & 1);
+            __syncwarp();
+            next = more && x.count() > 0 ? 0 : -1;
+            fetch(next == 0, x.b, x.place0(), x.sq.len, next_page);
+        };
+
+        // the iteration at which this warp copies or looks pages up next
+        auto due_at = [&]() {
+            return next < n_copy ? next - Sh::kLead : warp == after ? n_copy - 1 : n_copy;
+        };
+        int due = due_at();
+        for (int i = 0; i < n_copy; ++i) {
+            if (i == due) {
+                if (next < n_copy) produce_next();
+                if (i + 1 == n_copy && warp == after) look_after();
+                due = due_at();
+            }
+            const bool arrived = waits.on(full + stage, phase);
             const uint8_t *buf = smem + stage * Sh::kStage + warp * (kU * kGroup * D / 2);
             const uint8_t *sbuf =
                 smem + stage * Sh::kStage + Sh::kKScale + warp * (kU * kGroup * D / 16);
             int t0 = place0 + i * kTile + warp * (kU * kGroup);
 #pragma unroll 1
             for (int u = 0; u < kU; ++u, t0 += kGroup, buf += kGroup * D / 2, sbuf += kGroup * D / 16) {
-            if (!arrived || t0 >= sq.len) break;
-            const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
+                if (!arrived || t0 >= len) break;
+                const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
-            float s[NT][4];
-            scores<D, NT, kParts>(buf, sbuf, g, t4, queries + lane, s);
-            VShare<D> v;
-            v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
+                float s[4];
+                scores<D, kParts>(buf, sbuf, g, t4, queries + lane, s);
+                VShare<D> v;
+                v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
 
-            // Scores in log2 units less the row's `sub`, so that the row's largest number
-            // is about kLift.  One comparison finds those that call for more: above
-            // kLift + kRaise the maximum moves; below kLow probabilities lose bits.
-            float t[NT][4];
-            bool more = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                // Scores in log2 units less the row's `sub`, so that the row's largest number
+                // is about kLift.  One comparison finds those that call for more: above
+                // kLift + kRaise the maximum moves; below kLow probabilities lose bits.
+                float t[4];
+                bool more = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float &y = t[nt][e];
-                    y = fmaf(s[nt][e], mul[nt][e & 1], -sub[nt][e & 1]);
+                    t[e] = fmaf(s[e], mul[e & 1], -sub[e & 1]);
                     if (!whole) {
-                        const int at = t0 + place_of(g) + 8 * (e >> 1), r = 8 * nt + 2 * t4 + (e & 1);
-                        if (at < row_from[r] || at >= row_to[r]) y = -INFINITY;
+                        const int at = t0 + place_of(g) + 8 * (e >> 1), r = 2 * t4 + (e & 1);
+                        if (at < row_from[r] || at >= row_to[r]) t[e] = -INFINITY;
                     }
-                    more |= fabsf(y - kMid) > kHalf;
+                    more |= fabsf(t[e] - kMid) > kHalf;
                 }
-            const bool extra = __any_sync(0xffffffffu, more);
-            if (extra) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                const bool extra = __any_sync(0xffffffffu, more);
+                if (extra) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         // (+infinity in t is a row's first score: its own value decides)
                         float m = -INFINITY;
 #pragma unroll
                         for (int k = e; k < 4; k += 2)
-                            m = fmaxf(m, t[nt][k] == -INFINITY ? -INFINITY
-                                                               : s[nt][k] * mul[nt][e]);
+                            m = fmaxf(m, t[k] == -INFINITY ? -INFINITY : s[k] * mul[e]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                         m -= kLift;
-                        if (m > sub[nt][e] + kRaise) {
-                            const float f = ex2(sub[nt][e] - m);
-                            sub[nt][e] = m;
-                            sum[nt][e] *= f;
+                        if (m > sub[e] + kRaise) {
+                            const float f = ex2(sub[e] - m);
+                            sub[e] = m;
+                            sum[e] *= f;
 #pragma unroll
                             for (int k = 0; k < kT; ++k) {
-                                o[nt][k][e] *= f;
-                                o[nt][k][e + 2] *= f;
+                                o[k][e] *= f;
+                                o[k][e + 2] *= f;
                             }
                         }
 #pragma unroll
                         for (int k = e; k < 4; k += 2)
-                            if (t[nt][k] != -INFINITY)
-                                t[nt][k] = fmaf(s[nt][k], mul[nt][e], -sub[nt][e]);
+                            if (t[k] != -INFINITY) t[k] = fmaf(s[k], mul[e], -sub[e]);
                     }
-            }
+                }
 
-            uint32_t pf[kParts][NT][2];
-            float rest[NT][4];
-            bool low = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+                uint32_t pf[kParts][2];
+                float p[4], rest[4];
+                bool low = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(t[nt][e]);
-                    sum[nt][e & 1] += p[e];
+                    p[e] = ex2(t[e]);
+                    sum[e & 1] += p[e];
                 }
                 if (extra) {      // the small ones later, in a product of their own
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        rest[nt][e] = 0.f;
+                        rest[e] = 0.f;
                         if (p[e] < kLow) {
-                            rest[nt][e] = p[e];
+                            rest[e] = p[e];
                             p[e] = 0.f;
                         }
-                        low |= rest[nt][e] > 0.f;
+                        low |= rest[e] > 0.f;
                     }
                 }
-                operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
-            }
-            if (!whole) {
-                // Places behind the sequence's end may hold anything: their scales become 0.
-                // A NaN that some rows see and others do not would reach all of them through
-                // 0 * NaN: it is taken out of the product and put into the rows that see it.
-                constexpr int kBlocks = VShare<D>::kBlocks;
-                uint32_t nan[kBlocks] = {};
-                bool any = false;
+                operand_of<kSplit>(p, pf[0], pf[kParts - 1]);
+                if (!whole) {
+                    // Places behind the sequence's end may hold anything: their scales become 0.
+                    // A NaN that some rows see and others do not would reach all of them through
+                    // 0 * NaN: it is taken out of the product and put into the rows that see it.
+                    constexpr int kBlocks = VShare<D>::kBlocks;
+                    uint32_t nan[kBlocks] = {};
+                    bool any = false;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int off = v.place(j, t4);
-                    if (t0 + off >= sq.len) v.sb[j] = 0;
+                    for (int j = 0; j < 4; ++j) {
+                        const int off = v.place(j, t4);
+                        if (t0 + off >= len) v.sb[j] = 0;
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k)
-                        if (((v.sb[j] >> (8 * k)) & 0x7f) == 0x7f) {
-                            nan[k] |= 1u << off;
-                            any = true;
-                            v.sb[j] &= ~(0xffu << (8 * k));
-                        }
-                }
-                if (__any_sync(0xffffffffu, any)) {
+                        for (int k = 0; k < kBlocks; ++k)
+                            if (((v.sb[j] >> (8 * k)) & 0x7f) == 0x7f) {
+                                nan[k] |= 1u << off;
+                                any = true;
+                                v.sb[j] &= ~(0xffu << (8 * k));
+                            }
+                    }
+                    if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k) {
-                        nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 1);
-                        nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 2);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int k = 0; k < kBlocks; ++k) {
+                            nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 1);
+                            nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 2);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int r = 8 * nt + 2 * t4 + e;
+                                const int r = 2 * t4 + e;
                                 const int lo = min(16, max(0, row_from[r] - t0));
                                 const int hi = min(16, max(0, row_to[r] - t0));
                                 const uint32_t seen = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
                                 if (nan[k] & seen) {
 #pragma unroll
                                     for (int m = 0; m < kT / kBlocks; ++m) {
-                                        o[nt][k * (kT / kBlocks) + m][e] = NAN;
-                                        o[nt][k * (kT / kBlocks) + m][e + 2] = NAN;
+                                        o[k * (kT / kBlocks) + m][e] = NAN;
+                                        o[k * (kT / kBlocks) + m][e + 2] = NAN;
                                     }
                                 }
                             }
+                        }
                     }
                 }
-            }
-            product<D, NT, kParts, false>(v, pf, 1.f, o);
-            if (extra && __any_sync(0xffffffffu, low)) {
-                // what lies a factor kBand below the last product's range, until nothing is
-                // left
-                float factor = 1.f;
-                do {
-                    factor *= 1.f / kBand;
-                    low = false;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float p[4];
+                product<D, kParts, false>(v, pf, 1.f, o);
+                if (extra && __any_sync(0xffffffffu, low)) {
+                    // what lies a factor kBand below the last product's range, until nothing is
+                    // left
+                    float factor = 1.f;
+                    do {
+                        factor *= 1.f / kBand;
+                        low = false;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            rest[nt][e] *= kBand;
-                            p[e] = rest[nt][e] >= kLow ? rest[nt][e] : 0.f;
-                            if (p[e] > 0.f) rest[nt][e] = 0.f;
-                            low |= rest[nt][e] > 0.f;
+                            rest[e] *= kBand;
+                            p[e] = rest[e] >= kLow ? rest[e] : 0.f;
+                            if (p[e] > 0.f) rest[e] = 0.f;
+                            low |= rest[e] > 0.f;
                         }
-                        operand_of<kSplit>(p, pf[0][nt], pf[kParts - 1][nt]);
-                    }
-                    product<D, NT, kParts, true>(v, pf, factor, o);
-                } while (__any_sync(0xffffffffu, low));
-            }
+                        operand_of<kSplit>(p, pf[0], pf[kParts - 1]);
+                        product<D, kParts, true>(v, pf, factor, o);
+                    } while (__any_sync(0xffffffffu, low));
+                }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty + stage);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (warp == after) {
+            if (n_copy == 0) look_after();
+            if (next == 0)
+                produce(tiles_before + n_copy, walk[piece ^ 1].place0(), walk[piece ^ 1].h, next_page);
         }
         tiles_before += n_copy;
 
         // the warps' sums of this piece
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = sum[nt][e];
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) warp_ml[warp][8 * nt + 2 * t4 + e] = make_float2(sub[nt][e], x);
-            }
-        if (abort_flag && next >= kWarps && n_copy > 0) {
-            // a wait gave up: the last copy this warp issued is still waited for
-            const uint32_t n = tiles_before - n_copy + next - kWarps;
-            ptx::mbar_wait(full + n % kStages, (n / kStages) & 1, a.wait_limit);
+        for (int e = 0; e < 2; ++e) {
+            float x = sum[e];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (g == 0) warp_ml[warp][2 * t4 + e] = make_float2(sub[e], x);
         }
-        __syncthreads();              // every warp is done with the ring as well
-        float *merge = reinterpret_cast<float *>(smem);
+        __syncthreads();
+        const W &w = walk[piece];
+        const int h = w.h, row0 = w.row0(), rows = w.rows(a);
         const bool complete = w.complete();
         const long long slot = 2ll * blockIdx.x + (w.cur == beg ? 0 : 1);
         if (threadIdx.x == 0 && w.tile0 == 0 && !complete) {
             const long long end_tile = w.cur + w.n_tiles;
             const int last = (int)((end_tile * ctas - 1) / plan.total);   // CTA of its last tile
-            a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, row0, rows};
+            a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, w.sq.first, h, row0, rows};
         }
+        // The merge goes into the stage behind the one that the next piece's first tile may
+        // be on its way to: every warp is done with it, and it is filled again only in the
+        // next piece.
+        float *merge =
+            reinterpret_cast<float *>(smem + (tiles_before + 1) % kStages * Sh::kStage);
+        constexpr int kMr = Sh::kMergeRows;
+        const bool more = walk_more;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (8 * nt >= rows) break;
+        for (int half = 0; half < kRows / kMr; ++half) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 2 * t4 + e;
+                const int r = 2 * t4 + e - half * kMr;
+                if (r < 0 || r >= kMr) continue;
                 float m = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][8 * nt + r].x);
-                const float f = m == -INFINITY ? 1.f : ex2(sub[nt][e] - m);
-                float *p = merge + (warp * 8 + r) * D + g * (D / 8);
+                for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][2 * t4 + e].x);
+                const float f = m == -INFINITY ? 1.f : ex2(sub[e] - m);
+                float *p = merge + (warp * kMr + r) * D + g * (D / 8);
 #pragma unroll
                 for (int k = 0; k < kT; ++k)
                     *reinterpret_cast<float2 *>(p + 2 * k) =
-                        make_float2(o[nt][k][e] * f, o[nt][k][e + 2] * f);
+                        make_float2(o[k][e] * f, o[k][e + 2] * f);
             }
+            if (half == 0 && more && warp == 0) load_queries(walk[piece ^ 1], raw_q);
             __syncthreads();
-            for (int x = threadIdx.x; x < min(8, rows - 8 * nt) * (D / 4); x += kThreads) {
-                const int r8 = x / (D / 4), r = 8 * nt + r8, d = 4 * (x - r8 * (D / 4));
+            for (int x = threadIdx.x; x < min(kMr, rows - half * kMr) * (D / 4); x += kThreads) {
+                const int rm = x / (D / 4), r = half * kMr + rm, d = 4 * (x - rm * (D / 4));
                 float m = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][r].x);
@@ -673,30 +709,37 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     const float2 ml = warp_ml[k][r];
                     l += ml.y * (m == -INFINITY ? 1.f : ex2(ml.x - m));
                     const float4 y =
-                        *reinterpret_cast<const float4 *>(merge + (k * 8 + r8) * D + d);
+                        *reinterpret_cast<const float4 *>(merge + (k * kMr + rm) * D + d);
                     v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
                 }
                 if (complete) {
                     const int rr = row0 + r, j = rr / a.G, hq = h * a.G + rr - j * a.G;
+                    const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
                     const float inv = l == 0.f ? 0.f : gv / l;
-                    T *p = static_cast<T *>(a.o) + (sq.first + j) * a.o_tok + hq * a.o_head + d;
+                    T *p = static_cast<T *>(a.o) + (w.sq.first + j) * a.o_tok + hq * a.o_head + d;
                     store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                    if (a.lse && d == 0) a.lse[(long long)(sq.first + j) * a.Hq + hq] = lse_of(m, l);
+                    if (a.lse && d == 0) a.lse[(long long)(w.sq.first + j) * a.Hq + hq] = lse_of(m, l);
                 } else {
                     store4(a.part_o + (slot * kRows + r) * D + d, v.x, v.y, v.z, v.w);
                     if (d == 0) a.part_ml[slot * kRows + r] = make_float2(m, l);
                 }
             }
-            ptx::fence_proxy_async_smem();     // before copies go into the ring again
+            ptx::fence_proxy_async_smem();     // before copies go into that stage again
             __syncthreads();
         }
-    } while (w.next(a));
+        if (!more) break;
+        made = walk[piece ^ 1].count() > 0 ? 1 : 0;
+    }
+    if (abort_flag && last_made >= 0) {
+        // a wait gave up: the last copy this warp issued is still waited for
+        ptx::mbar_wait(full + last_made % kStages, (last_made / kStages) & 1, a.wait_limit);
+    }
 }
 
-template <typename T, int D, int NT, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
 gdn_status launch(AttnArgs &a, cudaStream_t st) {
-    using Sh = Shape<D, NT, kSplit, kU, kStages>;
-    auto kern = k_kv_attn<T, D, NT, kSplit, kU, kStages, kMinCtas>;
+    using Sh = Shape<D, kSplit, kU, kStages>;
+    auto kern = k_kv_attn<T, D, kSplit, kU, kStages, kMinCtas>;
     constexpr int kTile = Sh::kTile;
     static std::atomic<int> memo[kMaxDeviceMemo];
     // resident CTAs of the device, and the opt-in to the ring's shared memory
@@ -725,19 +768,21 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (cut) {
-        if (e == cudaSuccess) e = launch_join<T, D, Sh::kRows, kJoinWarps>(a, grid, st);
+        if (e == cudaSuccess) e = launch_join<T, D, Sh::kRows, kWarps, kWarps>(a, grid, st);
         const cudaError_t f = scratch_free(scratch, st);
         if (e == cudaSuccess) e = f;
     }
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// By the head's width alone: registers hold d / 4 sums a lane, and a stage has to
+// hold the merge of the warps' sums.
 template <typename T, bool kSplit>
 gdn_status pick(AttnArgs &a, cudaStream_t st) {
     switch (a.kv.d) {
-        case 64: return launch<T, 64, 1, kSplit, KU, KS, kSplit ? 1 : 2>(a, st);
-        case 128: return launch<T, 128, 1, kSplit, KU, KS, kSplit ? 1 : 2>(a, st);
-        default: return launch<T, 256, 1, kSplit, 1, 4, 1>(a, st);
+        case 64: return launch<T, 64, kSplit, 2, 3, kSplit ? 1 : 2>(a, st);
+        case 128: return launch<T, 128, kSplit, 2, 3, kSplit ? 1 : 2>(a, st);
+        default: return launch<T, 256, kSplit, 1, 4, 1>(a, st);
     }
 }
 

@@ -252,15 +252,14 @@ __device__ __forceinline__ float lse_of(float sub, float sum) {
     return sum == 0.f ? -INFINITY : (sub + log2f(sum)) * 0.69314718055994531f;
 }
 
-// Adds the pieces of what was cut, in order.  CTA (i, y): kJoinWarps / kStripes
-// rows of the one whose first piece CTA i of the attention kernel had; kStripes
+// Adds the pieces of what was cut, in order.  CTA (i, y): kJoin / kStripes rows of
+// the one whose first piece CTA i of the attention kernel had; kStripes of its kJoin
 // warps share a row's pieces (many pieces of few rows, or the other way round).
-constexpr int kJoinWarps = 4;
-template <typename T, int D, int kRows, int kStripes>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
-    constexpr int kVec = D / 32, kCtaRows = kJoinWarps / kStripes;
-    __shared__ float sums[kJoinWarps][D];
-    __shared__ float2 warp_ml[kJoinWarps];
+template <typename T, int D, int kRows, int kJoin, int kStripes>
+__global__ void __launch_bounds__(kJoin * 32) k_kv_join(const AttnArgs a) {
+    constexpr int kVec = D / 32, kCtaRows = kJoin / kStripes;
+    __shared__ float sums[kJoin][D];
+    __shared__ float2 warp_ml[kJoin];
     ptx::griddep_wait();
     const Cut c = a.cuts[blockIdx.x];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const AttnArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float v[kVec] = {}, l = 0.f;
-#pragma unroll 4
+#pragma unroll 5
     for (int k = stripe; k < c.pieces; k += kStripes) {
         const float2 ml = a.part_ml[slot(k)];
         const float f = m == -INFINITY ? 1.f : ex2(ml.x - m);
@@ -327,22 +326,22 @@ inline cudaError_t alloc_pieces(AttnArgs &a, int grid, void **scratch, cudaStrea
     return cudaSuccess;
 }
 // The join after such a launch: started while that runs, it waits for its end.
-template <typename T, int D, int kRows, int kStripes>
+template <typename T, int D, int kRows, int kJoin, int kStripes>
 inline cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t st) {
     const long long most = (long long)a.max_new * a.G;
-    const int rows = (int)(most < kRows ? most : kRows), per = kJoinWarps / kStripes;
+    const int rows = (int)(most < kRows ? most : kRows), per = kJoin / kStripes;
     if (grid < 2 || rows < 1) return cudaSuccess;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid, (rows + per - 1) / per);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.blockDim = dim3(kJoin * 32);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, k_kv_join<T, D, kRows, kStripes>, a);
+    return cudaLaunchKernelEx(&cfg, k_kv_join<T, D, kRows, kJoin, kStripes>, a);
 }
 
 // Many rows (gdn_kv_attn_tc.cu): bf16 rows, d = 64 or 128.

@@ -649,7 +649,7 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     timer_end(slot, st);
     count_launch();
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D, kRows, 1>(a, grid, st);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D, kRows, 4, 1>(a, grid, st);
     const cudaError_t f = scratch_free(scratch, st);
     if (e == cudaSuccess) e = f;
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
