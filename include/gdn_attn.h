@@ -11,8 +11,9 @@
  * Rows.  q, k, v and o are rows of d contiguous elements, found by strides, so
  * [B][H][T][d], [B][T][H][d], [tokens][H][d] and [H][tokens][d] all pass as
  * they are.  The base pointers of rows, pages, cos and sin and the strides of rows
- * are multiples of 16 bytes, the int32 and fp32 arrays' of 4 (GDN_ERR_ALIGNMENT).  Query head i reads key/value head i / (Hq / H): Hq is a
- * multiple of the cache's head count (GDN_ERR_INVALID_ARG).
+ * are multiples of 16 bytes, the int32 and fp32 arrays' of 4 (GDN_ERR_ALIGNMENT).
+ * Query head i reads key/value head i / (Hq / H): Hq is a multiple of the cache's
+ * head count (GDN_ERR_INVALID_ARG).
  *
  * Tokens.  The cache entry points work on the last tokens of N sequences,
  * packed in sequence order: sequence b has the tokens [cu_seqlens[b],
@@ -140,9 +141,10 @@ gdn_status gdn_kv_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, g
  *             from which the launch is planned (a larger device value is
  *             reported as GDN_ERR_INVALID_ARG by gdn_sync_check()).
  * The cache's numbers enter the tensor cores exactly (e2m1 * e4m3 fits fp16);
- * with bf16 rows the probabilities are rounded to fp16, with fp32 rows queries
- * and probabilities are carried as two fp16 numbers each.  Sums, maxima and
- * outputs are fp32 until o is rounded.  Scratch for splitting long sequences
+ * with bf16 rows the probabilities are rounded to fp16 (11 bits, down to 2^-22
+ * of the row's largest at least), with fp32 rows queries and probabilities are
+ * carried as two fp16 numbers each.  Sums, maxima and outputs are fp32 until o
+ * is rounded.  Scratch for splitting long sequences
  * comes from the library's pool.  The same inputs give the same bits.
  */
 enum { GDN_ATTN_CAUSAL = 1 };
