@@ -51,7 +51,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
 // Rows of a key/value head above which the products go to tcgen05 (gdn_kv_attn_tc.cu),
-// whose time does not depend on them up to 128: there 490 us for 64 ragged sequences, here
+// whose time does not depend on them up to 128: there 493 us for 64 ragged sequences, here
 // 165 for every 8 rows (one pass more over the cache), so 330 for 16 and 495 for 24.
 constexpr int kMany = 16;
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves

@@ -16,15 +16,24 @@
 //                    QK of the next tile's follow.
 // The products bound it (2 x 2 x 128^3 multiply-adds a tile at d = 128), and next
 // to them the exponentials; turning a tile into fp16 costs 1/4 of that time in
-// issue slots because 256 rows share it.
+// issue slots because 256 rows share it.  Fetching instructions is what a role
+// waits for most, so what runs once a tile is kept short: one copy of the
+// softmax's code, masks written into the scores before it, issuing loops rolled.
 //
 // e2m1 * e4m3 is exact in fp16, queries are scaled by a power of two per row, and
 // probabilities are fp16 numbers.  `sub` is set so that the first scores' maximum
 // is 2^kLift; it moves only when a tile's sum passes 2^15, which any number near
 // fp16's end brings about, so no maximum is taken otherwise.  A weight keeps its
-// 11 bits down to 2^-22 of the row's largest.
-#include <type_traits>
-
+// 11 bits down to 2^-22 of the row's largest.  Sums are fp32.
+//
+// Measured, join included (bf16, d = 128, 16 query and 4 key/value heads): chunks of
+// 2048 tokens over 12001 to 16384, two sequences: 374 us, 1.17 PFLOP/s (61 % of a
+// dense bf16 product's rate; 3300 cycles a tile where its products alone take
+// 2560: scores by halves, n = 64, take 48 cycles a product instead of 32, but
+// let products and softmax overlap: with whole tiles 10 % more).  Drafts of 5
+// tokens in a window of 4096, 16 sequences: 35 us, in 20 rows of the 256: a tile takes
+// 3000 to 3500 cycles there too, bound by the chain from scores to probabilities to
+// the next scores.
 #include "gdn_kv_attn.cuh"
 
 namespace gdn {
@@ -142,6 +151,9 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 // One token's codes and scales of K or V of a head, in registers.
 template <int D>
 struct Token {
@@ -307,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     __shared__ uint64_t bar[B_COUNT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    // NaN blocks of V of the last four tiles' tokens (a tile's are read before the
-    // fourth next is converted), and whether a warp found any
+    // NaN blocks of V of the last four tiles' tokens, and whether a warp found any.  A
+    // tile's are read before the scores of the second next are used, so before the
+    // values of the fourth next may be converted.
     __shared__ uint8_t nan_of[4][kTile];
     __shared__ uint32_t nan_any[4][4];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -387,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         const float up = row_up(most, down);
                         mul = down * a.scale_log2 *
                               (a.kv.head_scale ? __ldg(a.kv.head_scale + h) : 1.f);
+                        // (so that -infinity stays what it is; scores are below 2^40)
+                        if (mul == 0.f) mul = 0x1p-126f;
 #pragma unroll 4
                         for (int i = 0; i < D / 8; ++i) {
                             const uint4 x = piece(i);
@@ -399,10 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                             st_shared16(chunk_at(tile_q, row, i), y[0], y[1], y[2], y[3]);
                         }
                     }
+                    const uint32_t hidden = __float_as_uint(mul < 0.f ? INFINITY : -INFINITY);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_Q_FULL + m);
 
+                    // NaN blocks of V of the piece's tile i, known when a product with it is done
+                    auto see_nan = [&](int i) {
+                        const uint32_t *any = nan_any[(all + i) & 3];
+                        if ((any[0] | any[1] | any[2] | any[3]) == 0) return;
+                        const uint8_t *of = nan_of[(all + i) & 3];
+                        const int t0 = place0 + i * kTile;
+                        for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e) nan |= of[e];
+                    };
                     for (int i = 0; i < count; ++i, ++done) {
                         const int t0 = place0 + i * kTile;
                         // (every lane of a warp takes part in what follows, whatever it sees)
@@ -414,68 +438,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                             const uint32_t tH = tS + half * kHalf;
                             const bool ok = waits.on(bar + B_S_FULL + 2 * m + half, done & 1);
                             tc_fence_after();
-                            const uint32_t *any = nan_any[(all + i) & 3];
-                            if (half == 0 && ok && (any[0] | any[1] | any[2] | any[3])) {
-                                const uint8_t *of = nan_of[(all + i) & 3];
-                                for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e)
-                                    nan |= of[e];
-                            }
+                            if (half == 0 && i > 0) see_nan(i - 1);
                             uint32_t pk[kHalf / 2];
                             float part = 0.f;
-                            auto numbers = [&](auto masked) {
-                                const uint64_t mul2 = pack64(mul, mul), sub2 = pack64(-sub, -sub);
-                                uint64_t p2[2] = {};
-                                uint32_t x[2][32];
-                                tmem_ld32(tH, x[0]);
-                                tmem_ld32(tH + 32, x[1]);
-                                tmem_wait32(x[0]);
-                                tmem_wait32(x[1]);
-#pragma unroll
-                                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 2) {
-                                        const uint64_t t2 =
-                                            fma_f32x2(pack64(x[c][e], x[c][e + 1]), mul2, sub2);
-                                        float t[2];
-                                        unpack64(t2, t[0], t[1]);
-                                        if constexpr (masked.value) {
-                                            const int at = h0 + 32 * c + e;
-                                            if (at < from || at >= to) t[0] = -INFINITY;
-                                            if (at + 1 < from || at + 1 >= to) t[1] = -INFINITY;
-                                        }
-                                        t[0] = ex2(t[0]);
-                                        t[1] = ex2(t[1]);
-                                        p2[(e >> 1) & 1] =
-                                            add_f32x2(p2[(e >> 1) & 1], pack64(t[0], t[1]));
-                                        pk[16 * c + e / 2] = pack_f16(t[0], t[1]);
-                                    }
-                                float y[4];
-                                unpack64(p2[0], y[0], y[1]);
-                                unpack64(p2[1], y[2], y[3]);
-                                part = (y[0] + y[1]) + (y[2] + y[3]);
-                            };
-                            auto probabilities = [&]() {
-                                if (whole) numbers(std::false_type{});
-                                else numbers(std::true_type{});
-                            };
                             if (ok) {
-                                if (__all_sync(0xffffffffu, started)) probabilities();
-                                else part = INFINITY;
-                                const bool move = !started || part > kMostSum;
-                                if (__any_sync(0xffffffffu, move)) {
-                                    // the row's maximum of these scores, and `sub` by it
-                                    float top = -INFINITY;
+                                if (!whole) {
+                                    // what the row does not see becomes a score of -infinity
 #pragma unroll 1
                                     for (int c = 0; c < kHalf; c += 32) {
                                         uint32_t x[32];
                                         tmem_ld32(tH + c, x);
                                         tmem_wait32(x);
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e) {
-                                            const int at = h0 + c + e;
-                                            const float y = __uint_as_float(x[e]) * mul;
-                                            if (at >= from && at < to) top = fmaxf(top, y);
+                                        for (int e = 0; e < 32; ++e)
+                                            if (h0 + c + e < from || h0 + c + e >= to) x[e] = hidden;
+                                        tmem_st32(tH + c, x);
+                                    }
+                                    tmem_st_wait();
+                                }
+                                // A second pass where `sub` had to move: one copy of this code, as
+                                // fetching instructions is what waits otherwise.
+#pragma unroll 1
+                                for (int pass = 0;; ++pass) {
+                                    const uint64_t mul2 = pack64(mul, mul), sub2 = pack64(-sub, -sub);
+                                    uint64_t p2[2] = {};
+                                    uint32_t x[2][32];
+                                    tmem_ld32(tH, x[0]);
+                                    tmem_wait32(x[0]);
+                                    tmem_ld32(tH + 32, x[1]);
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) {
+                                        if (c == 1) tmem_wait32(x[1]);
+#pragma unroll
+                                        for (int e = 0; e < 32; e += 2) {
+                                            float t[2];
+                                            unpack64(fma_f32x2(pack64(x[c][e], x[c][e + 1]), mul2,
+                                                               sub2), t[0], t[1]);
+                                            t[0] = ex2(t[0]);
+                                            t[1] = ex2(t[1]);
+                                            p2[(e >> 1) & 1] =
+                                                add_f32x2(p2[(e >> 1) & 1], pack64(t[0], t[1]));
+                                            pk[16 * c + e / 2] = pack_f16(t[0], t[1]);
                                         }
+                                    }
+                                    float y[4];
+                                    unpack64(p2[0], y[0], y[1]);
+                                    unpack64(p2[1], y[2], y[3]);
+                                    part = (y[0] + y[1]) + (y[2] + y[3]);
+                                    const bool move = pass == 0 && (!started || part > kMostSum);
+                                    if (!__any_sync(0xffffffffu, move)) break;
+
+                                    // the row's maximum of these scores, and `sub` by it
+                                    float top = -INFINITY;
+#pragma unroll 1
+                                    for (int c = 0; c < kHalf; c += 32) {
+                                        uint32_t z[32];
+                                        tmem_ld32(tH + c, z);
+                                        tmem_wait32(z);
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e)
+                                            top = fmaxf(top, __uint_as_float(z[e]) * mul);
                                     }
                                     float f = 1.f;
                                     if (move && top > -INFINITY) {
@@ -496,17 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                                         tc_fence_after();
 #pragma unroll 1
                                         for (int c = 0; c < D; c += 32) {
-                                            uint32_t x[32];
-                                            tmem_ld32(tO + c, x);
-                                            tmem_wait32(x);
+                                            uint32_t z[32];
+                                            tmem_ld32(tO + c, z);
+                                            tmem_wait32(z);
 #pragma unroll
                                             for (int e = 0; e < 32; ++e)
-                                                x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                                            tmem_st32(tO + c, x);
+                                                z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
+                                            tmem_st32(tO + c, z);
                                         }
                                         tmem_st_wait();
                                     }
-                                    probabilities();
                                 }
                                 sum += part;
                                 tmem_st32(tH, pk);
@@ -519,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     }
                     waits.on(bar + B_O_FULL + 2 * m + 1, (done - 1) & 1);
                     tc_fence_after();
+                    see_nan(count - 1);
                 }
                 all += count;
 
@@ -587,25 +609,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
                            blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
                 };
-                int page = page_at(0), next_page = page_at(1);
+                // brings a token of a tile to come into L2: its lines from DRAM would take
+                // longer than the conversion of a tile
+                auto prefetch = [&](int i, int raw) {
+                    if ((unsigned)raw >= (unsigned)a.kv.n_pages) return;
+                    const int row = (place0 + i * kTile + tok) & (psz - 1);
+                    const uint8_t *blk = a.kv.pages + a.kv.block(raw, h);
+                    prefetch_l2(blk + k_code_at(psz, D, row));
+                    prefetch_l2(blk + v_code_at(psz, D, row));
+                    if ((tok & 15) == 0) {      // (a page has 16 tokens at least)
+                        prefetch_l2(blk + k_scale_at(psz, D, row));
+                        prefetch_l2(blk + v_scale_at(psz, D, row));
+                    }
+                };
+                int page = page_at(0), next_page = page_at(1), ahead[2] = {page_at(2), page_at(3)};
+                prefetch(1, next_page);
+                prefetch(2, ahead[0]);
                 load(k, 0, page, true);
                 load(v, 0, page, false);
                 for (int i = 0; i < count; ++i, ++n) {
                     const int buf = n & 1;
                     const uint32_t reuse = ((n >> 1) + 1) & 1;
-                    const uint32_t bad = v.take_nan();
                     const bool k_ok = n < 2 || waits.on(bar + B_K_FREE + buf, reuse);
-                    nan_of[n & 3][tok] = (uint8_t)bad;
-                    const uint32_t found = __ballot_sync(0xffffffffu, bad != 0);
-                    if (lane == 0) nan_any[n & 3][warp & 3] = found;
                     if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, tok);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_K_FULL + buf);
                     page = next_page;
-                    next_page = page_at(i + 2);
+                    next_page = ahead[0];
+                    ahead[0] = ahead[1];
+                    prefetch(i + 3, ahead[0]);
+                    ahead[1] = page_at(i + 4);
                     load(k, i + 1, page, true);
                     const bool v_ok = n < 2 || waits.on(bar + B_V_FREE + buf, reuse);
+                    const uint32_t bad = v.take_nan();
+                    nan_of[n & 3][tok] = (uint8_t)bad;
+                    const uint32_t found = __ballot_sync(0xffffffffu, bad != 0);
+                    if (lane == 0) nan_any[n & 3][warp & 3] = found;
                     if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, tok);
                     fence_proxy_async_smem();
                     __syncwarp();
