@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     const long long ctas = min((long long)gridDim.x, plan.total);
     if (a.cuts && threadIdx.x == 0) a.cuts[blockIdx.x].pieces = 0;
     if (blockIdx.x >= ctas) return;
-    const long long beg = plan.total * blockIdx.x / ctas, end = plan.total * (blockIdx.x + 1) / ctas;
+    const long long beg = quot(plan.total * blockIdx.x, ctas);
+    const long long end = quot(plan.total * (blockIdx.x + 1), ctas);
     const Waits waits{&abort_flag, a.err, a.wait_limit};
     const uint32_t ring_at = ptx::smem_u32(smem);
 
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         const long long slot = 2ll * blockIdx.x + (w.cur == beg ? 0 : 1);
         if (threadIdx.x == 0 && w.tile0 == 0 && !complete) {
             const long long end_tile = w.cur + w.n_tiles;
-            const int last = (int)((end_tile * ctas - 1) / plan.total);   // CTA of its last tile
+            const int last = (int)quot(end_tile * ctas - 1, plan.total);   // CTA of its last tile
             a.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, (int)slot, w.sq.first, h, row0, rows};
         }
         // The merge goes into the stage behind the one that the next piece's first tile may

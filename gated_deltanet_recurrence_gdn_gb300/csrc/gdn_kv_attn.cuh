@@ -35,6 +35,12 @@ struct Cut {
     int slot0, first, h, row0, rows;
 };
 
+// Quotients of counts, which seldom need 64 bits (a division in 64 takes about 500
+// cycles when its code is met for the first time).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // Tokens of one sequence and what its rows see.  Row r of a (sequence,
 // key/value head) is query head h G + r % G of new token r / G.
 struct Seq {
@@ -69,31 +75,47 @@ struct Plan {
     long long total;
 
     __device__ static __forceinline__ int row_tiles(const AttnArgs &a, const Seq &s) {
-        return (int)(((long long)s.n * a.G + kRows - 1) / kRows);
+        return (int)(((unsigned)s.n * (unsigned)a.G + kRows - 1) / kRows);   // (below 2^31 rows)
     }
     // Places [lo, lo + span) cover what any row of row tile rt sees; lo is rounded
     // down to a page or to 128, whichever is less.
     __device__ static __forceinline__ void range(const AttnArgs &a, const Seq &s, int rt, int &lo,
                                                  int &span) {
         int none, to;
-        s.sees(a, (int)((long long)rt * kRows / a.G), lo, none);
-        s.sees(a, min(s.n - 1, (int)(((long long)rt * kRows + kRows - 1) / a.G)), none, to);
+        const unsigned r0 = (unsigned)rt * kRows, G = a.G;
+        s.sees(a, (int)(r0 / G), lo, none);
+        s.sees(a, min(s.n - 1, (int)((r0 + kRows - 1) / G)), none, to);
         lo &= -min(a.kv.page_size(), 128);
         span = max(0, to - lo);
     }
     __device__ static __forceinline__ int tiles(int span) {
         return max(1, (span + kTile - 1) / kTile);
     }
-    // Tiles of one key/value head of the sequence.
-    __device__ static long long head_tiles(const AttnArgs &a, const Seq &s) {
-        const int n = row_tiles(a, s);
+    // Tiles of row tiles [r0, r1) of one key/value head of the sequence.
+    __device__ static __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s, int r0,
+                                                         int r1) {
         long long sum = 0;
-        for (int rt = 0; rt < n; ++rt) {
+        for (int rt = r0; rt < r1; ++rt) {
             int lo, span;
             range(a, s, rt, lo, span);
             sum += tiles(span);
         }
         return sum;
+    }
+    // The same of all row tiles by a warp, a run of `per` of them a lane: the sum up to
+    // and with this lane's in `upto`.
+    __device__ static __forceinline__ long long tiles_by_lane(const AttnArgs &a, const Seq &s,
+                                                              int &per, long long &upto) {
+        const int n = row_tiles(a, s), lane = threadIdx.x & 31;
+        per = (n + 31) / 32;
+        const long long own = tiles_of(a, s, min(n, lane * per), min(n, lane * per + per));
+        upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        return own;
     }
     // Whole CTA; `this` in shared memory.
     __device__ void build(const AttnArgs &a) {
@@ -101,12 +123,23 @@ struct Plan {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int share = (a.kv.N + kThreads - 1) / kThreads;
         long long mine = 0;
-        for (int i = 0; i < share; ++i) {
-            const int b = threadIdx.x * share + i;
-            if (b < a.kv.N) {
-                Seq s;
+        Seq s;
+        if (a.kv.N <= kThreads / 32) {      // a warp a sequence: few may have many row tiles
+            if (warp < a.kv.N) {
+                int per;
+                long long upto;
+                s.get(a, warp);
+                tiles_by_lane(a, s, per, upto);
+                if (lane == 31) prefix[warp] = a.kv.H * upto;
+            }
+            __syncthreads();
+            if (threadIdx.x < a.kv.N) mine = prefix[threadIdx.x];
+        } else {
+            for (int i = 0; i < share; ++i) {
+                const int b = threadIdx.x * share + i;
+                if (b >= a.kv.N) break;
                 s.get(a, b);
-                mine += a.kv.H * head_tiles(a, s);
+                mine += a.kv.H * tiles_of(a, s, 0, row_tiles(a, s));
             }
         }
         long long x = mine;
@@ -154,6 +187,7 @@ struct Walk {
         tile0 = from;
         tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
     }
+    // By whole warps.
     __device__ void start(const AttnArgs &a, const P &plan, long long at, long long until) {
         cur = at;
         end = until;
@@ -164,17 +198,22 @@ struct Walk {
             else j = m;
         }
         b = i * ((a.kv.N + kThreads - 1) / kThreads);
-        long long left = at - plan.prefix[i], per_head;
+        long long left = at - plan.prefix[i], per_head, own, upto;
+        int per;
         for (;; ++b) {
             sq.get(a, b);
-            per_head = P::head_tiles(a, sq);
+            own = P::tiles_by_lane(a, sq, per, upto);
+            per_head = __shfl_sync(0xffffffffu, upto, 31);
             if (left < per_head * a.kv.H) break;
             left -= per_head * a.kv.H;
         }
-        h = (int)(left / per_head);
+        h = (int)quot(left, per_head);
         left -= h * per_head;
         n_rt = P::row_tiles(a, sq);
-        for (rt = 0;; ++rt) {
+        // the lane that has the tile, then the row tile
+        const int lane = __ffs(__ballot_sync(0xffffffffu, upto > left)) - 1;
+        left -= __shfl_sync(0xffffffffu, upto - own, lane);
+        for (rt = lane * per;; ++rt) {
             P::range(a, sq, rt, lo, span);
             const int n = P::tiles(span);
             if (left < n) break;

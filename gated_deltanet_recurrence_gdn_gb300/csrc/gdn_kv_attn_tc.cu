@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     const long long ctas = min((long long)gridDim.x, plan.total);
     if (a.cuts && tid == 0) a.cuts[blockIdx.x].pieces = 0;
     const Waits waits{&abort_flag, a.err, a.wait_limit};
-    const long long beg = plan.total * blockIdx.x / max(ctas, 1ll);
-    const long long end = plan.total * (blockIdx.x + 1) / max(ctas, 1ll);
+    const long long beg = quot(plan.total * blockIdx.x, max(ctas, 1ll));
+    const long long end = quot(plan.total * (blockIdx.x + 1), max(ctas, 1ll));
 
     if (blockIdx.x < ctas) {
         W w;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 const bool complete = w.complete();
                 const long long slot = 2ll * blockIdx.x + (w.cur == beg ? 0 : 1);
                 if (tid == 0 && w.tile0 == 0 && !complete) {
-                    const int last = (int)(((w.cur + w.n_tiles) * ctas - 1) / plan.total);
+                    const int last = (int)quot((w.cur + w.n_tiles) * ctas - 1, plan.total);
                     a.cuts[blockIdx.x] =
                         Cut{last - (int)blockIdx.x + 1, (int)slot, sq.first, h, w.row0(), rows};
                 }
