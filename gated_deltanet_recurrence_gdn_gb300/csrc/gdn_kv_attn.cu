@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         abort_flag = 0;
         ptx::fence_mbar_init();
     }
+    ptx::griddep_launch_dependents();   // (the join, which waits for this kernel's end)
     plan.build(a);                  // (its barriers cover the initialisation)
     const long long ctas = min((long long)gridDim.x, plan.total);
     if (a.cuts && threadIdx.x == 0) a.cuts[blockIdx.x].pieces = 0;

@@ -308,27 +308,48 @@ __global__ void __launch_bounds__(kJoin * 32) k_kv_join(const AttnArgs a) {
     auto slot = [&](int k) {
         return (k == 0 ? (long long)c.slot0 : 2ll * (blockIdx.x + k)) * kRows + r;
     };
+    // (a row's first pieces are on their way while its maximum is found)
+    constexpr int kFirst = 2;
+    struct Piece {
+        float2 ml;
+        float v[kVec];
+        __device__ __forceinline__ void load(const AttnArgs &a, long long at, int lane) {
+            const float *p = a.part_o + at * D + lane * kVec;
+            ml = a.part_ml[at];
+            if constexpr (kVec == 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(p);
+                v[0] = x.x; v[1] = x.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(p + e);
+                    v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
+                }
+            }
+        }
+    } first[kFirst];
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u)
+        if (stripe + u * kStripes < c.pieces) first[u].load(a, slot(stripe + u * kStripes), lane);
     float m = -INFINITY;
     for (int k = lane; k < c.pieces; k += 32) m = fmaxf(m, a.part_ml[slot(k)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float v[kVec] = {}, l = 0.f;
-#pragma unroll 5
-    for (int k = stripe; k < c.pieces; k += kStripes) {
-        const float2 ml = a.part_ml[slot(k)];
-        const float f = m == -INFINITY ? 1.f : ex2(ml.x - m);
-        const float *p = a.part_o + slot(k) * D + lane * kVec;
-        l += ml.y * f;
-        if constexpr (kVec == 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(p);
-            v[0] += x.x * f; v[1] += x.y * f;
-        } else {
+    auto add = [&](const Piece &x) {
+        const float f = m == -INFINITY ? 1.f : ex2(x.ml.x - m);
+        l += x.ml.y * f;
 #pragma unroll
-            for (int e = 0; e < kVec; e += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(p + e);
-                v[e] += x.x * f; v[e + 1] += x.y * f; v[e + 2] += x.z * f; v[e + 3] += x.w * f;
-            }
-        }
+        for (int e = 0; e < kVec; ++e) v[e] += x.v[e] * f;
+    };
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u)
+        if (stripe + u * kStripes < c.pieces) add(first[u]);
+#pragma unroll 4
+    for (int k = stripe + kFirst * kStripes; k < c.pieces; k += kStripes) {
+        Piece x;
+        x.load(a, slot(k), lane);
+        add(x);
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
