@@ -35,12 +35,12 @@
 //   adds them in a fixed order.
 //
 // Measured, join included (bf16, d = 128, one token a sequence, pages read cold):
-//   256 sequences of 8000 to 8192, 8 heads:    473 us, 5.0 TB/s (2.39 GB);
-//   64 ragged ones of 128 to 16384, 8 heads:   167 us, 4.0 TB/s (665 MB);
-//   one of 131072, 4 heads:                     35 us, 2.2 TB/s (75 MB).
+//   256 sequences of 8000 to 8192, 8 heads:    470 us, 5.1 TB/s (2.39 GB);
+//   64 ragged ones of 128 to 16384, 8 heads:   165 us, 4.0 TB/s (665 MB);
+//   one of 131072, 4 heads:                     33 us, 2.3 TB/s (75 MB).
 // Issue slots bound the first (about 340 instructions per 16 tokens and warp, 65 %
-// of the slots taken, DRAM at 74 %); the last one spends 10 us in starting up,
-// finding its pages and the join.
+// of the slots taken, DRAM at 75 %).  The last one's first copy starts 5 us in: the
+// division of the work 2, its place in it 2, the page numbers 1; the join takes 5.
 #include "gdn_kv_attn.cuh"
 
 namespace gdn {

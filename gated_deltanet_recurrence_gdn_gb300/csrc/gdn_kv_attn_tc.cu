@@ -27,11 +27,11 @@
 // 11 bits down to 2^-22 of the row's largest.  Sums are fp32.
 //
 // Measured, join included (bf16, d = 128, 16 query and 4 key/value heads): chunks of
-// 2048 tokens over 12001 to 16384, two sequences: 374 us, 1.17 PFLOP/s (61 % of a
+// 2048 tokens over 12001 to 16384, two sequences: 350 us, 1.25 PFLOP/s (65 % of a
 // dense bf16 product's rate; 3300 cycles a tile where its products alone take
 // 2560: scores by halves, n = 64, take 48 cycles a product instead of 32, but
 // let products and softmax overlap: with whole tiles 10 % more).  Drafts of 5
-// tokens in a window of 4096, 16 sequences: 35 us, in 20 rows of the 256: a tile takes
+// tokens in a window of 4096, 16 sequences: 33.5 us, in 20 rows of the 256: a tile takes
 // 3000 to 3500 cycles there too, bound by the chain from scores to probabilities to
 // the next scores.
 #include "gdn_kv_attn.cuh"

@@ -6,10 +6,10 @@
 // pairs (gdn_kv.cuh) of one token, keeps that unit's cosines and sines in
 // registers and walks over the heads, so the table is read once a token, not
 // once a row.  The next head's loads are issued before this one's stores; what
-// hides their latency is occupancy: four CTAs an SM with one head in flight took
-// 32.6 us at B4 T4096, 16 + 4 heads, d = 128 bf16 (168 MB, 76 % of the copy rate
-// with the launch in it) and 66.8 us at 371 MB (82 %); two CTAs with four heads
-// in flight 44 and 97 us.
+// hides their latency is occupancy: four CTAs an SM with one head in flight take
+// 29.9 us at B4 T4096, 16 + 4 heads, d = 128 bf16 (170 MB, 84 % of a copy's rate)
+// and 64.9 us at 371 MB (84 %); two CTAs with four heads in flight took 44 and
+// 97 us, five CTAs 35 and 72.  A few tokens take 2.7 us: the launch.
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -58,8 +58,9 @@ cudaError_t launch(const gdn_rows *q, const gdn_rows *qo, const gdn_rows *k, con
     const int Hq = q->heads, Hk = k ? k->heads : 0;
     const int n = B * Tn;
     const long long gx = ((long long)n + per - 1) / per;
-    // Few tokens: the heads are spread over CTAs until there are about 4 an SM.
-    const long long want = (152 * 4 + gx - 1) / gx;
+    // Few tokens: the heads are spread over CTAs until there are 3 an SM (4096 tokens of 64
+    // + 16 heads 30.2 us; at 4 an SM, a full wave before the tail, 36.5, at 2 32.5).
+    const long long want = (152 * 3 + gx - 1) / gx;
     const int split = (int)(want < Hq + Hk ? want : Hq + Hk);
     const int heads_per = (Hq + Hk + split - 1) / split;
     const int gy = (Hq + Hk + heads_per - 1) / heads_per;
