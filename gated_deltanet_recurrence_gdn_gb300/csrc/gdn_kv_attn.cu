@@ -54,6 +54,7 @@ constexpr int kGroup = 16;                    // tokens of a warp's step
 // whose time does not depend on them up to 128: there 493 us for 64 ragged sequences, here
 // 165 for every 8 rows (one pass more over the cache), so 330 for 16 and 495 for 24.
 constexpr int kMany = 16;
+constexpr int kQueryWarp = 4;                 // (the first tile is copied by warp 0)
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         }
     };
 
-    // Queries of a piece, by warp 0: the lane's part of row g, loaded ...
+    // Queries of a piece, by one warp: the lane's part of row g, loaded ...
     auto row_of = [&](const W &w, bool &there, int &j) {
         const int r = w.row0() + g;
         there = g < w.rows(a);
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     }
     __syncthreads();
     Run<T> raw_q[D / 32];
-    if (warp == 0) load_queries(walk[0], raw_q);
+    if (warp == kQueryWarp) load_queries(walk[0], raw_q);
     // Tile n of the CTA (over all its pieces) is copied by warp n % kWarps; a piece's
     // first tile already while the last tile of the piece before it is worked on.
     uint32_t tiles_before = 0;      // of the earlier pieces
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         };
         fetch_next();
         if (next < min(Sh::kLead, n_copy)) produce_next();
-        if (warp == 0) put_queries(walk[piece], raw_q);
+        if (warp == kQueryWarp) put_queries(walk[piece], raw_q);
         __syncthreads();
         const int all_from = all_seen[0], all_to = all_seen[1];   // places that every row sees
         float mul[2], o[kT][4], sub[2], sum[2];   // sub: what scores lose before ex2
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     *reinterpret_cast<float2 *>(p + 2 * k) =
                         make_float2(o[k][e] * f, o[k][e + 2] * f);
             }
-            if (half == 0 && more && warp == 0) load_queries(walk[piece ^ 1], raw_q);
+            if (half == 0 && more && warp == kQueryWarp) load_queries(walk[piece ^ 1], raw_q);
             __syncthreads();
             for (int x = threadIdx.x; x < min(kMr, rows - half * kMr) * (D / 4); x += kThreads) {
                 const int rm = x / (D / 4), r = half * kMr + rm, d = 4 * (x - rm * (D / 4));

@@ -38,7 +38,8 @@ struct Cut {
 // Quotients of counts, which seldom need 64 bits (a division in 64 takes about 500
 // cycles when its code is met for the first time).
 __device__ __forceinline__ long long quot(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+    if (__builtin_expect((a | b) >> 32 != 0, 0)) return a / b;
+    return (unsigned)a / (unsigned)b;
 }
 
 // Tokens of one sequence and what its rows see.  Row r of a (sequence,
@@ -108,6 +109,10 @@ struct Plan {
                                                               int &per, long long &upto) {
         const int n = row_tiles(a, s), lane = threadIdx.x & 31;
         per = (n + 31) / 32;
+        if (n <= 1) {
+            upto = tiles_of(a, s, 0, n);
+            return lane == 0 ? upto : 0;
+        }
         const long long own = tiles_of(a, s, min(n, lane * per), min(n, lane * per + per));
         upto = own;
 #pragma unroll
