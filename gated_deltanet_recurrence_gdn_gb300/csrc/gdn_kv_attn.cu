@@ -54,7 +54,7 @@ constexpr int kGroup = 16;                    // tokens of a warp's step
 // whose time does not depend on them up to 128: there 493 us for 64 ragged sequences, here
 // 165 for every 8 rows (one pass more over the cache), so 330 for 16 and 495 for 24.
 constexpr int kMany = 16;
-constexpr int kQueryWarp = 4;                 // (the first tile is copied by warp 0)
+constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     __shared__ int abort_flag;
     __shared__ float2 warp_ml[kWarps][kRows];
     __shared__ float row_mul[kRows];
-    __shared__ W walk[2];           // the piece at work and the one after it
-    __shared__ bool walk_more;      // there is one
+    __shared__ W walk[3];           // the piece at work and the two after it, in a ring
+    __shared__ bool walk_more[3];   // whether there is one behind each
     __shared__ int row_from[kRows], row_to[kRows], all_seen[2];
     uint4 *queries = reinterpret_cast<uint4 *>(smem + Sh::kRing);
 
@@ -435,6 +435,16 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         }
     };
 
+    // the piece behind that of `at`, into `to` (one warp)
+    auto walk_on = [&](int at, int to) {
+        W x = walk[at];
+        const bool more = x.next(a);
+        __syncwarp();
+        if (lane == 0) {
+            walk[to] = x;
+            walk_more[at] = more;
+        }
+    };
     {
         W w;
         w.start(a, plan, beg, end);
@@ -442,13 +452,18 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     }
     __syncthreads();
     Run<T> raw_q[D / 32];
-    if (warp == kQueryWarp) load_queries(walk[0], raw_q);
+    if (warp == kQueryWarp) {
+        load_queries(walk[0], raw_q);
+        put_queries(walk[0], raw_q);
+    } else if (warp == kWalkWarp) {
+        walk_on(0, 1);
+    }
     // Tile n of the CTA (over all its pieces) is copied by warp n % kWarps; a piece's
     // first tile already while the last tile of the piece before it is worked on.
     uint32_t tiles_before = 0;      // of the earlier pieces
     uint32_t stage = 0, phase = 0;  // of the tile at work
     int made = 0;                   // tiles of this piece that are on their way already
-    for (int piece = 0;; piece ^= 1) {
+    for (int piece = 0, after_piece = 1;;) {
         const int n_copy = walk[piece].count(), place0 = walk[piece].place0();
         const int len = walk[piece].sq.len;
         int next = (warp - (int)tiles_before) & (kWarps - 1);   // the warp's next tile to copy
@@ -464,8 +479,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         };
         fetch_next();
         if (next < min(Sh::kLead, n_copy)) produce_next();
-        if (warp == kQueryWarp) put_queries(walk[piece], raw_q);
-        __syncthreads();
+        if (tiles_before == 0) __syncthreads();     // (later ones: with the merge's last)
         const int all_from = all_seen[0], all_to = all_seen[1];   // places that every row sees
         float mul[2], o[kT][4], sub[2], sum[2];   // sub: what scores lose before ex2
 #pragma unroll
@@ -482,17 +496,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         // looked up before this piece's last tile is worked on and copied behind it.
         const int after = (tiles_before + n_copy) & (kWarps - 1);
         auto look_after = [&]() {
-            W x = walk[piece];
-            const bool more = x.next(a);
-            if (lane == 0) {
-                walk[piece ^ 1] = x;
-                walk_more = more;
-            }
-            __syncwarp();
-            next = more && x.count() > 0 ? 0 : -1;
+            const W &x = walk[after_piece];
+            next = walk_more[piece] && x.count() > 0 ? 0 : -1;
             fetch(next == 0, x.b, x.place0(), x.sq.len, next_page);
         };
-
         // the iteration at which this warp copies or looks pages up next
         auto due_at = [&]() {
             return next < n_copy ? next - Sh::kLead : warp == after ? n_copy - 1 : n_copy;
@@ -653,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         if (warp == after) {
             if (n_copy == 0) look_after();
             if (next == 0)
-                produce(tiles_before + n_copy, walk[piece ^ 1].place0(), walk[piece ^ 1].h, next_page);
+                produce(tiles_before + n_copy, walk[after_piece].place0(), walk[after_piece].h,
+                        next_page);
         }
         tiles_before += n_copy;
 
@@ -682,7 +690,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         float *merge =
             reinterpret_cast<float *>(smem + (tiles_before + 1) % kStages * Sh::kStage);
         constexpr int kMr = Sh::kMergeRows;
-        const bool more = walk_more;
+        const bool more = walk_more[piece];
+        // what the next piece starts with, by warps that have less of the merge to do
+        if (more && warp == kQueryWarp) load_queries(walk[after_piece], raw_q);
 #pragma unroll
         for (int half = 0; half < kRows / kMr; ++half) {
 #pragma unroll
@@ -699,8 +709,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     *reinterpret_cast<float2 *>(p + 2 * k) =
                         make_float2(o[k][e] * f, o[k][e + 2] * f);
             }
-            if (half == 0 && more && warp == kQueryWarp) load_queries(walk[piece ^ 1], raw_q);
             __syncthreads();
+            if (half == 0 && more) {
+                if (warp == kQueryWarp) put_queries(walk[after_piece], raw_q);
+                else if (warp == kWalkWarp) walk_on(after_piece, 3 - piece - after_piece);
+            }
             for (int x = threadIdx.x; x < min(kMr, rows - half * kMr) * (D / 4); x += kThreads) {
                 const int rm = x / (D / 4), r = half * kMr + rm, d = 4 * (x - rm * (D / 4));
                 float m = -INFINITY, l = 0.f;
@@ -731,7 +744,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             __syncthreads();
         }
         if (!more) break;
-        made = walk[piece ^ 1].count() > 0 ? 1 : 0;
+        made = walk[after_piece].count() > 0 ? 1 : 0;
+        const int third = 3 - piece - after_piece;
+        piece = after_piece;
+        after_piece = third;
     }
     if (abort_flag && last_made >= 0) {
         // a wait gave up: the last copy this warp issued is still waited for
