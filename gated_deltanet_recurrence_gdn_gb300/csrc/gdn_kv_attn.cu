@@ -9,9 +9,10 @@
 // - A tile (256 tokens; 128 at d = 256) is copied into a ring of shared memory by
 //   bulk copies, one per page and part of it, each warp issuing every eighth
 //   tile's; a warp takes its 16 or 32 tokens of every tile, and no barrier joins
-//   the warps until a piece of work ends.  The next piece's first tile and its
-//   place in the work are fetched with the last tile of the piece before it
-//   (64 ragged sequences below: 178 us without that).
+//   the warps until a piece of work ends.  The next piece's first tile is copied
+//   with the last tile of the piece before it, and its queries and the place of
+//   the piece after it are found while that one's sums are merged (64 ragged
+//   sequences below: 178 us without either, 165 without the second).
 // - Tokens are the M side of the products: S^T[16 x 8] = K[16 x d] Q^T[d x 8],
 //   O^T[d x 8] += V^T[d x 16] P^T[16 x 8], so 8 query rows of a key/value head
 //   cost one n = 8 tile and a single row no more.
@@ -35,8 +36,8 @@
 //   adds them in a fixed order.
 //
 // Measured, join included (bf16, d = 128, one token a sequence, pages read cold):
-//   256 sequences of 8000 to 8192, 8 heads:    470 us, 5.1 TB/s (2.39 GB);
-//   64 ragged ones of 128 to 16384, 8 heads:   165 us, 4.0 TB/s (665 MB);
+//   256 sequences of 8000 to 8192, 8 heads:    469 us, 5.1 TB/s (2.39 GB);
+//   64 ragged ones of 128 to 16384, 8 heads:   162 us, 4.1 TB/s (665 MB);
 //   one of 131072, 4 heads:                     33 us, 2.3 TB/s (75 MB).
 // Issue slots bound the first (about 340 instructions per 16 tokens and warp, 65 %
 // of the slots taken, DRAM at 75 %).  The last one's first copy starts 5 us in: the
@@ -51,8 +52,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
 // Rows of a key/value head above which the products go to tcgen05 (gdn_kv_attn_tc.cu),
-// whose time does not depend on them up to 128: there 493 us for 64 ragged sequences, here
-// 165 for every 8 rows (one pass more over the cache), so 330 for 16 and 495 for 24.
+// whose time does not depend on them up to 128: there 480 us for 64 ragged sequences, here
+// 162 for every 8 rows (one pass more over the cache), so 324 for 16 and 486 for 24.
 constexpr int kMany = 16;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
