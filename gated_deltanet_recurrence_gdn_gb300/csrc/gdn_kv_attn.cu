@@ -52,8 +52,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
 // Rows of a key/value head above which the products go to tcgen05 (gdn_kv_attn_tc.cu),
-// whose time does not depend on them up to 128: there 480 us for 64 ragged sequences, here
-// 162 for every 8 rows (one pass more over the cache), so 324 for 16 and 486 for 24.
+// whose time hardly depends on them up to 128: 20 rows of 64 ragged sequences take 450 us
+// there and 478 in three passes of 8 rows here, in a window of 4096 places 38 and 44; up
+// to 16 rows take 325 here.  (Some hundred places: 17.5 there, 12.3 here.)
 constexpr int kMany = 16;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
