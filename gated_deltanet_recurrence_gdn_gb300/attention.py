@@ -49,6 +49,7 @@ _KV = struct.Struct("@PPPPPiiiiiii4xq")
 assert (_ROWS.size, _ROTARY.size, _KV.size) == tuple(map(ctypes.sizeof, (_Rows, _Rotary, _Kv)))
 
 _f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+_INT_MAX = 2 ** 31 - 1     # (larger bounds and windows mean the same)
 _axes_kept: dict = {}      # axis numbers by their value, as C arrays
 
 
@@ -289,7 +290,7 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
     if max_new is None:
         max_new = n if cu_seqlens is not None else n // max(kv_len.shape[0], 1)
     _call(load().gdn_kv_attn, "gdn_kv_attn", q, check, kv, _rows3("q", q, Hq, n, d, dtype),
-          _rows3("out", out, Hq, n, d, dtype), None if lse is None else lse.data_ptr(), max_len,
-          max_new, d ** -0.5 if scale is None else scale, window,
-          GDN_ATTN_CAUSAL if causal else 0, _DT[dtype])
+          _rows3("out", out, Hq, n, d, dtype), None if lse is None else lse.data_ptr(),
+          min(max_len, _INT_MAX), min(max_new, _INT_MAX), d ** -0.5 if scale is None else scale,
+          min(window, _INT_MAX), GDN_ATTN_CAUSAL if causal else 0, _DT[dtype])
     return (out, lse) if return_lse else out

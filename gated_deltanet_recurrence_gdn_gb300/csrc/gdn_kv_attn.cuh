@@ -55,11 +55,12 @@ struct Seq {
             if (n > a.max_new) n = 0;
         }
     }
-    // Places [from, to) that new token j sees.
+    // Places [from, to) that new token j sees.  (p may be far below 0 and the window as
+    // large as an int: their difference is formed only where it is not negative.)
     __device__ __forceinline__ void sees(const AttnArgs &a, int j, int &from, int &to) const {
         const int p = len - n + j;
         to = p < 0 ? 0 : a.causal ? p + 1 : len;
-        from = a.window > 0 ? max(0, p + 1 - a.window) : 0;
+        from = a.window > 0 && p >= a.window ? p + 1 - a.window : 0;
     }
 };
 
