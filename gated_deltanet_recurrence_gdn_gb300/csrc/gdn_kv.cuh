@@ -233,7 +233,8 @@ struct Kv {
         return page_checked(page_raw(b, p), err);
     }
     // Tokens [first, first + n) and length of sequence b.  Offsets or lengths
-    // out of range are recorded, and the sequence then counts as having none.
+    // out of range are recorded, and the sequence then counts as having none; so are
+    // offsets that do not begin at 0 or end at n_tokens (tokens of no sequence).
     __device__ __forceinline__ void tokens(int b, int &first, int &n, int &len, int *err) const {
         if (cu) {
             first = __ldg(cu + b);
@@ -249,6 +250,8 @@ struct Kv {
             atomicCAS(err, 0, kErrBadIndex);
             if (bad_n) n = first = 0;
             if (bad_len) len = 0;
+        } else if ((b == 0 && first != 0) || (b == N - 1 && first + n != n_tokens)) {
+            atomicCAS(err, 0, kErrBadIndex);
         }
     }
     // Sequence of packed token t: the last b with cu[b] <= t (empty sequences

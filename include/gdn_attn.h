@@ -5,8 +5,9 @@
  * statuses, dtypes, streams, scratch and error reporting as in gdn.h:
  * arguments are checked synchronously, work is enqueued on `stream`, errors
  * found by a kernel (a position outside its table, a page outside the pool, a
- * length outside its bound) are reported by gdn_sync_check() as
- * GDN_ERR_INVALID_ARG, and leave the rows concerned unspecified.
+ * length outside its bound, offsets that do not pack the tokens) are reported by
+ * gdn_sync_check() as GDN_ERR_INVALID_ARG, and leave the rows concerned
+ * unspecified.
  *
  * Rows.  q, k, v and o are rows of d contiguous elements, found by strides, so
  * [B][H][T][d], [B][T][H][d], [tokens][H][d] and [H][tokens][d] all pass as
@@ -17,7 +18,8 @@
  *
  * Tokens.  The cache entry points work on the last tokens of N sequences,
  * packed in sequence order: sequence b has the tokens [cu_seqlens[b],
- * cu_seqlens[b+1]), or, where cu_seqlens is NULL, n_tokens / N tokens each.
+ * cu_seqlens[b+1]), from cu_seqlens[0] = 0 to cu_seqlens[N] = n_tokens, or, where
+ * cu_seqlens is NULL, n_tokens / N tokens each.
  * kv_len[b] counts the sequence's tokens INCLUDING these n_b, so the j-th of
  * them lies at place kv_len[b] - n_b + j.  A token whose place is negative (an
  * idle slot of a batch: kv_len[b] = 0) is not written, reads back as zero, and
