@@ -88,6 +88,7 @@ ABI = [
     ("gdn_kv_append", _i, [_vp] * 6 + [_i, _vp]),
     ("gdn_kv_read", _i, [_vp] * 3 + [_i, _vp]),
     ("gdn_kv_attn", _i, [_vp] * 4 + [_i] * 2 + [ctypes.c_float, _i, ctypes.c_uint, _i, _vp]),
+    ("gdn_selftest_ring", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
     ("gdn_selftest_wait", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
 ]
 
@@ -447,6 +448,17 @@ def selftest_wait(complete: bool, limit: int, device=None):
         _check(load().gdn_selftest_wait(1 if complete else 0, int(limit), ok, _stream(device)),
                "gdn_selftest_wait")
     return bool(ok[0]), bool(ok[1])
+
+
+def selftest_ring(complete: bool, limit: int, device=None):
+    """The same for the warp-wide waits of the attention kernels over the cache
+    (gdn_selftest_ring): how many of 256 threads found the phase complete, in a
+    wait and in one more after it."""
+    out = (_i * 2)()
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(load().gdn_selftest_ring(1 if complete else 0, int(limit), out, _stream(device)),
+               "gdn_selftest_ring")
+    return tuple(out)
 
 
 class use_impl:

@@ -252,7 +252,21 @@ struct Waits {
     volatile int *abort;
     int *err;
     uint32_t limit;
+    // By a whole warp, all lanes of which learn the same: lanes poll the barrier and the
+    // CTA's flag one by one, so they vote.  What follows may be for the whole warp.
     __device__ __forceinline__ bool on(uint64_t *bar, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        for (uint32_t i = 0; i < limit; ++i) {
+            if (__any_sync(0xffffffffu, *abort != 0)) return false;
+            if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        }
+        *abort = 1;
+        atomicCAS(err, 0, kErrTimeout);
+        return false;
+    }
+    // A lane's own: lanes may learn different things when it gives up, so that nothing
+    // which the whole warp takes part in may depend on the result.
+    __device__ __forceinline__ bool on_lane(uint64_t *bar, uint32_t parity) const {
         if (ptx::mbar_try_wait(bar, parity)) return true;
         for (uint32_t i = 0; i < limit; ++i) {
             if (*abort) return false;

@@ -232,7 +232,7 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
     const uint64_t dV = make_sdesc(base + L::OFF_V, 16384, 1024, kSwizzle128B);
     const uint32_t tS = tmem + L::TM_S + 128 * m, tO = tmem + L::TM_O + 128 * m;
     uint32_t n = 0, done = 0, pieces = 0;
-    bool alive = true;
+    bool alive = true;            // (a lane's: only the elected one's counts)
     // Q K^T with half of the token tile in `buf`; the second half's frees the keys
     auto scores = [&](int half, int buf) {
         if (elect_one()) {
@@ -260,8 +260,8 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
             // no rows: the tiles go by, in step with the other warp's
 #pragma unroll 1
             for (int i = 0; i < count; ++i, ++n) {
-                waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
-                waits.on(bar + B_V_FULL + (n & 1), (n >> 1) & 1);
+                waits.on_lane(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
+                waits.on_lane(bar + B_V_FULL + (n & 1), (n >> 1) & 1);
                 if (elect_one()) {
                     mbar_arrive(bar + B_K_FREE + (n & 1));
                     mbar_arrive(bar + B_V_FREE + (n & 1));
@@ -270,9 +270,8 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
             }
             continue;
         }
-        alive &= waits.on(bar + B_Q_FULL + m, pieces++ & 1);
-        alive &= waits.on(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
-        alive = __all_sync(0xffffffffu, alive);
+        alive &= waits.on_lane(bar + B_Q_FULL + m, pieces++ & 1);
+        alive &= waits.on_lane(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
         tc_fence_after();
         scores(0, n & 1);
         scores(1, n & 1);
@@ -280,12 +279,11 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
         for (int i = 0; i < count; ++i, ++n, ++done) {
             const int buf = n & 1;
             const bool more = i + 1 < count;
-            if (more) alive &= waits.on(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
-            alive &= waits.on(bar + B_V_FULL + buf, (n >> 1) & 1);
+            if (more) alive &= waits.on_lane(bar + B_K_FULL + (buf ^ 1), ((n + 1) >> 1) & 1);
+            alive &= waits.on_lane(bar + B_V_FULL + buf, (n >> 1) & 1);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                alive &= waits.on(bar + B_P_FULL + 2 * m + half, done & 1);
-                alive = __all_sync(0xffffffffu, alive);
+                alive &= waits.on_lane(bar + B_P_FULL + 2 * m + half, done & 1);
                 tc_fence_after();
                 if (elect_one()) {
                     if (alive) {
@@ -630,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 for (int i = 0; i < count; ++i, ++n) {
                     const int buf = n & 1;
                     const uint32_t reuse = ((n >> 1) + 1) & 1;
-                    const bool k_ok = n < 2 || waits.on(bar + B_K_FREE + buf, reuse);
+                    const bool k_ok = n < 2 || waits.on_lane(bar + B_K_FREE + buf, reuse);
                     if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, tok);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -641,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     prefetch(i + 3, ahead[0]);
                     ahead[1] = page_at(i + 4);
                     load(k, i + 1, page, true);
-                    const bool v_ok = n < 2 || waits.on(bar + B_V_FREE + buf, reuse);
+                    const bool v_ok = n < 2 || waits.on_lane(bar + B_V_FREE + buf, reuse);
                     const uint32_t bad = v.take_nan();
                     nan_of[n & 3][tok] = (uint8_t)bad;
                     const uint32_t found = __ballot_sync(0xffffffffu, bad != 0);

@@ -12,6 +12,7 @@
 #include "gdn.h"
 #include "gdn_selftest.h"
 #include "gdn_internal.h"
+#include "gdn_kv_attn.cuh"
 #include "tc_common.cuh"
 
 namespace gdn {
@@ -47,6 +48,33 @@ k_wait_selftest(int complete, uint32_t limit, int *err, int *out) {
     out[1] = flag_ok ? 1 : 0;
 }
 
+constexpr int kRingThreads = 256;
+__device__ int g_ring_out[2];
+
+// The attention kernels' waits (kv::Waits), by eight warps on a phase that the CTA
+// completes itself or that nothing completes, and once more on the same phase: how
+// many threads found it complete each time.
+__global__ void __launch_bounds__(kRingThreads, 1)
+k_ring_selftest(int complete, uint32_t limit, int *err, int *out) {
+    __shared__ uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&bar, 1);
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (complete && threadIdx.x == 0) ptx::mbar_arrive(&bar);
+    __syncwarp();
+    const kv::Waits waits{&abort_flag, err, limit};
+    const bool first = waits.on(&bar, 0), second = waits.on(&bar, 0);
+    const int n_first = __syncthreads_count(first), n_second = __syncthreads_count(second);
+    if (threadIdx.x == 0) {
+        out[0] = n_first;
+        out[1] = n_second;
+    }
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -71,5 +99,26 @@ extern "C" gdn_status gdn_selftest_wait(int complete, long long limit, int *wait
         waits_ok[0] = host[0];
         waits_ok[1] = host[1];
     }
+    return GDN_OK;
+}
+
+extern "C" gdn_status gdn_selftest_ring(int complete, long long limit, int *result,
+                                        void *stream) {
+    if ((complete != 0 && complete != 1) || limit < 1 || limit > gdn::kMaxSelftestLimit || !result)
+        return GDN_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int *err = gdn::device_error_word();
+    int *out = nullptr;
+    if (!err || cudaGetSymbolAddress(reinterpret_cast<void **>(&out), gdn::g_ring_out) !=
+                    cudaSuccess)
+        return GDN_ERR_CUDA;
+    gdn::k_ring_selftest<<<1, gdn::kRingThreads, 0, st>>>(complete, static_cast<uint32_t>(limit),
+                                                          err, out);
+    gdn::count_launch();
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (cudaMemcpyAsync(result, out, sizeof(gdn::g_ring_out), cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return GDN_ERR_CUDA;
     return GDN_OK;
 }
