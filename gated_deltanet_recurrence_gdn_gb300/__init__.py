@@ -453,8 +453,9 @@ def selftest_wait(complete: bool, limit: int, device=None):
 def selftest_ring(complete: bool, limit: int, device=None):
     """The same for the warp-wide waits of the attention kernels over the cache
     (gdn_selftest_ring): how many of 256 threads found the phase complete, in a
-    wait and in one more after it."""
-    out = (_i * 2)()
+    wait and in one more after it, and how many words of two copies of 1024 were
+    there once the ring that they went to was drained."""
+    out = (_i * 3)()
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         _check(load().gdn_selftest_ring(1 if complete else 0, int(limit), out, _stream(device)),
                "gdn_selftest_ring")

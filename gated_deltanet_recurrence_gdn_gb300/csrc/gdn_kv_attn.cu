@@ -60,16 +60,6 @@ constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by wa
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
-// Copy of `bytes` (a multiple of 16, both sides 16-byte aligned) into shared
-// memory, counted on the mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(dst), "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm(
@@ -288,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ typename W::P plan;
     __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ uint32_t armed[kStages];     // tiles that were copied into each stage
     __shared__ int abort_flag;
     __shared__ float2 warp_ml[kWarps][kRows];
     __shared__ float row_mul[kRows];
@@ -302,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(full + i, 1);
             ptx::mbar_init(empty + i, kWarps);
+            armed[i] = 0;
         }
         abort_flag = 0;
         ptx::fence_mbar_init();
@@ -334,20 +326,24 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             raw[k] = there && in_tile < kTile && at < len ? a.kv.page_raw(b, at) : Kv::kNoPage;
         }
     };
-    // copies the CTA's tile n, whose first place is `place` (one warp)
-    int last_made = -1;                           // the last one that this warp copied
+    // Copies the CTA's tile n, whose first place is `place` (one warp).  Once a wait has given
+    // up nothing more is copied, and a warp frees no stage that it has not waited for: a
+    // stage is filled again only behind eight warps that had its tile.
     auto produce = [&](uint32_t n, int place, int h, const int (&raw)[kRuns]) {
         int page[kRuns];
 #pragma unroll
         for (int k = 0; k < kRuns; ++k) page[k] = a.kv.page_checked(raw[k], a.err);
         const uint32_t stage = n % kStages;
         if (n >= kStages && !waits.on(empty + stage, ((n / kStages) + 1) & 1)) return;
+        if (__any_sync(0xffffffffu, *waits.abort != 0)) return;
         uint32_t runs = 0;
 #pragma unroll
         for (int k = 0; k < kRuns; ++k)
             runs += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && lane_part == 0));
-        last_made = n;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
+        if (lane == 0) {
+            armed[stage] = n / kStages + 1;
+            ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
+        }
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < kRuns; ++k) {
@@ -652,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     } while (__any_sync(0xffffffffu, low));
                 }
             }
+            if (!arrived) break;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty + stage);
             if (++stage == kStages) {
@@ -677,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             if (g == 0) warp_ml[warp][2 * t4 + e] = make_float2(sub[e], x);
         }
         __syncthreads();
+        if (*waits.abort) break;        // (no wait is made between here and the next barrier)
         const W &w = walk[piece];
         const int h = w.h, row0 = w.row0(), rows = w.rows(a);
         const bool complete = w.complete();
@@ -751,10 +749,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         piece = after_piece;
         after_piece = third;
     }
-    if (abort_flag && last_made >= 0) {
-        // a wait gave up: the last copy this warp issued is still waited for
-        ptx::mbar_wait(full + last_made % kStages, (last_made / kStages) & 1, a.wait_limit);
-    }
+    // a wait gave up: copies that no warp has waited for may still be on their way
+    if (*waits.abort && warp == 0) drain_ring<kStages>(full, armed);
 }
 
 template <typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>

@@ -246,6 +246,24 @@ struct Walk {
     }
 };
 
+// Copy of `bytes` (a multiple of 16, both sides 16-byte aligned) into shared
+// memory, counted on the mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst), "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+
+// Waits, in one warp, for the copies still on their way into a ring: armed[s] is the number
+// of phases of full[s] that copies have been counted on, the last one's may be in flight.
+template <int kStages>
+__device__ __forceinline__ void drain_ring(uint64_t *full, const uint32_t *armed) {
+    for (int s = 0; s < kStages; ++s)
+        if (armed[s] > 0) ptx::mbar_wait(full + s, (armed[s] - 1) & 1, ptx::kDrainLimit);
+}
+
 // The waits of a CTA: bounded, and over at once when one of them has given up
 // (the error is recorded, and the CTA runs to its end without computing).
 struct Waits {

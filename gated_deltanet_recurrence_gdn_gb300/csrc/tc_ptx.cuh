@@ -86,6 +86,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
     return false;
 }
 
+// Polls of the waits for what is still on its way into shared or tensor memory when a
+// CTA ends: a bound of their own, whatever the caller's that may just have run out.
+constexpr uint32_t kDrainLimit = 1u << 22;
+
 // Release / acquire on a CTA-shared 32-bit word: a cheaper one-way hand-off
 // than an mbarrier arrive for a single waiting thread.  A counter that only
 // grows (chunk index + 1) has no phase to confuse.

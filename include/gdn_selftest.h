@@ -43,11 +43,13 @@ gdn_status gdn_selftest_wait(int complete, long long limit, int *waits_ok, void 
 /*
  * The same for the waits of the attention kernels over the cache, which a whole
  * warp makes and whose result every lane of it shares: 256 threads wait on an
- * mbarrier phase, and once more on the same.
+ * mbarrier phase, and once more on the same, while two copies of 1024 words are
+ * on their way into a ring of three stages.
  *   complete, limit, stream, status   as above (a wait gives up after
  *               limit + 1 suspending polls, the second one at once).
- *   result      host pointer to 2 ints: the threads for which the first and the
- *               second wait succeeded, 256 or 0 each.
+ *   result      host pointer to 3 ints: the threads for which the first and the
+ *               second wait succeeded, 256 or 0 each, and the words that were
+ *               there once the ring was drained, 2048.
  */
 gdn_status gdn_selftest_ring(int complete, long long limit, int *result, void *stream);
 

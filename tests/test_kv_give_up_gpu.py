@@ -32,6 +32,38 @@ def test_waits_that_nothing_completes_give_up_in_every_lane(limit):
     check(c, queries(6, 4, 64, torch.bfloat16, "thd", 61))
 
 
+@pytest.mark.parametrize("complete,limit", [(True, 1000), (False, 1), (False, 64)])
+def test_copies_that_nobody_waited_for_are_drained(complete, limit):
+    # by the drain's own bound, not the one that has run out
+    for _ in range(20):
+        assert gdn.selftest_ring(complete, limit)[2] == 2048
+    status()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("limit", [1, 2, 8])
+def test_short_limits_end_in_a_status(limit, io):
+    # whether or not a wait runs out at so few polls, the call ends, says so, and the next one
+    # is right (8 rows of a head at most: the kernel whose tiles arrive by bulk copies)
+    c = R.Cache([9000, 77, 0, 4000, 12001], 2, 16, 64, seed=62)
+    q = queries(5, 8, 64, io, "thd", 63)
+    want = check(c, q)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    prev = gdn.get_option(gdn.GDN_OPT_WAIT_LIMIT)
+    gdn.set_option(gdn.GDN_OPT_WAIT_LIMIT, limit)
+    try:
+        for _ in range(5):
+            flush.zero_()
+            o = gdn.gdn_kv_attn(q, c.pages, c.table_t, c.len_t)
+            s = status()
+            assert s in (gdn.GDN_OK, gdn.GDN_ERR_DEVICE_TIMEOUT)
+            if s == gdn.GDN_OK:
+                assert (o.double().cpu().numpy() == want).all()
+    finally:
+        gdn.set_option(gdn.GDN_OPT_WAIT_LIMIT, prev)
+    assert (check(c, q) == want).all()
+
+
 def test_refusals():
     for args in ((True, 0), (True, -1), (False, 1 << 23)):
         with pytest.raises(gdn.GdnError):
