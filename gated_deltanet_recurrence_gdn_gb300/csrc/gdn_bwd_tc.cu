@@ -569,7 +569,7 @@ k_bwd_dstate_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             // every issued MMA has finished before TMEM is released
             mma_commit(bar + B_DRAIN);
-            mbar_wait(bar + B_DRAIN, 0, ctl.limit);
+            mbar_wait(bar + B_DRAIN, 0, kDrainLimit);
         }
     } else {
         // ============================================== prep MMA issuer
@@ -619,7 +619,7 @@ k_bwd_dstate_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 BTRACE(3, j, 5, true);
             }
             mma_commit(bar + B_DRAIN2);
-            mbar_wait(bar + B_DRAIN2, 0, ctl.limit);
+            mbar_wait(bar + B_DRAIN2, 0, kDrainLimit);
         }
     }
     tc_fence_before();

@@ -675,7 +675,7 @@ k_gdn_fused(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 // every issued MMA has finished before tensor memory is released
                 mma_commit(bar + B_DRAIN2);
-                mbar_wait(bar + B_DRAIN2, 0, ctl.limit);
+                mbar_wait(bar + B_DRAIN2, 0, kDrainLimit);
             } else {
                 auto mma_w = [&](int jj) -> bool {
                     const int s = jj % kSlots;
@@ -757,7 +757,7 @@ k_gdn_fused(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     if (ok) ok = mma_o(j);
                 }
                 mma_commit(bar + B_DRAIN);
-                mbar_wait(bar + B_DRAIN, 0, ctl.limit);
+                mbar_wait(bar + B_DRAIN, 0, kDrainLimit);
             }
         }
     }

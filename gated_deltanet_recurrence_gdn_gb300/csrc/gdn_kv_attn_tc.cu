@@ -304,7 +304,7 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
     // before tensor memory is given back, whatever happened
     if (elect_one()) mma_commit(bar + B_DRAIN + m);
     __syncwarp();
-    mbar_wait(bar + B_DRAIN + m, 0, a.wait_limit);
+    mbar_wait(bar + B_DRAIN + m, 0, kDrainLimit);
 }
 
 template <int D>

@@ -774,7 +774,7 @@ __device__ __forceinline__ void gdn_tc_body(const CUtensorMap *tm_q, const CUten
             }
             // every issued MMA has finished before TMEM is released
             mma_commit(bar + B_DRAIN);
-            mbar_wait(bar + B_DRAIN, 0, ctl.limit);
+            mbar_wait(bar + B_DRAIN, 0, kDrainLimit);
         }
     } else if (warp == 10) {
         // ============================================== prep MMA issuer
@@ -815,7 +815,7 @@ __device__ __forceinline__ void gdn_tc_body(const CUtensorMap *tm_q, const CUten
                 TRACE(3, j, 3, true);
             }
             mma_commit(bar + B_DRAIN2);
-            mbar_wait(bar + B_DRAIN2, 0, ctl.limit);
+            mbar_wait(bar + B_DRAIN2, 0, kDrainLimit);
         }
     }
     tc_fence_before();

@@ -446,7 +446,7 @@ __device__ __forceinline__ void gdn_tcw_body(const CUtensorMap *tm_q, const CUte
             }
             // every issued MMA has finished before TMEM is released
             mma_commit(bar + W_DRAIN);
-            mbar_wait(bar + W_DRAIN, 0, ctl.limit);
+            mbar_wait(bar + W_DRAIN, 0, kDrainLimit);
         }
     } else {
         // ====================================== gates and P' (warps 10-11)
@@ -624,7 +624,7 @@ __device__ __forceinline__ void gdn_tcw_body(const CUtensorMap *tm_q, const CUte
         // every Gram issued here has finished before TMEM is released
         if (t == 0 && nch > 0 && !so) {
             mma_commit(bar + W_DRAIN2);
-            mbar_wait(bar + W_DRAIN2, 0, ctl.limit);
+            mbar_wait(bar + W_DRAIN2, 0, kDrainLimit);
         }
     }
     tc_fence_before();

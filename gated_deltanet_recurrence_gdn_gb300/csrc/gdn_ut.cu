@@ -201,7 +201,7 @@ k_gdn_ut(const __grid_constant__ CUtensorMap tm_k, UtParams p) {
         if (lane == 0) {
             // every issued MMA and copy has finished before the CTA leaves
             mma_commit(bar + U_DRAIN);
-            mbar_wait(bar + U_DRAIN, 0, ctl.limit);
+            mbar_wait(bar + U_DRAIN, 0, kDrainLimit);
             if (*abort_flag)
                 for (long long i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i)
                     mbar_wait(bar + U_FULL + (i & 1), (uint32_t)((i >> 1) & 1), ctl.limit);

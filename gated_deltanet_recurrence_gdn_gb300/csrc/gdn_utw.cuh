@@ -452,11 +452,11 @@ __device__ __forceinline__ void utw_run(uint8_t *sm, uint32_t tmem, int tid, uin
     // the CTA leaves (each issuing thread drains its own MMAs)
     if (tid == 0) {
         mma_commit(bar + V_DRAIN);
-        mbar_wait(bar + V_DRAIN, 0, ctl.limit);
+        mbar_wait(bar + V_DRAIN, 0, kDrainLimit);
     }
     if (tid == kIssuer) {
         mma_commit(bar + V_DRAIN2);
-        mbar_wait(bar + V_DRAIN2, 0, ctl.limit);
+        mbar_wait(bar + V_DRAIN2, 0, kDrainLimit);
         for (long long u = grammed; u < loaded; ++u)
             mbar_wait(bar + V_FULL + (u & 1), (uint32_t)((u >> 1) & 1), ctl.limit);
     }
