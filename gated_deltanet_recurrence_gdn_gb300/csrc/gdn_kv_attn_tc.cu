@@ -65,8 +65,9 @@ enum : int {
     B_S_FULL = 10,            // [2][2] scores of a row tile with each half of the tokens
     B_P_FULL = 14,            // [2][2] probabilities; 4 warps
     B_O_FULL = 18,            // [2][2] their PV is done
-    B_DRAIN = 22,             // [2]
-    B_COUNT = 24
+    B_SEEN = 22,              // row tile 1 has read a piece's last NaN blocks; 4 warps
+    B_DRAIN = 23,             // [2]
+    B_COUNT = 25
 };
 
 template <int D>
@@ -257,7 +258,9 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
         const int count = w.count();
         if (count == 0) continue;
         if (w.rows(a) <= m * kRowTile) {
-            // no rows: the tiles go by, in step with the other warp's
+            // no rows: the tiles go by, in step with the other warp's, once the softmax's warps
+            // are done with the last piece that had some
+            if (pieces > 0) waits.on_lane(bar + B_SEEN, (pieces - 1) & 1);
 #pragma unroll 1
             for (int i = 0; i < count; ++i, ++n) {
                 waits.on_lane(bar + B_K_FULL + (n & 1), (n >> 1) & 1);
@@ -317,9 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     __shared__ uint64_t bar[B_COUNT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    // NaN blocks of V of the last four tiles' tokens, and whether a warp found any.  A
-    // tile's are read before the scores of the second next are used, so before the
-    // values of the fourth next may be converted.
+    // NaN blocks of V of the last four tiles' tokens, and whether a warp found any.  A tile's
+    // are read by a row tile's softmax before its probabilities of the next tile are stored,
+    // and the values of the fourth next tile are converted behind the products of the second
+    // next.  A piece's last ones are read by row tile 0 before its next piece's first
+    // probabilities; row tile 1 may have none in the next pieces, whose tiles then go by only
+    // behind B_SEEN.
     __shared__ uint8_t nan_of[4][kTile];
     __shared__ uint32_t nan_any[4][4];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
             const bool warps = i < B_K_FREE || i == B_V_FULL || i == B_V_FULL + 1 ||
-                               i == B_Q_FULL || i == B_Q_FULL + 1 ||
+                               i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_SEEN ||
                                (i >= B_P_FULL && i < B_O_FULL);
             const bool free = (i >= B_K_FREE && i < B_V_FULL) || (i >= B_V_FREE && i < B_Q_FULL);
             mbar_init(bar + i, warps ? 4 : free ? 2 : 1);
@@ -539,6 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     waits.on(bar + B_O_FULL + 2 * m + 1, (done - 1) & 1);
                     tc_fence_after();
                     see_nan(count - 1);
+                    if (m == 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar + B_SEEN);
+                    }
                 }
                 all += count;
 
