@@ -1,15 +1,15 @@
 // gdn_check.cuh -- the debug bounds-check build (-DGDN_BOUNDS_CHECK).
 //
-// Under the flag, the tcgen05 and chunk-prep kernels check every shared-memory
-// access they make through the helpers (row stores, bulk-copy destinations,
-// mbarriers, MMA operand descriptors), every tensor-memory column they load,
-// and the global indices of their loads and stores against the sizes of the
-// arrays.  A failed check skips the access and records the source line of the
-// first failure in a word of its translation unit; gdn_sync_check() folds the
-// words of all translation units into GDN_ERR_BOUNDS and
-// gdn_bounds_violation() returns the line.  Nothing traps or asserts: the
-// context stays usable.  Without the flag every check is the constant true and
-// compiles away.
+// Under the flag, the tcgen05, chunk-prep and cache attention kernels check every
+// shared-memory access they make through the helpers (row stores, bulk-copy
+// destinations, mbarriers, MMA operand descriptors), every tensor-memory column they
+// load, and the global indices of their loads and stores against the sizes of the
+// arrays; the cache attention kernels' pages, rows and pieces among them.  Shared
+// memory is the dynamic block: barriers lie in it.  A failed check skips the access
+// and records the source line of the first failure in a word of its translation unit;
+// gdn_sync_check() folds the words of all translation units into GDN_ERR_BOUNDS and
+// gdn_bounds_violation() returns the line.  Nothing traps or asserts: the context
+// stays usable.  Without the flag every check is the constant true and compiles away.
 //
 // Misaligned or out-of-range bulk-copy inputs fail silently or fault
 // ("Gated DeltaNet GPU并行实现", section 5.2, second pitfall), so this build is

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "gdn_attn.h"
+#include "gdn_check.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -217,11 +218,17 @@ struct Kv {
     __device__ __forceinline__ long long block(int page, int h) const {
         return ((long long)page * H + h) * block_bytes(1 << page_shift, d);
     }
+    // (the bounds-check build: `bytes` bytes from `at` in a page's block lie in the pool)
+    __device__ __forceinline__ bool bytes_ok(int page, int h, int at, int bytes) const {
+        return GDN_IDX_OK(h, 1, H) && GDN_IDX_OK(at, bytes, block_bytes(1 << page_shift, d)) &&
+               GDN_IDX_OK(page, 1, n_pages);
+    }
     // Page of place p of sequence b as the table has it, and the same checked: -1 with
     // the error recorded if it is outside the pool.  (Apart, so that a look-up made
     // ahead is not waited for where it is made; kNoPage passes through as -1.)
     static constexpr int kNoPage = -0x7fffffff;
     __device__ __forceinline__ int page_raw(int b, int p) const {
+        if (!GDN_IDX_OK(b, 1, N) || !GDN_IDX_OK(p >> page_shift, 1, max_pages)) return kNoPage;
         return __ldg(page_table + b * table_stride + (p >> page_shift));
     }
     __device__ __forceinline__ int page_checked(int g, int *err) const {
@@ -236,6 +243,8 @@ struct Kv {
     // out of range are recorded, and the sequence then counts as having none; so are
     // offsets that do not begin at 0 or end at n_tokens (tokens of no sequence).
     __device__ __forceinline__ void tokens(int b, int &first, int &n, int &len, int *err) const {
+        first = n = len = 0;
+        if (!GDN_IDX_OK(b, 1, N)) return;
         if (cu) {
             first = __ldg(cu + b);
             n = __ldg(cu + b + 1) - first;

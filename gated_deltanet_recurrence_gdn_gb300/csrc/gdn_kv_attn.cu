@@ -125,7 +125,11 @@ struct Shape {
     // rows of every warp that are merged at a time, in one stage
     static constexpr int kMergeRows = kWarps * 8 * D * 4 <= kStage ? 8 : 4;
     static_assert(kWarps * kMergeRows * D * 4 <= kStage, "a stage holds a merge");
-    static constexpr int kSmem = kRing + kQueries;
+    // After the ring and the queries: which stages are full, which empty.  (bf16, d = 128:
+    // 112688 bytes, next to 2960 static ones; above 115712 in all a second CTA does not fit,
+    // and 256 sequences take 637 us instead of 464.  Hence no more alignment than copies want.)
+    static constexpr int kBars = kRing + kQueries;
+    static constexpr int kSmem = kBars + 2 * kStages * 8;
     static constexpr int kLead = kStages - 2;                  // tiles copied ahead
 };
 
@@ -275,9 +279,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     // lifted maximum lies above it, and that range's middle and half in log2 units.
     constexpr float kLow = kSplit ? 0x1p-3f : 0x1p-14f, kBand = kSplit ? 0x1p18f : 0x1p29f;
     constexpr float kMid = kSplit ? 6.f : 0.5f, kHalf = kLift + kRaise - kMid;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ typename W::P plan;
-    __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint32_t armed[kStages];     // tiles that were copied into each stage
     __shared__ int abort_flag;
     __shared__ float2 warp_ml[kWarps][kRows];
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     __shared__ bool walk_more[3];   // whether there is one behind each
     __shared__ int row_from[kRows], row_to[kRows], all_seen[2];
     uint4 *queries = reinterpret_cast<uint4 *>(smem + Sh::kRing);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Sh::kBars), *empty = full + kStages;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -350,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             if (page[k] < 0) continue;
             const int psz = a.kv.page_size(), in_tile = (lane_run + 8 * k) * run;
             const int at = (place + in_tile) & (psz - 1);
-            const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + at * row_bytes +
-                                 (lane_part == 0   ? 0
-                                  : lane_part == 1 ? v_code_at(psz, D, 0)
-                                  : lane_part == 2 ? k_scale_at(psz, D, 0)
-                                                   : v_scale_at(psz, D, 0));
+            const int from = at * row_bytes + (lane_part == 0   ? 0
+                                               : lane_part == 1 ? v_code_at(psz, D, 0)
+                                               : lane_part == 2 ? k_scale_at(psz, D, 0)
+                                                                : v_scale_at(psz, D, 0));
+            if (!a.kv.bytes_ok(page[k], h, from, run * row_bytes)) continue;
+            const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + from;
             bulk_load(ring_at + stage * Sh::kStage + lane_dst + in_tile * row_bytes, src,
                       run * row_bytes, full + stage);
         }
@@ -365,7 +370,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         const int r = w.row0() + g;
         there = g < w.rows(a);
         j = there ? r / a.G : 0;
-        return there ? r - j * a.G : 0;
+        const int i = there ? r - j * a.G : 0;
+        if (there) there = a.row_ok((long long)w.sq.first + j, w.h * a.G + i);
+        return i;
     };
     auto load_queries = [&](const W &w, Run<T> (&x)[D / 32]) {
         bool there;
@@ -732,10 +739,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                     const int rr = row0 + r, j = rr / a.G, hq = h * a.G + rr - j * a.G;
                     const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
                     const float inv = l == 0.f ? 0.f : gv / l;
+                    if (!a.row_ok((long long)w.sq.first + j, hq)) continue;
                     T *p = static_cast<T *>(a.o) + (w.sq.first + j) * a.o_tok + hq * a.o_head + d;
                     store4(p, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                     if (a.lse && d == 0) a.lse[(long long)(w.sq.first + j) * a.Hq + hq] = lse_of(m, l);
-                } else {
+                } else if (a.part_ok(slot * kRows + r, kRows)) {
                     store4(a.part_o + (slot * kRows + r) * D + d, v.x, v.y, v.z, v.w);
                     if (d == 0) a.part_ml[slot * kRows + r] = make_float2(m, l);
                 }

@@ -26,6 +26,15 @@ struct AttnArgs {
     struct Cut *cuts;          // [grid], nullptr where nothing is cut
     int *err;
     uint32_t wait_limit;       // polls of a wait before it gives up
+
+    // The bounds-check build: a row of q, o and lse; one of the pieces' rows, of `rows` each
+    // in two slots a CTA.
+    __device__ __forceinline__ bool row_ok(long long tok, int hq) const {
+        return GDN_IDX_OK(tok, 1, kv.n_tokens) && GDN_IDX_OK(hq, 1, Hq);
+    }
+    __device__ __forceinline__ bool part_ok(long long row, int rows) const {
+        return GDN_IDX_OK(row, 1, 2ll * gridDim.x * rows);
+    }
 };
 
 // A (sequence, key/value head, row tile) that is cut, written by the CTA with its
@@ -250,6 +259,7 @@ struct Walk {
 // memory, counted on the mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
                                           uint64_t *bar) {
+    if (!GDN_SMEM_OK(dst, bytes) || !GDN_SMEM_OK(ptx::smem_u32(bar), 8)) return;
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
             "r"(dst), "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
@@ -352,6 +362,7 @@ __global__ void __launch_bounds__(kJoin * 32) k_kv_join(const AttnArgs a) {
         float2 ml;
         float v[kVec];
         __device__ __forceinline__ void load(const AttnArgs &a, long long at, int lane) {
+            if (!a.part_ok(at, kRows)) return;
             const float *p = a.part_o + at * D + lane * kVec;
             ml = a.part_ml[at];
             if constexpr (kVec == 2) {
@@ -370,7 +381,8 @@ __global__ void __launch_bounds__(kJoin * 32) k_kv_join(const AttnArgs a) {
     for (int u = 0; u < kFirst; ++u)
         if (stripe + u * kStripes < c.pieces) first[u].load(a, slot(stripe + u * kStripes), lane);
     float m = -INFINITY;
-    for (int k = lane; k < c.pieces; k += 32) m = fmaxf(m, a.part_ml[slot(k)].x);
+    for (int k = lane; k < c.pieces; k += 32)
+        if (a.part_ok(slot(k), kRows)) m = fmaxf(m, a.part_ml[slot(k)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float v[kVec] = {}, l = 0.f;
@@ -401,6 +413,7 @@ __global__ void __launch_bounds__(kJoin * 32) k_kv_join(const AttnArgs a) {
     const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + c.h) : 1.f;
     const float inv = l == 0.f ? 0.f : gv / l;
     T *p = static_cast<T *>(a.o) + (c.first + j) * a.o_tok + hq * a.o_head;
+    if (!a.row_ok((long long)c.first + j, hq)) return;
     for (int d = 4 * lane; d < D; d += 128) {
         float x[4] = {};
 #pragma unroll

@@ -76,7 +76,8 @@ struct Lay {
     static constexpr int OFF_Q = 0;                              // [2]
     static constexpr int OFF_K = 2 * kOperand;                   // [2]
     static constexpr int OFF_V = 4 * kOperand;                   // [2]
-    static constexpr int SIZE = 6 * kOperand + 1024;             // (aligned up to 1024)
+    static constexpr int OFF_BAR = 6 * kOperand;                 // mbarriers
+    static constexpr int SIZE = OFF_BAR + B_COUNT * 8 + 1024;    // (aligned up to 1024)
     static constexpr uint32_t TM_S = 0, TM_O = 256;              // TMEM columns, 128 a row tile
 };
 
@@ -87,6 +88,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
+    if (!GDN_TMEM_OK(d, 128) || !GDN_TMEM_OK(a, 8)) return;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -95,6 +97,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, u
         : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    if (!GDN_TMEM_OK(taddr, 32)) return;   // the address is warp-uniform
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " GDN_OPS32 ";" ::"r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
                  "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
@@ -108,6 +111,7 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d) {
+    if (!GDN_SMEM_OK(at, 16)) return;
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
                  "r"(d)
                  : "memory");
@@ -241,8 +245,9 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
 #pragma unroll 1
                 for (int s = 0; s < D / 64; ++s) {
                     const uint64_t q = dQ + ((s * 16384) >> 4);
-                    const uint64_t k =
-                        dK + ((buf * L::kOperand + s * 16384 + half * kHalf * 128) >> 4);
+                    const uint32_t at = buf * L::kOperand + s * 16384 + half * kHalf * 128;
+                    if (!GDN_SMEM_OK(base + L::OFF_K + at, kHalf * 128)) break;
+                    const uint64_t k = dK + (at >> 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         mma_bf16(tS + kHalf * half, q + 2 * e, k + 2 * e, id_qk, (s | e) != 0);
@@ -290,11 +295,14 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
                 tc_fence_after();
                 if (elect_one()) {
                     if (alive) {
-                        const uint64_t v = dV + ((buf * L::kOperand + half * kHalf * 128) >> 4);
+                        const uint32_t at = buf * L::kOperand + half * kHalf * 128;
+                        const uint64_t v = dV + (at >> 4);
 #pragma unroll
                         for (int s = 0; s < kHalf / 16; ++s)
-                            mma_ts(tO, tS + kHalf * half + 8 * s, v + s * (2048 >> 4), id_pv,
-                                   (i | half | s) != 0);
+                            if (GDN_SMEM_OK(base + L::OFF_V + at + s * 2048,
+                                            (D / 64 - 1) * 16384 + 2048))
+                                mma_ts(tO, tS + kHalf * half + 8 * s, v + s * (2048 >> 4), id_pv,
+                                       (i | half | s) != 0);
                     }
                     mma_commit(bar + B_O_FULL + 2 * m + half);
                     if (half == 1) mma_commit(bar + B_V_FREE + buf);
@@ -315,9 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     using L = Lay<D>;
     using W = Walk<kTile, kRows, kThreads>;
     using T = __nv_bfloat16;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ typename W::P plan;
-    __shared__ uint64_t bar[B_COUNT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     // NaN blocks of V of the last four tiles' tokens, and whether a warp found any.  A tile's
@@ -329,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     __shared__ uint8_t nan_of[4][kTile];
     __shared__ uint32_t nan_any[4][4];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint64_t *bar =
+        reinterpret_cast<uint64_t *>(smem_raw + (base - smem_u32(smem_raw)) + L::OFF_BAR);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kIssuer / 32) {
@@ -372,8 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 const Seq sq = w.sq;
                 const int h = w.h, rows = w.rows(a), count = w.count(), place0 = w.place0();
                 const int mine = m * kRowTile + row, r = w.row0() + mine;
-                const bool there = mine < rows;
+                bool there = mine < rows;
                 const int j = there ? r / a.G : 0, hq = h * a.G + (there ? r - j * a.G : 0);
+                if (there) there = a.row_ok((long long)sq.first + j, hq);
                 const float gv = a.kv.head_scale ? __ldg(a.kv.head_scale + a.kv.H + h) : 1.f;
                 int from = 0, to = sq.len;
                 if (there) sq.sees(a, j, from, to);
@@ -582,12 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                             }
                             if (!there) continue;
                             if (complete) store8(po + 32 * c + e, v);
-                            else store8(pp + 32 * c + e, v);
+                            else if (a.part_ok(slot * kRows + mine, kRows)) store8(pp + 32 * c + e, v);
                         }
                     }
                     if (there) {
-                        if (!complete) a.part_ml[slot * kRows + mine] = make_float2(lost, sum);
-                        else if (a.lse)
+                        if (!complete) {
+                            if (a.part_ok(slot * kRows + mine, kRows))
+                                a.part_ml[slot * kRows + mine] = make_float2(lost, sum);
+                        } else if (a.lse)
                             a.lse[(long long)(sq.first + j) * a.Hq + hq] = lse_of(lost, sum);
                     }
                 }
@@ -613,6 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         return;
                     }
                     const int row = (place0 + i * kTile + tok) & (psz - 1);
+                    if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
+                        x.clear();
+                        return;
+                    }
                     const uint8_t *blk = a.kv.pages + a.kv.block(page, h);
                     x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
                            blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
