@@ -53,47 +53,57 @@ _INT_MAX = 2 ** 31 - 1     # (larger bounds and windows mean the same)
 _axes_kept: dict = {}      # axis numbers by their value, as C arrays
 
 
-def _rows3(name, t, heads, n, d, dtype):
+def _device(name, t):
+    """The GPU of the call, that of t."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return at
+
+
+def _rows3(name, t, heads, n, d, dtype, at):
     """[tokens, heads, d] rows."""
     tok, head, one = t.stride()
-    if t.shape != (n, heads, d) or one != 1 or t.dtype != dtype or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor [tokens, heads, d] of the call's dtype, its last "
-                         "dimension contiguous" % name)
+    if t.shape != (n, heads, d) or one != 1 or t.dtype != dtype or t.get_device() != at:
+        raise ValueError("%s must be a CUDA tensor [tokens, heads, d] of the call's dtype and "
+                         "device, its last dimension contiguous" % name)
     # (a dimension of one entry may have any stride)
     return _ROWS.pack(t.data_ptr(), 0, head if heads > 1 else 0, tok if n > 1 else 0, heads)
 
 
-def _rows4(name, t, like, heads):
+def _rows4(name, t, like, heads, at):
     """[B, heads, T, d] rows, like's but for the heads."""
     B, _, T, d = like.shape
-    if t.shape != (B, heads, T, d) or t.stride(3) != 1 or t.dtype != like.dtype or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor [B, heads, T, d] of the call's dtype, its last "
-                         "dimension contiguous" % name)
+    if t.shape != (B, heads, T, d) or t.stride(3) != 1 or t.dtype != like.dtype or \
+            t.get_device() != at:
+        raise ValueError("%s must be a CUDA tensor [B, heads, T, d] of the call's dtype and "
+                         "device, its last dimension contiguous" % name)
     seq, head, tok, _ = t.stride()
     return _ROWS.pack(t.data_ptr(), seq if B > 1 else 0, head if heads > 1 else 0,
                       tok if T > 1 else 0, heads)
 
 
-def _int32(name, t, dims):
-    if t.dim() != dims or t.dtype != _i32 or not t.is_cuda or \
+def _int32(name, t, dims, at):
+    if t.dim() != dims or t.dtype != _i32 or t.get_device() != at or \
             (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s must be a %d-D int32 CUDA tensor, its last dimension contiguous"
-                         % (name, dims))
+        raise ValueError("%s must be a %d-D int32 tensor on the call's device, its last dimension "
+                         "contiguous" % (name, dims))
 
 
-def _rotary(cos, sin, pos, axes, flags, shape):
+def _rotary(cos, sin, pos, axes, flags, shape, at):
     """shape: the shape that one axis of `pos` has, or may have without its first part."""
     table = cos.shape
     if cos.dim() != 2 or table != sin.shape or cos.dtype != _f32 or sin.dtype != _f32 or \
-            not cos.is_cuda or not sin.is_cuda or not cos.is_contiguous() or \
+            cos.get_device() != at or sin.get_device() != at or not cos.is_contiguous() or \
             not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous fp32 CUDA tensors [positions, d_rot / 2]")
+        raise ValueError("cos and sin must be contiguous fp32 tensors [positions, d_rot / 2] on "
+                         "the call's device")
     lead = 0 if axes is None else 1
     whole = pos.dim() == lead + len(shape)
-    _int32("pos", pos, lead + (len(shape) if whole else 1))
+    _int32("pos", pos, lead + (len(shape) if whole else 1), at)
     if pos.shape[lead:] != (shape if whole else shape[-1:]):
         raise ValueError("pos must hold a position per token%s" % (" on each axis" if lead else ""))
-    at = 0
+    axes_at = 0
     if lead:
         axes = bytes(axes)
         if len(axes) != table[1]:
@@ -101,29 +111,31 @@ def _rotary(cos, sin, pos, axes, flags, shape):
         kept = _axes_kept.get(axes)
         if kept is None:
             kept = _axes_kept[axes] = ctypes.create_string_buffer(axes, max(1, len(axes)))
-        at = ctypes.addressof(kept)
-    return _ROTARY.pack(cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), at,
+        axes_at = ctypes.addressof(kept)
+    return _ROTARY.pack(cos.data_ptr(), sin.data_ptr(), pos.data_ptr(), axes_at,
                         pos.stride(0) if lead else 0,
                         pos.stride(lead) if whole and len(shape) == 2 else 0, table[0],
                         2 * table[1], pos.shape[0] if lead else 1, flags)
 
 
-def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d):
+def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at):
     """The packed gdn_kv, and the cache's heads and page size."""
-    if pages.dim() != 3 or pages.dtype != _u8 or not pages.is_cuda or not pages.is_contiguous():
-        raise ValueError("pages must be a contiguous uint8 CUDA tensor [n_pages, heads, page bytes]")
+    if pages.dim() != 3 or pages.dtype != _u8 or pages.get_device() != at or \
+            not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous uint8 tensor [n_pages, heads, page bytes] on "
+                         "the call's device")
     n_pages, heads, size = pages.shape
     page_size = size * 8 // (9 * d)
     if page_size * d * 9 != size * 8:
         raise ValueError("a page of %d bytes does not hold rows of d = %d" % (size, d))
-    _int32("page_table", page_table, 2)
-    _int32("kv_len", kv_len, 1)
+    _int32("page_table", page_table, 2, at)
+    _int32("kv_len", kv_len, 1, at)
     N, (rows, max_pages) = kv_len.shape[0], page_table.shape
     if rows != N:
         raise ValueError("page_table must have a row per sequence")
     cu = 0
     if cu_seqlens is not None:
-        _int32("cu_seqlens", cu_seqlens, 1)
+        _int32("cu_seqlens", cu_seqlens, 1, at)
         if cu_seqlens.shape[0] != N + 1:
             raise ValueError("cu_seqlens must have one entry more than there are sequences")
         cu = cu_seqlens.data_ptr()
@@ -131,26 +143,26 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d):
         raise ValueError("without cu_seqlens every sequence has the same number of tokens")
     scale = 0
     if kv_scale is not None:
-        if kv_scale.shape != (2, heads) or kv_scale.dtype != _f32 or not kv_scale.is_cuda or \
-                not kv_scale.is_contiguous():
-            raise ValueError("kv_scale must be a contiguous fp32 CUDA tensor [2, heads]")
+        if kv_scale.shape != (2, heads) or kv_scale.dtype != _f32 or \
+                kv_scale.get_device() != at or not kv_scale.is_contiguous():
+            raise ValueError("kv_scale must be a contiguous fp32 tensor [2, heads] on the call's "
+                             "device")
         scale = kv_scale.data_ptr()
     return _KV.pack(pages.data_ptr(), scale, page_table.data_ptr(), kv_len.data_ptr(), cu, n_pages,
                     page_size, heads, d, N, max_pages, n_tokens, page_table.stride(0)), \
         heads, page_size
 
 
-def _call(fn, what, t, check, *args):
-    """fn(*args, stream) on t's device and its current stream."""
-    at = t.get_device()
+def _call(fn, what, at, check, *args):
+    """fn(*args, stream) on GPU `at` and its current stream."""
     if torch._C._cuda_getDevice() != at:
         with torch.cuda.device(at):
-            return _call(fn, what, t, check, *args)
+            return _call(fn, what, at, check, *args)
     rc = fn(*args, torch._C._cuda_getCurrentRawStream(at))
     if rc:
         raise GdnError(rc, what)
     if check:
-        _check(load().gdn_sync_check(_stream(t.device)), what + " (device)")
+        _check(load().gdn_sync_check(_stream(at)), what + " (device)")
 
 
 def gdn_kv_page_bytes(page_size: int, d: int) -> int:
@@ -194,15 +206,17 @@ def gdn_rope_axes(sections, interleave=False):
 def _rope(q, k, cos, sin, pos, axes, flags, out, check, what):
     if q.dtype not in _DT or q.dim() != 4:
         raise ValueError("q must be [B, heads, T, d], bf16 or fp32")
+    at = _device("q", q)
     B, Hq, T, d = q.shape
     qo, ko = out if out is not None else (torch.empty_like(q),
                                           None if k is None else torch.empty_like(k))
     rk = rko = None
     if k is not None:
         Hk = k.shape[1]
-        rk, rko = _rows4("k", k, q, Hk), _rows4("out[1]", ko, q, Hk)
-    _call(load().gdn_rope, what, q, check, _rows4("q", q, q, Hq), _rows4("out[0]", qo, q, Hq), rk,
-          rko, B, T, d, _rotary(cos, sin, pos, axes, flags, (B, T)), _DT[q.dtype])
+        rk, rko = _rows4("k", k, q, Hk, at), _rows4("out[1]", ko, q, Hk, at)
+    _call(load().gdn_rope, what, at, check, _rows4("q", q, q, Hq, at),
+          _rows4("out[0]", qo, q, Hq, at), rk, rko, B, T, d,
+          _rotary(cos, sin, pos, axes, flags, (B, T), at), _DT[q.dtype])
     return qo, ko
 
 
@@ -235,19 +249,21 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     number of new tokens each; kv_scale fp32 [2, heads]: a further scale per head."""
     if k.dtype not in _DT or k.dim() != 3:
         raise ValueError("k must be [tokens, heads, d], bf16 or fp32")
+    at = _device("k", k)
     n, _, d = k.shape
     dtype = k.dtype
-    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at)
     rq = rqo = rot = None
     if q is not None:
         if out is None:
             out = torch.empty_like(q)
         Hq = q.shape[1]
-        rq, rqo = _rows3("q", q, Hq, n, d, dtype), _rows3("out", out, Hq, n, d, dtype)
+        rq, rqo = _rows3("q", q, Hq, n, d, dtype, at), _rows3("out", out, Hq, n, d, dtype, at)
     if cos is not None:
-        rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,))
-    _call(load().gdn_kv_append, "gdn_kv_append", k, check, kv, _rows3("k", k, heads, n, d, dtype),
-          _rows3("v", v, heads, n, d, dtype), rq, rqo, rot, _DT[dtype])
+        rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,), at)
+    _call(load().gdn_kv_append, "gdn_kv_append", at, check, kv,
+          _rows3("k", k, heads, n, d, dtype, at), _rows3("v", v, heads, n, d, dtype, at), rq, rqo,
+          rot, _DT[dtype])
     return out if q is not None else None
 
 
@@ -255,15 +271,16 @@ def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_s
                 dtype=torch.bfloat16, out=None, check=False):
     """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
     they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
-    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d)
+    at = _device("pages", pages)
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at)
     if out is None:
         k = torch.empty((n_tokens, heads, d), dtype=dtype, device=pages.device)
         v = torch.empty_like(k)
     else:
         k, v = out
-    _call(load().gdn_kv_read, "gdn_kv_read", pages, check, kv,
-          _rows3("out", k, heads, n_tokens, d, dtype), _rows3("out", v, heads, n_tokens, d, dtype),
-          _DT[dtype])
+    _call(load().gdn_kv_read, "gdn_kv_read", at, check, kv,
+          _rows3("out", k, heads, n_tokens, d, dtype, at),
+          _rows3("out", v, heads, n_tokens, d, dtype, at), _DT[dtype])
     return k, v
 
 
@@ -279,9 +296,10 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
     the last `window` places up to its own (0: all)."""
     if q.dtype not in _DT or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
+    at = _device("q", q)
     n, Hq, d = q.shape
     dtype = q.dtype
-    kv, _, page_size = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d)
+    kv, _, page_size = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at)
     if out is None:
         out = torch.empty_like(q)
     lse = torch.empty((n, Hq), dtype=_f32, device=q.device) if return_lse else None
@@ -289,8 +307,8 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
         max_len = page_table.shape[1] * page_size
     if max_new is None:
         max_new = n if cu_seqlens is not None else n // max(kv_len.shape[0], 1)
-    _call(load().gdn_kv_attn, "gdn_kv_attn", q, check, kv, _rows3("q", q, Hq, n, d, dtype),
-          _rows3("out", out, Hq, n, d, dtype), None if lse is None else lse.data_ptr(),
+    _call(load().gdn_kv_attn, "gdn_kv_attn", at, check, kv, _rows3("q", q, Hq, n, d, dtype, at),
+          _rows3("out", out, Hq, n, d, dtype, at), None if lse is None else lse.data_ptr(),
           min(max_len, _INT_MAX), min(max_new, _INT_MAX), d ** -0.5 if scale is None else scale,
           min(window, _INT_MAX), GDN_ATTN_CAUSAL if causal else 0, _DT[dtype])
     return (out, lse) if return_lse else out
