@@ -211,6 +211,8 @@ def _rope(q, k, cos, sin, pos, axes, flags, out, check, what):
     qo, ko = out if out is not None else (torch.empty_like(q),
                                           None if k is None else torch.empty_like(k))
     rk = rko = None
+    if (k is None) != (ko is None):
+        raise ValueError("out must hold a place for k where there is a k, and None elsewhere")
     if k is not None:
         Hk = k.shape[1]
         rk, rko = _rows4("k", k, q, Hk, at), _rows4("out[1]", ko, q, Hk, at)
@@ -254,6 +256,11 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     dtype = k.dtype
     kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at)
     rq = rqo = rot = None
+    if cos is None or sin is None or pos is None:
+        if adjacent or any(x is not None for x in (cos, sin, pos, axes)):
+            raise ValueError("cos, sin and pos go together, and axes and adjacent with them")
+    if q is None and out is not None:
+        raise ValueError("out is where q goes, and there is no q")
     if q is not None:
         if out is None:
             out = torch.empty_like(q)
