@@ -125,8 +125,8 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at):
         raise ValueError("pages must be a contiguous uint8 tensor [n_pages, heads, page bytes] on "
                          "the call's device")
     n_pages, heads, size = pages.shape
-    page_size = size * 8 // (9 * d)
-    if page_size * d * 9 != size * 8:
+    page_size = size * 8 // (9 * d) if d > 0 else 0
+    if page_size * d * 9 != size * 8 or page_size < 1:
         raise ValueError("a page of %d bytes does not hold rows of d = %d" % (size, d))
     _int32("page_table", page_table, 2, at)
     _int32("kv_len", kv_len, 1, at)
@@ -139,7 +139,7 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at):
         if cu_seqlens.shape[0] != N + 1:
             raise ValueError("cu_seqlens must have one entry more than there are sequences")
         cu = cu_seqlens.data_ptr()
-    elif n_tokens and (N == 0 or n_tokens % N):
+    elif n_tokens < 0 or n_tokens and (N == 0 or n_tokens % N):
         raise ValueError("without cu_seqlens every sequence has the same number of tokens")
     scale = 0
     if kv_scale is not None:
@@ -181,6 +181,8 @@ def gdn_kv_pages(n_pages, heads, page_size, d, device=None):
 
 def gdn_rope_table(n_pos, d_rot, base=10000.0, device=None):
     """(cos, sin), fp32 [n_pos, d_rot / 2], of position * base^(-2 i / d_rot), formed in fp64."""
+    if n_pos < 0 or d_rot < 0 or d_rot % 2:
+        raise ValueError("a table has n_pos >= 0 positions of d_rot / 2 pairs")
     device = "cuda" if device is None else device
     f = torch.exp(torch.arange(0, d_rot, 2, dtype=torch.float64, device=device)
                   * (-math.log(base) / max(d_rot, 1)))
@@ -192,6 +194,8 @@ def gdn_rope_axes(sections, interleave=False):
     """The axis of each pair, for `axes`: sections[a] pairs go by axis a, in runs, or dealt out
     in turn as long as an axis has some left."""
     left = list(sections)
+    if any(n < 0 for n in left):
+        raise ValueError("sections are numbers of pairs")
     if not interleave:
         return bytes(a for a, n in enumerate(left) for _ in range(n))
     out = []
@@ -214,7 +218,7 @@ def _rope(q, k, cos, sin, pos, axes, flags, out, check, what):
     if (k is None) != (ko is None):
         raise ValueError("out must hold a place for k where there is a k, and None elsewhere")
     if k is not None:
-        Hk = k.shape[1]
+        Hk = k.shape[1] if k.dim() == 4 else 0
         rk, rko = _rows4("k", k, q, Hk, at), _rows4("out[1]", ko, q, Hk, at)
     _call(load().gdn_rope, what, at, check, _rows4("q", q, q, Hq, at),
           _rows4("out[0]", qo, q, Hq, at), rk, rko, B, T, d,
@@ -264,7 +268,7 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     if q is not None:
         if out is None:
             out = torch.empty_like(q)
-        Hq = q.shape[1]
+        Hq = q.shape[1] if q.dim() == 3 else 0
         rq, rqo = _rows3("q", q, Hq, n, d, dtype, at), _rows3("out", out, Hq, n, d, dtype, at)
     if cos is not None:
         rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,), at)
@@ -278,6 +282,8 @@ def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_s
                 dtype=torch.bfloat16, out=None, check=False):
     """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
     they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
+    if dtype not in _DT:
+        raise ValueError("k and v are read as bf16 or fp32")
     at = _device("pages", pages)
     kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at)
     if out is None:

@@ -63,3 +63,31 @@ def test_rope_writes_both_or_one(calls):
         with pytest.raises(ValueError):
             gdn.gdn_rope(q, a, *at, out=(q, b))
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("call", [
+    lambda: gdn.gdn_kv_read(*cache(), 4, 0),
+    lambda: gdn.gdn_kv_read(*cache(), 4, -64),
+    lambda: gdn.gdn_kv_read(*cache(), -2, 64),
+    lambda: gdn.gdn_kv_read(*cache(), 4, 64, dtype=torch.float16),
+    lambda: gdn.gdn_kv_attn(on(4, 4, 0), *cache()),
+    lambda: gdn.gdn_kv_attn(on(4, 4, 64), on(5, 2, 0, dtype=torch.uint8), *cache()[1:]),
+    lambda: append(q=on(4), out=on(4)),
+    lambda: append(q=on(4, 4, 1, 64), out=on(4, 4, 1, 64)),
+    lambda: gdn.gdn_rope(on(2, 4, 3, 64), on(3), *(TURN["cos"], TURN["sin"], on(3, dtype=i32)),
+                         out=(on(2, 4, 3, 64), on(3))),
+    lambda: gdn.gdn_rope_table(4, 63, device="cpu"),
+    lambda: gdn.gdn_rope_table(4, -2, device="cpu"),
+    lambda: gdn.gdn_rope_table(-1, 64, device="cpu"),
+    lambda: gdn.gdn_rope_axes((8, -1, 8)),
+], ids=lambda c: None)
+def test_refusals_are_value_errors(calls, call):
+    with pytest.raises(ValueError):
+        call()
+    assert not calls
+
+
+def test_negative_sections_dealt_out_end():
+    # (dealing out in turn never came to an end: nothing was left to run out)
+    with pytest.raises(ValueError):
+        gdn.gdn_rope_axes((2, -1), interleave=True)
