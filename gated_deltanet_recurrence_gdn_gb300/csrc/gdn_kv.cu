@@ -226,7 +226,8 @@ gdn_status check_kv(const gdn_kv *kv, Kv *out) {
     if (!kv->pages || !kv->page_table || !kv->kv_len || kv->n_pages < 1 || kv->max_pages < 1 ||
         kv->heads < 1)
         return GDN_ERR_INVALID_ARG;
-    if (gdn_kv_page_bytes(kv->page_size, kv->d) == 0 || kv->heads > 65535 || kv->N > (1 << 24))
+    if (gdn_kv_page_bytes(kv->page_size, kv->d) == 0 || kv->heads > 65535 || kv->N > (1 << 24) ||
+        kv->n_tokens > kMaxTokens)
         return GDN_ERR_UNSUPPORTED;
     if (!kv->cu_seqlens && kv->n_tokens % kv->N) return GDN_ERR_INVALID_ARG;
     const void *ptrs[] = {kv->head_scale, kv->page_table, kv->kv_len, kv->cu_seqlens};
@@ -235,7 +236,7 @@ gdn_status check_kv(const gdn_kv *kv, Kv *out) {
     if (!aligned16(kv->pages)) return GDN_ERR_ALIGNMENT;
     int shift = 4;
     while ((1 << shift) < kv->page_size) ++shift;
-    if ((long long)kv->max_pages << shift > 0x7fffff00LL) return GDN_ERR_UNSUPPORTED;
+    if ((long long)kv->max_pages << shift > kMaxTokens) return GDN_ERR_UNSUPPORTED;
     *out = Kv{static_cast<uint8_t *>(kv->pages), kv->head_scale, kv->page_table, kv->kv_len,
               kv->cu_seqlens, kv->n_pages, shift, kv->heads, kv->d, kv->N, kv->max_pages,
               kv->n_tokens, (long long)kv->table_stride};

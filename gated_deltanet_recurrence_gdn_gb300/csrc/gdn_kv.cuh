@@ -15,6 +15,7 @@ namespace kv {
 
 constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 128;   // d_rot / 2 at d = 256
+constexpr long long kMaxTokens = 0x7fffff00;   // so that a grid's last tokens fit an int
 
 // ------------------------------------------------------------------- rows
 

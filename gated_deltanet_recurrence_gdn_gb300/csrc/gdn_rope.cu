@@ -124,7 +124,7 @@ extern "C" gdn_status gdn_rope(const gdn_rows *q, const gdn_rows *q_out, const g
         return GDN_ERR_INVALID_ARG;
     if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if (d < 16 || d % 16 || d > 256) return GDN_ERR_UNSUPPORTED;
-    if ((long long)B * T > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if ((long long)B * T > kMaxTokens) return GDN_ERR_UNSUPPORTED;
     if (B == 0 || T == 0) return GDN_OK;
     gdn_status rc;
     const gdn_rows *rows[] = {q, q_out, k, k_out};

@@ -37,6 +37,9 @@
  * 9/8 d bytes hold a token's key and value of one head (144 at d = 128).
  * Place p of sequence b lies in page page_table[b * table_stride + p / page_size], row
  * p % page_size.  What lies in rows that no sequence counts is never used.
+ *
+ * Sizes.  A call has at most 2^31 - 256 tokens, and a page table as many places a
+ * sequence (GDN_ERR_UNSUPPORTED).
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H
