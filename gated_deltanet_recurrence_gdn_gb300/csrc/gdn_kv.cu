@@ -267,10 +267,14 @@ gdn_status gdn_kv_append(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v,
     Kv dev;
     gdn_status rc = check_kv(kv, &dev);
     if (rc != GDN_OK) return rc;
-    if ((rc = check_rows(k, dt)) != GDN_OK || (rc = check_rows(v, dt)) != GDN_OK) return rc;
+    if ((rc = check_rows(k, dt, true)) != GDN_OK ||
+        (rc = check_rows(v, dt, true)) != GDN_OK)
+        return rc;
     if (k->heads != kv->heads || v->heads != kv->heads) return GDN_ERR_INVALID_ARG;
     if (q) {
-        if ((rc = check_rows(q, dt)) != GDN_OK || (rc = check_rows(q_out, dt)) != GDN_OK) return rc;
+        if ((rc = check_rows(q, dt, true)) != GDN_OK ||
+            (rc = check_rows(q_out, dt, true)) != GDN_OK)
+            return rc;
         if (q->heads != q_out->heads) return GDN_ERR_INVALID_ARG;
     }
     Rotary r{};
@@ -291,7 +295,9 @@ gdn_status gdn_kv_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, g
     Kv dev;
     gdn_status rc = check_kv(kv, &dev);
     if (rc != GDN_OK) return rc;
-    if ((rc = check_rows(k, dt)) != GDN_OK || (rc = check_rows(v, dt)) != GDN_OK) return rc;
+    if ((rc = check_rows(k, dt, true)) != GDN_OK ||
+        (rc = check_rows(v, dt, true)) != GDN_OK)
+        return rc;
     if (k->heads != kv->heads || v->heads != kv->heads) return GDN_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dt == GDN_BF16 ? launch_read<__nv_bfloat16>(dev, k, v, st)

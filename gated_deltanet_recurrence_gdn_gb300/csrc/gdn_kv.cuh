@@ -280,8 +280,8 @@ struct Kv {
 
 // Host side: checks a gdn_kv (n_tokens > 0 and N > 0 known), fills the kernel's form.
 gdn_status check_kv(const gdn_kv *kv, Kv *out);
-// Checks rows of `d` elements of `dt` with `heads` heads.
-gdn_status check_rows(const gdn_rows *r, gdn_dtype dt);
+// Checks rows of elements of `dt`; packed: of packed tokens, which have no stride_seq.
+gdn_status check_rows(const gdn_rows *r, gdn_dtype dt, bool packed);
 // Checks a rotation over rows of d elements; unit = required divisor of d_rot.
 gdn_status check_rotary(const gdn_rotary *r, int d, bool append, Rotary *out);
 

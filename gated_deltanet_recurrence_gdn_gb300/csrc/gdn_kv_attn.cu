@@ -828,7 +828,9 @@ extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn
     AttnArgs a{};
     gdn_status rc = check_kv(kv, &a.kv);
     if (rc != GDN_OK) return rc;
-    if ((rc = check_rows(q, dt)) != GDN_OK || (rc = check_rows(o, dt)) != GDN_OK) return rc;
+    if ((rc = check_rows(q, dt, true)) != GDN_OK ||
+        (rc = check_rows(o, dt, true)) != GDN_OK)
+        return rc;
     if (q->heads != o->heads || q->heads % kv->heads) return GDN_ERR_INVALID_ARG;
     if (!aligned4(lse)) return GDN_ERR_ALIGNMENT;
     if ((long long)kv->n_tokens * q->heads > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;

@@ -75,11 +75,12 @@ cudaError_t launch(const gdn_rows *q, const gdn_rows *qo, const gdn_rows *k, con
 
 }  // namespace
 
-gdn_status check_rows(const gdn_rows *r, gdn_dtype dt) {
+gdn_status check_rows(const gdn_rows *r, gdn_dtype dt, bool packed) {
     if (!r || !r->data || r->heads < 1) return GDN_ERR_INVALID_ARG;
     if (r->heads > 65535) return GDN_ERR_UNSUPPORTED;
     const int e = dt == GDN_BF16 ? 8 : 4;   // elements in 16 bytes
-    if (!aligned16(r->data) || r->stride_seq % e || r->stride_head % e || r->stride_tok % e)
+    if (!aligned16(r->data) || (!packed && r->stride_seq % e) || r->stride_head % e ||
+        r->stride_tok % e)
         return GDN_ERR_ALIGNMENT;
     return GDN_OK;
 }
@@ -129,7 +130,7 @@ extern "C" gdn_status gdn_rope(const gdn_rows *q, const gdn_rows *q_out, const g
     gdn_status rc;
     const gdn_rows *rows[] = {q, q_out, k, k_out};
     for (const gdn_rows *r : rows)
-        if (r && (rc = check_rows(r, dt)) != GDN_OK) return rc;
+        if (r && (rc = check_rows(r, dt, false)) != GDN_OK) return rc;
     if (q->heads != q_out->heads || (k && k->heads != k_out->heads)) return GDN_ERR_INVALID_ARG;
     Rotary r{};
     if ((rc = check_rotary(rot, d, false, &r)) != GDN_OK) return rc;

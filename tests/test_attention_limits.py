@@ -22,3 +22,15 @@ def test_cache_tokens_of_the_last_block_fit_an_int(lib, n):  # noqa: F811
     assert lib.gdn_kv_append(ref(c), ref(rows(2)), ref(rows(2)), None, None, None, 1, None) == un
     assert lib.gdn_kv_read(ref(c), ref(rows(2)), ref(rows(2)), 1, None) == un
     assert lib.gdn_kv_attn(ref(c), ref(rows(2)), ref(rows(2)), None, 9, 1, 1.0, 0, 1, 1, None) == un
+
+
+def test_packed_tokens_have_no_stride_seq(lib):  # noqa: F811
+    # (rows of packed tokens ignore it, so it may be anything; what else is wrong is still found)
+    al, bad = gdn.GDN_ERR_ALIGNMENT, gdn.GDN_ERR_INVALID_ARG
+    r, q3 = rows(2, seq=3), rows(3, seq=3)
+    assert lib.gdn_kv_append(ref(kv()), ref(r), ref(r), ref(rows(4, seq=5)), ref(rows(5, seq=7)), None, 1,
+                             None) == bad
+    assert lib.gdn_kv_read(ref(kv()), ref(r), ref(q3), 1, None) == bad
+    assert lib.gdn_kv_attn(ref(kv()), ref(q3), ref(q3), None, 9, 1, 1.0, 0, 1, 1, None) == bad
+    assert lib.gdn_kv_read(ref(kv()), ref(rows(2, tok=132, seq=3)), ref(r), 1, None) == al
+    assert lib.gdn_rope(ref(r), ref(r), None, None, 1, 2, 128, ref(rotary()), 1, None) == al
