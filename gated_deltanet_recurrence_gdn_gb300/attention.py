@@ -305,8 +305,10 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
 
     The cache arguments as in gdn_kv_append, after the append.  max_len and max_new: bounds on
     kv_len and on a sequence's tokens in this call, known on the host (default: what the page
-    table and q can hold); they plan the launch.  scale: default d^-1/2.  window: a token sees
-    the last `window` places up to its own (0: all)."""
+    table holds, and the same number of tokens each, or with cu_seqlens all of the call's); they
+    plan the launch and choose its kernel.  A decode step that carries cu_seqlens should pass
+    max_new=1: without it the call is planned for one sequence that has all the tokens.  scale:
+    default d^-1/2.  window: a token sees the last `window` places up to its own (0: all)."""
     if q.dtype not in _DT or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
     at = _device("q", q)

@@ -2,9 +2,9 @@
 // tokens, drafts, fp32 I/O).
 //
 // S = Q K^T and O = P V with one pass over the cache, the running maximum and
-// sum of the softmax kept per row.  Reading the cache bounds it, and next to
-// that the instructions that turn 4-bit numbers into fp16 operands: at 144 bytes
-// a (token, head) of d = 128 and 6.8 TB/s an SM has 3 issue slots per element.
+// sum of the softmax kept per row.  Its floor is reading the cache, and next to
+// that stand the instructions that turn 4-bit numbers into fp16 operands: at 144
+// bytes a (token, head) of d = 128 and 6.8 TB/s an SM has 3 issue slots per element.
 //
 // - A tile (256 tokens; 128 at d = 256) is copied into a ring of shared memory by
 //   bulk copies, one per page and part of it, each warp issuing every eighth
@@ -36,11 +36,14 @@
 //   adds them in a fixed order.
 //
 // Measured, join included (bf16, d = 128, one token a sequence, pages read cold):
-//   256 sequences of 8000 to 8192, 8 heads:    469 us, 5.1 TB/s (2.39 GB);
-//   64 ragged ones of 128 to 16384, 8 heads:   162 us, 4.1 TB/s (665 MB);
+//   256 sequences of 8000 to 8192, 8 heads:    464 us, 5.1 TB/s (2.39 GB);
+//   64 ragged ones of 128 to 16384, 8 heads:   163 us, 4.1 TB/s (665 MB);
 //   one of 131072, 4 heads:                     33 us, 2.3 TB/s (75 MB).
-// Issue slots bound the first (about 340 instructions per 16 tokens and warp, 65 %
-// of the slots taken, DRAM at 75 %).  The last one's first copy starts 5 us in: the
+// No unit is full in the first two: issue slots 66 and 63 % (about 340 instructions per
+// 16 tokens and warp), DRAM 5.2 and 4.3 TB/s without the join, 77 and 63 % of a copy's.
+// Registers and the ring allow 16 warps an SM, and of the 6 cycles between two
+// instructions of a warp 1.4 go by for the fixed latency of the one before, 1.0 for other
+// warps' turns and 0.65 for a pipe.  The last one's first copy starts 5 us in: the
 // division of the work 2, its place in it 2, the page numbers 1; the join takes 5.
 #include "gdn_kv_attn.cuh"
 
@@ -52,9 +55,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;                    // tokens of a warp's step
 // Rows of a key/value head above which the products go to tcgen05 (gdn_kv_attn_tc.cu),
-// whose time hardly depends on them up to 128: 20 rows of 64 ragged sequences take 450 us
-// there and 478 in three passes of 8 rows here, in a window of 4096 places 38 and 44; up
-// to 16 rows take 325 here.  (Some hundred places: 17.5 there, 12.3 here.)
+// whose time hardly depends on them up to 128: 20 rows of 64 ragged sequences take 447 us
+// there and 474 in three passes of 8 rows here, 16 sequences in a window of 4096 places 34
+// and 42; up to 16 rows take 329 here.  (Some hundred places, which the rule does not look
+// at: 16 sequences of 200 to 800 take 25 and 26 us, 64 of 128 to 512 take 82 there and 63
+// here.)
 constexpr int kMany = 16;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves

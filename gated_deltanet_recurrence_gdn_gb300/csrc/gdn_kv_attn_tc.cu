@@ -31,7 +31,7 @@
 // dense bf16 product's rate; 3300 cycles a tile where its products alone take
 // 2560: scores by halves, n = 64, take 48 cycles a product instead of 32, but
 // let products and softmax overlap: with whole tiles 10 % more).  Drafts of 5
-// tokens in a window of 4096, 16 sequences: 33.5 us, in 20 rows of the 256: a tile takes
+// tokens in a window of 4096, 16 sequences: 34 us, in 20 rows of the 256: a tile takes
 // 3000 to 3500 cycles there too, bound by the chain from scores to probabilities to
 // the next scores.
 #include "gdn_kv_attn.cuh"

@@ -23,7 +23,8 @@
  * kv_len[b] counts the sequence's tokens INCLUDING these n_b, so the j-th of
  * them lies at place kv_len[b] - n_b + j.  A token whose place is negative (an
  * idle slot of a batch: kv_len[b] = 0) is not written, reads back as zero, and
- * sees nothing.
+ * sees nothing; its query is turned like any other, by a position that has to
+ * lie in the table.
  *
  * Cache.  `pages` is [n_pages][H][gdn_kv_page_bytes(page_size, d)] bytes.  The
  * block of one (page, head) holds, in this order,
@@ -129,7 +130,8 @@ gdn_status gdn_kv_append(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v,
                          gdn_dtype dt, void *stream);
 
 /* Reads the call's tokens back from the cache into k and v, as the values they
- * stand for, rounded once to dt. */
+ * stand for: e2m1 * e4m3 is exact, its product with the head's scale is rounded
+ * to fp32, and that to dt. */
 gdn_status gdn_kv_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, gdn_dtype dt,
                        void *stream);
 
@@ -144,13 +146,17 @@ gdn_status gdn_kv_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, g
  *             exp(scale * q . k_t), or NULL.
  *   max_len, max_new   HOST bounds on kv_len and on the tokens of one sequence,
  *             from which the launch is planned (a larger device value is
- *             reported as GDN_ERR_INVALID_ARG by gdn_sync_check()).
+ *             reported as GDN_ERR_INVALID_ARG by gdn_sync_check()).  max_new
+ *             also chooses the kernel for the whole call (bf16, d <= 128: above
+ *             16 rows max_new * Hq / H the one for many rows), so a bound far
+ *             above what the sequences have costs time.
  * The cache's numbers enter the tensor cores exactly (e2m1 * e4m3 fits fp16);
  * with bf16 rows the probabilities are rounded to fp16 (11 bits, down to 2^-22
- * of the row's largest at least), with fp32 rows queries and probabilities are
- * carried as two fp16 numbers each.  Sums, maxima and outputs are fp32 until o
- * is rounded.  Scratch for splitting long sequences
- * comes from the library's pool.  The same inputs give the same bits.
+ * of the row's largest at least; the kernel for many rows leaves out what lies
+ * below 2^-33 of it), with fp32 rows queries and probabilities are carried as two
+ * fp16 numbers each.  Sums, maxima and outputs are fp32 until o is rounded.
+ * Scratch for splitting long sequences comes from the library's pool.  The same
+ * inputs give the same bits.
  */
 enum { GDN_ATTN_CAUSAL = 1 };
 gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, float *lse,
