@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                             }
                             if (!there) continue;
                             if (complete) store8(po + 32 * c + e, v);
-                            else if (a.part_ok(slot * kRows + mine, kRows)) store8(pp + 32 * c + e, v);
+                            else if (a.part_ok(slot * kRows + mine, kRows))
+                                store8(pp + 32 * c + e, v);
                         }
                     }
                     if (there) {

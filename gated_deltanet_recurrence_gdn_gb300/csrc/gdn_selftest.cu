@@ -143,8 +143,8 @@ extern "C" gdn_status gdn_selftest_ring(int complete, long long limit, int *resu
     if (!err || cudaGetSymbolAddress(reinterpret_cast<void **>(&out), gdn::g_ring_out) !=
                     cudaSuccess)
         return GDN_ERR_CUDA;
-    gdn::k_ring_selftest<<<1, gdn::kRingThreads, gdn::kRingSmem, st>>>(complete, static_cast<uint32_t>(limit),
-                                                          err, out);
+    gdn::k_ring_selftest<<<1, gdn::kRingThreads, gdn::kRingSmem, st>>>(
+        complete, static_cast<uint32_t>(limit), err, out);
     gdn::count_launch();
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     if (cudaMemcpyAsync(result, out, sizeof(gdn::g_ring_out), cudaMemcpyDeviceToHost, st) !=
