@@ -16,6 +16,8 @@ The softmax-attention layers of a hybrid decoder (``attention.py``,
     q = gdn_kv_append(pages, k, v, page_table, kv_len, q=q, cos=cos, sin=sin, pos=pos)
     o = gdn_kv_attn(q, pages, page_table, kv_len)
 
+(``gdn_kv8_append``, ``gdn_kv8_attn``: the same over a cache in 8 bits.)
+
 Layouts follow ``include/gdn.h``: dense q, k [B,H,T,d_k], v [B,H,T,d_v]; packed
 q, k [H,T_total,d_k], v [H,T_total,d_v]; gates fp32; h0 / hT [.., H, d_v, d_k]
 fp32; q, k, v share one dtype (bf16 or fp32), which is also the dtype of o.
@@ -88,6 +90,10 @@ ABI = [
     ("gdn_kv_append", _i, [_vp] * 6 + [_i, _vp]),
     ("gdn_kv_read", _i, [_vp] * 3 + [_i, _vp]),
     ("gdn_kv_attn", _i, [_vp] * 4 + [_i] * 2 + [ctypes.c_float, _i, ctypes.c_uint, _i, _vp]),
+    ("gdn_kv8_page_bytes", ctypes.c_int64, [_i] * 2),
+    ("gdn_kv8_append", _i, [_vp] * 6 + [_i, _vp]),
+    ("gdn_kv8_read", _i, [_vp] * 3 + [_i, _vp]),
+    ("gdn_kv8_attn", _i, [_vp] * 4 + [_i] * 2 + [ctypes.c_float, _i, ctypes.c_uint, _i, _vp]),
     ("gdn_selftest_ring", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
     ("gdn_selftest_wait", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
 ]
@@ -481,5 +487,7 @@ class use_impl:
         return False
 
 
-from .attention import (gdn_kv_append, gdn_kv_attn, gdn_kv_page_bytes, gdn_kv_pages,  # noqa: E402,F401
-                        gdn_kv_read, gdn_rope, gdn_rope_axes, gdn_rope_bwd, gdn_rope_table)
+from .attention import (gdn_kv8_append, gdn_kv8_attn, gdn_kv8_page_bytes,  # noqa: E402,F401
+                        gdn_kv8_pages, gdn_kv8_read, gdn_kv_append, gdn_kv_attn, gdn_kv_page_bytes,
+                        gdn_kv_pages, gdn_kv_read, gdn_rope, gdn_rope_axes, gdn_rope_bwd,
+                        gdn_rope_table)

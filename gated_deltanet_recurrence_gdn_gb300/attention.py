@@ -1,6 +1,6 @@
 """Binding of the softmax-attention layers of a hybrid decoder
-(``include/gdn_attn.h``): rotary positions, a paged key/value cache held in 4
-bits, and attention over that cache.
+(``include/gdn_attn.h``): rotary positions, a paged key/value cache held in 4 or
+8 bits, and attention over that cache.
 
 Rows are found by strides: q, k, v and o may be any views whose last dimension
 is contiguous ([tokens, heads, d], or a transposed [heads, tokens, d]).  The
@@ -118,15 +118,28 @@ def _rotary(cos, sin, pos, axes, flags, shape, at):
                         2 * table[1], pos.shape[0] if lead else 1, flags)
 
 
-def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at):
+def _page_size4(size, d):
+    """Tokens of a page whose block has `size` bytes; 0 if no page has."""
+    n = size * 8 // (9 * d) if d > 0 else 0
+    return n if n * d * 9 == size * 8 else 0
+
+
+def _page_size8(size, d):
+    n = (size - 16) // (2 * d) if d > 0 else 0
+    if n > 128:
+        n = (size - 32) // (2 * d)
+    return n if n > 0 and 2 * n * d + 16 * max(1, n // 128) == size else 0
+
+
+def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at, page_size_of=_page_size4):
     """The packed gdn_kv, and the cache's heads and page size."""
     if pages.dim() != 3 or pages.dtype != _u8 or pages.get_device() != at or \
             not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 tensor [n_pages, heads, page bytes] on "
                          "the call's device")
     n_pages, heads, size = pages.shape
-    page_size = size * 8 // (9 * d) if d > 0 else 0
-    if page_size * d * 9 != size * 8 or page_size < 1:
+    page_size = page_size_of(size, d)
+    if page_size < 1:
         raise ValueError("a page of %d bytes does not hold rows of d = %d" % (size, d))
     _int32("page_table", page_table, 2, at)
     _int32("kv_len", kv_len, 1, at)
@@ -244,6 +257,20 @@ def gdn_rope_bwd(dq, dk, cos, sin, pos, *, axes=None, adjacent=False, out=None, 
                  "gdn_rope_bwd")
 
 
+def gdn_kv8_page_bytes(page_size: int, d: int) -> int:
+    """Bytes of one page of one head in 8 bits; 0 where the sizes are not supported."""
+    return int(load().gdn_kv8_page_bytes(int(page_size), int(d)))
+
+
+def gdn_kv8_pages(n_pages, heads, page_size, d, device=None):
+    """A new cache in 8 bits: uint8 [n_pages, heads, page bytes], zeroed."""
+    size = gdn_kv8_page_bytes(page_size, d)
+    if size == 0:
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and d 64, 128 or 256")
+    return torch.zeros((n_pages, heads, size), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
 def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, kv_scale=None,
                   cos=None, sin=None, pos=None, axes=None, adjacent=False, out=None, check=False):
     """Appends k, v [tokens, heads, d] to the cache, k turned by its positions (where cos, sin
@@ -253,12 +280,27 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     pages: the cache (gdn_kv_pages), written in place; page_table int32 [N, pages]; kv_len int32
     [N], the sequences' tokens with the new ones; cu_seqlens int32 [N + 1] or None for the same
     number of new tokens each; kv_scale fp32 [2, heads]: a further scale per head."""
+    return _append("gdn_kv_append", _page_size4, pages, k, v, page_table, kv_len, q, cu_seqlens,
+                   kv_scale, cos, sin, pos, axes, adjacent, out, check)
+
+
+def gdn_kv8_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, kv_scale=None,
+                   cos=None, sin=None, pos=None, axes=None, adjacent=False, out=None, check=False):
+    """gdn_kv_append to a cache in 8 bits (gdn_kv8_pages).  A block of 16 places has one exponent
+    for its keys and one for its values: where a new token is too large for it, the block's other
+    rows are rounded again under the larger one."""
+    return _append("gdn_kv8_append", _page_size8, pages, k, v, page_table, kv_len, q, cu_seqlens,
+                   kv_scale, cos, sin, pos, axes, adjacent, out, check)
+
+
+def _append(name, page_size_of, pages, k, v, page_table, kv_len, q, cu_seqlens, kv_scale, cos, sin,
+            pos, axes, adjacent, out, check):
     if k.dtype not in _DT or k.dim() != 3:
         raise ValueError("k must be [tokens, heads, d], bf16 or fp32")
     at = _device("k", k)
     n, _, d = k.shape
     dtype = k.dtype
-    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at)
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at, page_size_of)
     rq = rqo = rot = None
     if cos is None or sin is None or pos is None:
         if adjacent or any(x is not None for x in (cos, sin, pos, axes)):
@@ -272,7 +314,7 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
         rq, rqo = _rows3("q", q, Hq, n, d, dtype, at), _rows3("out", out, Hq, n, d, dtype, at)
     if cos is not None:
         rot = _rotary(cos, sin, pos, axes, GDN_ROPE_ADJACENT if adjacent else 0, (n,), at)
-    _call(load().gdn_kv_append, "gdn_kv_append", at, check, kv,
+    _call(getattr(load(), name), name, at, check, kv,
           _rows3("k", k, heads, n, d, dtype, at), _rows3("v", v, heads, n, d, dtype, at), rq, rqo,
           rot, _DT[dtype])
     return out if q is not None else None
@@ -282,16 +324,30 @@ def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_s
                 dtype=torch.bfloat16, out=None, check=False):
     """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
     they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
+    return _read("gdn_kv_read", _page_size4, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
+                 kv_scale, dtype, out, check)
+
+
+def gdn_kv8_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_scale=None,
+                 dtype=torch.bfloat16, out=None, check=False):
+    """gdn_kv_read from a cache in 8 bits."""
+    return _read("gdn_kv8_read", _page_size8, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
+                 kv_scale, dtype, out, check)
+
+
+def _read(name, page_size_of, pages, page_table, kv_len, n_tokens, d, cu_seqlens, kv_scale, dtype,
+          out, check):
     if dtype not in _DT:
         raise ValueError("k and v are read as bf16 or fp32")
     at = _device("pages", pages)
-    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at)
+    kv, heads, _ = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at,
+                       page_size_of)
     if out is None:
         k = torch.empty((n_tokens, heads, d), dtype=dtype, device=pages.device)
         v = torch.empty_like(k)
     else:
         k, v = out
-    _call(load().gdn_kv_read, "gdn_kv_read", at, check, kv,
+    _call(getattr(load(), name), name, at, check, kv,
           _rows3("out", k, heads, n_tokens, d, dtype, at),
           _rows3("out", v, heads, n_tokens, d, dtype, at), _DT[dtype])
     return k, v
@@ -309,12 +365,27 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
     plan the launch and choose its kernel.  A decode step that carries cu_seqlens should pass
     max_new=1: without it the call is planned for one sequence that has all the tokens.  scale:
     default d^-1/2.  window: a token sees the last `window` places up to its own (0: all)."""
+    return _attn("gdn_kv_attn", _page_size4, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
+                 max_len, max_new, scale, causal, window, out, return_lse, check)
+
+
+def gdn_kv8_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None, max_len=None,
+                 max_new=None, scale=None, causal=True, window=0, out=None, return_lse=False,
+                 check=False):
+    """gdn_kv_attn over a cache in 8 bits."""
+    return _attn("gdn_kv8_attn", _page_size8, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
+                 max_len, max_new, scale, causal, window, out, return_lse, check)
+
+
+def _attn(name, page_size_of, q, pages, page_table, kv_len, cu_seqlens, kv_scale, max_len, max_new,
+          scale, causal, window, out, return_lse, check):
     if q.dtype not in _DT or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
     at = _device("q", q)
     n, Hq, d = q.shape
     dtype = q.dtype
-    kv, _, page_size = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at)
+    kv, _, page_size = _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n, d, at,
+                           page_size_of)
     if out is None:
         out = torch.empty_like(q)
     lse = torch.empty((n, Hq), dtype=_f32, device=q.device) if return_lse else None
@@ -322,7 +393,7 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
         max_len = page_table.shape[1] * page_size
     if max_new is None:
         max_new = n if cu_seqlens is not None else n // max(kv_len.shape[0], 1)
-    _call(load().gdn_kv_attn, "gdn_kv_attn", at, check, kv, _rows3("q", q, Hq, n, d, dtype, at),
+    _call(getattr(load(), name), name, at, check, kv, _rows3("q", q, Hq, n, d, dtype, at),
           _rows3("out", out, Hq, n, d, dtype, at), None if lse is None else lse.data_ptr(),
           min(max_len, _INT_MAX), min(max_new, _INT_MAX), d ** -0.5 if scale is None else scale,
           min(window, _INT_MAX), GDN_ATTN_CAUSAL if causal else 0, _DT[dtype])

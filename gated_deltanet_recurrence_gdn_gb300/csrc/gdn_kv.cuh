@@ -1,6 +1,6 @@
 // gdn_kv.cuh -- what the attention-layer kernels (gdn_rope.cu, gdn_kv.cu,
-// gdn_kv_attn.cu) share: rows and their strides, the rotation of a unit of
-// pairs, the 4-bit page format, and where a sequence's tokens lie.
+// gdn_kv8.cu, gdn_kv_attn.cu) share: rows and their strides, the rotation of a
+// unit of pairs, the page formats, and where a sequence's tokens lie.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -194,7 +194,7 @@ __device__ __forceinline__ void turn(bool adjacent, const float (&c)[8], const f
 
 // -------------------------------------------------------------- page format
 
-// Byte offsets inside the block of one (page, head).
+// Byte offsets inside the block of one (page, head), 4 bits.
 __host__ __device__ __forceinline__ int block_bytes(int page, int d) { return page * d * 9 / 8; }
 __host__ __device__ __forceinline__ int k_code_at(int, int d, int row) { return row * (d / 2); }
 __host__ __device__ __forceinline__ int v_code_at(int page, int d, int row) {
@@ -207,7 +207,35 @@ __host__ __device__ __forceinline__ int v_scale_at(int page, int d, int row) {
     return page * d + (page + row) * (d / 16);
 }
 
-// Kernel-side form of gdn_kv.
+// The two formats of a cache: 4 bits with a scale per 16 neighbours of a row, and 8 bits
+// with an exponent for 16 places of a head.
+struct Fmt4 {
+    static constexpr int kBits = 4;
+    __host__ __device__ static __forceinline__ int block_bytes(int page, int d) {
+        return kv::block_bytes(page, d);
+    }
+};
+struct Fmt8 {
+    static constexpr int kBits = 8;
+    static constexpr int kMostExponent = 22;     // a byte e stands for 2^(e - 15)
+    static constexpr int kBlock = 16;            // places that share one
+    static constexpr int kGroup = 128;           // places whose exponents lie in 16 bytes
+    __host__ __device__ static __forceinline__ int block_bytes(int page, int d) {
+        return 2 * page * d + 16 * (page > kGroup ? page / kGroup : 1);
+    }
+    // codes of a key row; a value row lies `page` rows behind
+    __host__ __device__ static __forceinline__ int code_at(int d, int row) { return row * d; }
+    // the 16 bytes with a row's exponents: 8 of keys, 8 of values
+    __host__ __device__ static __forceinline__ int exponents_at(int page, int d, int row) {
+        return 2 * page * d + 16 * (row / kGroup);
+    }
+    // the byte of a row's block among the eight
+    __host__ __device__ static __forceinline__ int exponent_of(int row) {
+        return row % kGroup / kBlock;
+    }
+};
+
+// Kernel-side form of gdn_kv and gdn_kv8.
 struct Kv {
     uint8_t *pages;
     const float *head_scale;
@@ -216,12 +244,14 @@ struct Kv {
     long long table_stride;
 
     __device__ __forceinline__ int page_size() const { return 1 << page_shift; }
+    template <typename F = Fmt4>
     __device__ __forceinline__ long long block(int page, int h) const {
-        return ((long long)page * H + h) * block_bytes(1 << page_shift, d);
+        return ((long long)page * H + h) * F::block_bytes(1 << page_shift, d);
     }
     // (the bounds-check build: `bytes` bytes from `at` in a page's block lie in the pool)
+    template <typename F = Fmt4>
     __device__ __forceinline__ bool bytes_ok(int page, int h, int at, int bytes) const {
-        return GDN_IDX_OK(h, 1, H) && GDN_IDX_OK(at, bytes, block_bytes(1 << page_shift, d)) &&
+        return GDN_IDX_OK(h, 1, H) && GDN_IDX_OK(at, bytes, F::block_bytes(1 << page_shift, d)) &&
                GDN_IDX_OK(page, 1, n_pages);
     }
     // Page of place p of sequence b as the table has it, and the same checked: -1 with
@@ -285,7 +315,7 @@ gdn_status check_rows(const gdn_rows *r, gdn_dtype dt, bool packed);
 // Checks a rotation over rows of d elements; unit = required divisor of d_rot.
 gdn_status check_rotary(const gdn_rotary *r, int d, bool append, Rotary *out);
 
-// ------------------------------------------------------------ 4-bit numbers
+// --------------------------------------------------- 4-bit and 8-bit numbers
 
 // e4m3 byte of x >= 0 (or NaN), to nearest even, at most 448.
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
@@ -325,6 +355,49 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
         "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(w));
+}
+
+// The four e4m3 bytes of w as fp16x2, two each.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t (&r)[2]) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(r[0]), "=r"(r[1])
+        : "r"(w));
+}
+// Four numbers as e4m3 bytes, to nearest even; magnitudes above 448 become 448.
+__device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+// The same of four fp16 numbers.
+__device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t ab, uint32_t cd) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "r"(ab), "r"(cd));
+    return r;
+}
+// Nonzero (0x80 in its byte) where a byte of w is an e4m3 NaN.
+__device__ __forceinline__ uint32_t e4m3x4_nan(uint32_t w) {
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// 2^(e - 15) of an exponent byte e <= 22 as an fp16 number (e = 0 is a subnormal one).
+__device__ __forceinline__ uint32_t exponent_f16(uint32_t e) { return max(e << 10, 0x200u); }
+__device__ __forceinline__ __half2 exponent_f16x2(uint32_t e) {
+    const uint32_t two = __byte_perm(exponent_f16(e), 0, 0x1010);
+    return *reinterpret_cast<const __half2 *>(&two);
+}
+__device__ __forceinline__ float exponent_f32(uint32_t e) {
+    return __uint_as_float((e + 112u) << 23);
 }
 
 // max that keeps a NaN of either side

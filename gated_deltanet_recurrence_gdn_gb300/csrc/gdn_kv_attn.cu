@@ -98,6 +98,12 @@ __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t
 // quarter warp reads of K differ in parity, which keeps its banks apart.
 __device__ __forceinline__ int place_of(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1; }
 
+// The row of K that S^T's row g is.
+template <typename F>
+__device__ __forceinline__ int row_of_place(int g) {
+    return F::kBits == 4 ? place_of(g) : g;
+}
+
 // Probabilities p of S^T's rows g (p[0], p[1]: two columns) and g + 8 as the B
 // operand of the second product; kSplit: what hi leaves of them in lo.
 template <bool kSplit>
@@ -117,14 +123,17 @@ __device__ __forceinline__ void operand_of(const float (&p)[4], uint32_t (&hi)[2
 // kSplit: queries and probabilities as two fp16 numbers each (fp32 I/O).
 // kU: groups of a warp in a tile.  Two groups and three stages leave room for two
 // CTAs an SM (bf16, d <= 128); two stages took 522 us where three took 462.
-template <int D, bool kSplit, int kU, int kStages>
+template <typename F, int D, bool kSplit, int kU, int kStages>
 struct Shape {
     static constexpr int kTile = kWarps * kU * kGroup;
     static constexpr int kRows = 8;
     static constexpr int kParts = kSplit ? 2 : 1;
-    // a stage: key codes, value codes, key scales, value scales of a tile
-    static constexpr int kVCode = kTile * D / 2, kKScale = kTile * D, kVScale = kTile * D * 17 / 16;
-    static constexpr int kStage = kTile * D * 9 / 8;
+    // a stage: key codes, value codes, key scales, value scales of a tile (8 bits: and the
+    // exponents, 16 bytes a page or 128 places of it)
+    static constexpr int kRowBytes = D * F::kBits / 8;
+    static constexpr int kVCode = kTile * kRowBytes, kKScale = 2 * kVCode;
+    static constexpr int kVScale = kKScale + (F::kBits == 4 ? kTile * D / 16 : 0);
+    static constexpr int kStage = kKScale + (F::kBits == 4 ? kTile * D / 8 : kTile);
     static constexpr int kRing = kStages * kStage;
     static constexpr int kQueries = kParts * (D / 16) * 32 * 8;
     // rows of every warp that are merged at a time, in one stage
@@ -141,8 +150,8 @@ struct Shape {
 // S^T of a warp's group (its first row at `codes` and `scales`): K, rows
 // place_of(g) and 8 more, times Q^T.
 template <int D, int kParts>
-__device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scales, int g, int t4,
-                                       const uint4 *queries, float (&s)[4]) {
+__device__ __forceinline__ void scores(Fmt4, const uint8_t *codes, const uint8_t *scales, int g,
+                                       int t4, const uint4 *queries, float (&s)[4]) {
     constexpr int kW = D / 32;      // 32-bit words of a lane's share of a row
     uint32_t kw[2][kW];
     __half2 ks[2][kW / 2];          // scale of each block, twice
@@ -195,10 +204,52 @@ __device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scal
     for (int e = 0; e < 4; ++e) s[e] += s2[e];
 }
 
+// The same of 8-bit numbers, rows g and g + 8: the group is one block, whose exponent
+// (at `exponent`) the scores are multiplied by.
+template <int D, int kParts>
+__device__ __forceinline__ void scores(Fmt8, const uint8_t *codes, const uint8_t *exponent, int g,
+                                       int t4, const uint4 *queries, float (&s)[4]) {
+    float s2[4];                    // a second chain of products
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {      // 16 numbers of a row at a time
+        uint32_t k[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(codes + (g + 8 * r) * D + t4 * (D / 4) +
+                                                             16 * w);
+            k[r][0] = x.x; k[r][1] = x.y; k[r][2] = x.z; k[r][3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            uint32_t a0[2], a1[2], b0[2], b1[2];
+            e4m3x4_f16(k[0][i], a0);
+            e4m3x4_f16(k[1][i], a1);
+            e4m3x4_f16(k[0][i + 1], b0);
+            e4m3x4_f16(k[1][i + 1], b1);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                const uint4 q = queries[(part * (D / 32) + 2 * w + i / 2) * 32];
+                if (w == 0 && i == 0 && part == 0) {
+                    mma16816_zero(s, a0[0], a1[0], a0[1], a1[1], q.x, q.y);
+                    mma16816_zero(s2, b0[0], b1[0], b0[1], b1[1], q.z, q.w);
+                } else {
+                    mma16816(s, a0[0], a1[0], a0[1], a1[1], q.x, q.y);
+                    mma16816(s2, b0[0], b1[0], b0[1], b1[1], q.z, q.w);
+                }
+            }
+        }
+    }
+    const float f = exponent_f32(*exponent);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * f;
+}
+
 // A lane's numbers of V of one group: D / 8 elements of the tokens t4, 4 + (t4 ^ 1)
 // and those 8 further, with their scales.
+template <typename F, int D>
+struct VShare;
 template <int D>
-struct VShare {
+struct VShare<Fmt4, D> {
     static constexpr int kWords = D / 64, kBlocks = D == 256 ? 2 : 1;
     uint32_t w[4][kWords], sb[4];
 
@@ -232,50 +283,125 @@ struct VShare {
             e4m3x2_f16(__byte_perm(sb[2 * e], sb[2 * e + 1], k == 0 ? 0x0040 : 0x0051));
         return *reinterpret_cast<const __half2 *>(&two);
     }
+    // Takes token j out of the product.
+    __device__ __forceinline__ void clear(int j) { sb[j] = 0; }
+    // Whether token j has a NaN in block k; it is taken out if so.
+    __device__ __forceinline__ bool take_nan(int j, int k) {
+        if (((sb[j] >> (8 * k)) & 0x7f) != 0x7f) return false;
+        sb[j] &= ~(0xffu << (8 * k));
+        return true;
+    }
 };
+// Of 8-bit numbers: of the tokens 2 t4, 2 t4 + 1 and those 8 further, which share one
+// exponent.
+template <int D>
+struct VShare<Fmt8, D> {
+    static constexpr int kWords = D / 32, kBlocks = D == 256 ? 2 : 1;
+    uint32_t w[4][kWords], e;
+
+    __device__ static __forceinline__ int place(int j, int t4) {
+        return 2 * t4 + (j & 1) + 8 * (j >> 1);
+    }
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *exponent, int g,
+                                         int t4) {
+        e = *exponent;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint8_t *p = codes + place(j, t4) * D + g * (D / 8);
+            if constexpr (D == 64) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                w[j][0] = x.x; w[j][1] = x.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords; i += 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+                    w[j][i] = x.x; w[j][i + 1] = x.y; w[j][i + 2] = x.z; w[j][i + 3] = x.w;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void clear(int j) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[j][i] = 0;
+    }
+    __device__ __forceinline__ bool take_nan(int j, int k) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = k * (kWords / kBlocks); i < (k + 1) * (kWords / kBlocks); ++i)
+            bad |= e4m3x4_nan(w[j][i]);
+        if (bad == 0) return false;
+#pragma unroll
+        for (int i = k * (kWords / kBlocks); i < (k + 1) * (kWords / kBlocks); ++i) w[j][i] = 0;
+        return true;
+    }
+};
+
+// acc += A B, or with kScaled acc += factor * (A B), B in kParts parts.
+template <int kParts, bool kScaled>
+__device__ __forceinline__ void add_product(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, const uint32_t (&b)[kParts][2],
+                                            float factor) {
+    if constexpr (!kScaled) {
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+            mma16816(acc, a0, a1, a2, a3, b[part][0], b[part][1]);
+    } else {
+        float x[4] = {};
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+            mma16816(x, a0, a1, a2, a3, b[part][0], b[part][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
+    }
+}
 
 // O^T += V^T P^T, or with kScaled O^T += factor * (V^T P^T).
 template <int D, int kParts, bool kScaled>
-__device__ __forceinline__ void product(const VShare<D> &v, const uint32_t (&pf)[kParts][2],
+__device__ __forceinline__ void product(const VShare<Fmt4, D> &v, const uint32_t (&pf)[kParts][2],
                                         float factor, float (&o)[D / 16][4]) {
-    __half2 sc[VShare<D>::kBlocks][2];
+    using V = VShare<Fmt4, D>;
+    __half2 sc[V::kBlocks][2];
 #pragma unroll
-    for (int k = 0; k < VShare<D>::kBlocks; ++k)
+    for (int k = 0; k < V::kBlocks; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) sc[k][e] = v.scale(k, e);
 #pragma unroll
-    for (int w = 0; w < VShare<D>::kWords; ++w) {
+    for (int w = 0; w < V::kWords; ++w) {
         constexpr uint32_t kEven = 0x0f0f0f0fu;
         uint32_t e1[4], d1[4], e2[4], d2[4];   // even and odd elements of the two token pairs
         e2m1x8_f16(select_bits(v.w[0][w], v.w[1][w] << 4, kEven), e1);
         e2m1x8_f16(select_bits(v.w[0][w] >> 4, v.w[1][w], kEven), d1);
         e2m1x8_f16(select_bits(v.w[2][w], v.w[3][w] << 4, kEven), e2);
         e2m1x8_f16(select_bits(v.w[2][w] >> 4, v.w[3][w], kEven), d2);
-        const __half2 s1 = sc[w / 2 % VShare<D>::kBlocks][0], s2 = sc[w / 2 % VShare<D>::kBlocks][1];
+        const __half2 s1 = sc[w / 2 % V::kBlocks][0], s2 = sc[w / 2 % V::kBlocks][1];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t a0 = mul2(e1[k], s1), a1 = mul2(d1[k], s1);
-            const uint32_t a2 = mul2(e2[k], s2), a3 = mul2(d2[k], s2);
-            float (&acc)[4] = o[4 * w + k];
-            if constexpr (!kScaled) {
+        for (int k = 0; k < 4; ++k)
+            add_product<kParts, kScaled>(o[4 * w + k], mul2(e1[k], s1), mul2(d1[k], s1),
+                                         mul2(e2[k], s2), mul2(d2[k], s2), pf, factor);
+    }
+}
+template <int D, int kParts, bool kScaled>
+__device__ __forceinline__ void product(const VShare<Fmt8, D> &v, const uint32_t (&pf)[kParts][2],
+                                        float factor, float (&o)[D / 16][4]) {
+    const __half2 f = exponent_f16x2(v.e);
 #pragma unroll
-                for (int part = 0; part < kParts; ++part)
-                    mma16816(acc, a0, a1, a2, a3, pf[part][0], pf[part][1]);
-            } else {
-                float x[4] = {};
+    for (int w = 0; w < VShare<Fmt8, D>::kWords; ++w) {
 #pragma unroll
-                for (int part = 0; part < kParts; ++part)
-                    mma16816(x, a0, a1, a2, a3, pf[part][0], pf[part][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], factor, acc[e]);
-            }
+        for (int k = 0; k < 2; ++k) {
+            // two elements of four tokens: bytes of two tokens side by side
+            uint32_t x[2], y[2];
+            e4m3x4_f16(__byte_perm(v.w[0][w], v.w[1][w], k == 0 ? 0x5140 : 0x7362), x);
+            e4m3x4_f16(__byte_perm(v.w[2][w], v.w[3][w], k == 0 ? 0x5140 : 0x7362), y);
+            add_product<kParts, kScaled>(o[2 * w + k], mul2(x[0], f), mul2(x[1], f), mul2(y[0], f),
+                                         mul2(y[1], f), pf, factor);
         }
     }
 }
 
-template <typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename F, typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
-    using Sh = Shape<D, kSplit, kU, kStages>;
+    using Sh = Shape<F, D, kSplit, kU, kStages>;
+    using V = VShare<F, D>;
     constexpr int kTile = Sh::kTile;
     using W = Walk<kTile, Sh::kRows, kThreads>;
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
@@ -319,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
 
     // Copies: lane (run, part) of the issuing warp copies one part of a run of tokens
     // that lie together, a page's or as many of it as make a tile.
-    const int run = min(a.kv.page_size(), 128);
+    const int run_shift = min(a.kv.page_shift, 7), run = 1 << run_shift;
     const int lane_run = lane >> 2, lane_part = lane & 3;
-    const int row_bytes = lane_part < 2 ? D / 2 : D / 16;
+    const int row_bytes = lane_part < 2 ? Sh::kRowBytes : D / 16;
     const uint32_t lane_dst = lane_part == 0   ? 0
                               : lane_part == 1 ? Sh::kVCode
                               : lane_part == 2 ? Sh::kKScale
@@ -351,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             runs += __popc(__ballot_sync(0xffffffffu, page[k] >= 0 && lane_part == 0));
         if (lane == 0) {
             armed[stage] = n / kStages + 1;
-            ptx::mbar_arrive_expect_tx(full + stage, runs * run * (D * 9 / 8));
+            ptx::mbar_arrive_expect_tx(full + stage, F::kBits == 4 ? runs * run * (D * 9 / 8)
+                                                                   : runs * (run * (2 * D) + 16));
         }
         __syncwarp();
 #pragma unroll
@@ -359,14 +486,24 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             if (page[k] < 0) continue;
             const int psz = a.kv.page_size(), in_tile = (lane_run + 8 * k) * run;
             const int at = (place + in_tile) & (psz - 1);
-            const int from = at * row_bytes + (lane_part == 0   ? 0
-                                               : lane_part == 1 ? v_code_at(psz, D, 0)
-                                               : lane_part == 2 ? k_scale_at(psz, D, 0)
-                                                                : v_scale_at(psz, D, 0));
-            if (!a.kv.bytes_ok(page[k], h, from, run * row_bytes)) continue;
-            const uint8_t *src = a.kv.pages + a.kv.block(page[k], h) + from;
-            bulk_load(ring_at + stage * Sh::kStage + lane_dst + in_tile * row_bytes, src,
-                      run * row_bytes, full + stage);
+            int from, bytes;
+            uint32_t to = ring_at + stage * Sh::kStage + lane_dst;
+            if constexpr (F::kBits == 4) {
+                from = at * row_bytes + (lane_part == 0   ? 0
+                                         : lane_part == 1 ? v_code_at(psz, D, 0)
+                                         : lane_part == 2 ? k_scale_at(psz, D, 0)
+                                                          : v_scale_at(psz, D, 0));
+                bytes = run * row_bytes;
+                to += in_tile * row_bytes;
+            } else {
+                if (lane_part == 3) continue;
+                from = lane_part == 2 ? F::exponents_at(psz, D, at)
+                                      : F::code_at(D, lane_part == 0 ? at : psz + at);
+                bytes = lane_part == 2 ? 16 : run * D;
+                to += lane_part == 2 ? 16 * (lane_run + 8 * k) : in_tile * D;
+            }
+            if (!a.kv.bytes_ok<F>(page[k], h, from, bytes)) continue;
+            bulk_load(to, a.kv.pages + a.kv.block<F>(page[k], h) + from, bytes, full + stage);
         }
     };
 
@@ -522,19 +659,30 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 due = due_at();
             }
             const bool arrived = waits.on(full + stage, phase);
-            const uint8_t *buf = smem + stage * Sh::kStage + warp * (kU * kGroup * D / 2);
+            const uint8_t *buf = smem + stage * Sh::kStage + warp * (kU * kGroup * Sh::kRowBytes);
             const uint8_t *sbuf =
                 smem + stage * Sh::kStage + Sh::kKScale + warp * (kU * kGroup * D / 16);
             int t0 = place0 + i * kTile + warp * (kU * kGroup);
 #pragma unroll 1
-            for (int u = 0; u < kU; ++u, t0 += kGroup, buf += kGroup * D / 2, sbuf += kGroup * D / 16) {
+            for (int u = 0; u < kU;
+                 ++u, t0 += kGroup, buf += kGroup * Sh::kRowBytes, sbuf += kGroup * D / 16) {
                 if (!arrived || t0 >= len) break;
                 const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
                 float s[4];
-                scores<D, kParts>(buf, sbuf, g, t4, queries + lane, s);
-                VShare<D> v;
-                v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
+                V v;
+                if constexpr (F::kBits == 4) {
+                    scores<D, kParts>(F(), buf, sbuf, g, t4, queries + lane, s);
+                    v.load(buf + Sh::kVCode, sbuf + (Sh::kVScale - Sh::kKScale), g, t4);
+                } else {
+                    // the group's exponents, among the 16 bytes of its run of places
+                    const int in_tile = (warp * kU + u) * kGroup;
+                    const uint8_t *ex = smem + stage * Sh::kStage + Sh::kKScale +
+                                        16 * (in_tile >> run_shift) +
+                                        ((in_tile & (run - 1)) / F::kBlock);
+                    scores<D, kParts>(F(), buf, ex, g, t4, queries + lane, s);
+                    v.load(buf + Sh::kVCode, ex + 8, g, t4);
+                }
 
                 // Scores in log2 units less the row's `sub`, so that the row's largest number
                 // is about kLift.  One comparison finds those that call for more: above
@@ -545,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 for (int e = 0; e < 4; ++e) {
                     t[e] = fmaf(s[e], mul[e & 1], -sub[e & 1]);
                     if (!whole) {
-                        const int at = t0 + place_of(g) + 8 * (e >> 1), r = 2 * t4 + (e & 1);
+                        const int at = t0 + row_of_place<F>(g) + 8 * (e >> 1), r = 2 * t4 + (e & 1);
                         if (at < row_from[r] || at >= row_to[r]) t[e] = -INFINITY;
                     }
                     more |= fabsf(t[e] - kMid) > kHalf;
@@ -600,22 +748,20 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 }
                 operand_of<kSplit>(p, pf[0], pf[kParts - 1]);
                 if (!whole) {
-                    // Places behind the sequence's end may hold anything: their scales become 0.
-                    // A NaN that some rows see and others do not would reach all of them through
+                    // Places behind the sequence's end may hold anything: they become 0.  A NaN that some rows see and others do not would reach all of them through
                     // 0 * NaN: it is taken out of the product and put into the rows that see it.
-                    constexpr int kBlocks = VShare<D>::kBlocks;
+                    constexpr int kBlocks = V::kBlocks;
                     uint32_t nan[kBlocks] = {};
                     bool any = false;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int off = v.place(j, t4);
-                        if (t0 + off >= len) v.sb[j] = 0;
+                        if (t0 + off >= len) v.clear(j);
 #pragma unroll
                         for (int k = 0; k < kBlocks; ++k)
-                            if (((v.sb[j] >> (8 * k)) & 0x7f) == 0x7f) {
+                            if (v.take_nan(j, k)) {
                                 nan[k] |= 1u << off;
                                 any = true;
-                                v.sb[j] &= ~(0xffu << (8 * k));
                             }
                     }
                     if (__any_sync(0xffffffffu, any)) {
@@ -766,10 +912,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     if (*waits.abort && warp == 0) drain_ring<kStages>(full, armed);
 }
 
-template <typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename F, typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
 gdn_status launch(AttnArgs &a, cudaStream_t st) {
-    using Sh = Shape<D, kSplit, kU, kStages>;
-    auto kern = k_kv_attn<T, D, kSplit, kU, kStages, kMinCtas>;
+    using Sh = Shape<F, D, kSplit, kU, kStages>;
+    auto kern = k_kv_attn<F, T, D, kSplit, kU, kStages, kMinCtas>;
     constexpr int kTile = Sh::kTile;
     static std::atomic<int> memo[kMaxDeviceMemo];
     // resident CTAs of the device, and the opt-in to the ring's shared memory
@@ -792,7 +938,7 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     const bool cut = a.max_len > kTile;     // else no piece of work has two tiles
     void *scratch = nullptr;
     if (cut && alloc_pieces<D, Sh::kRows>(a, grid, &scratch, st) != cudaSuccess) return GDN_ERR_CUDA;
-    const int slot = timer_begin(st, "k_kv_attn");
+    const int slot = timer_begin(st, F::kBits == 4 ? "k_kv_attn" : "k_kv8_attn");
     kern<<<grid, kThreads, Sh::kSmem, st>>>(a);
     timer_end(slot, st);
     count_launch();
@@ -806,24 +952,29 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
 }
 
 // By the head's width alone: registers hold d / 4 sums a lane, and a stage has to
-// hold the merge of the warps' sums.
-template <typename T, bool kSplit>
+// hold the merge of the warps' sums.  (8 bits: tiles of half the places, of as many bytes.)
+template <typename F, typename T, bool kSplit>
 gdn_status pick(AttnArgs &a, cudaStream_t st) {
-    switch (a.kv.d) {
-        case 64: return launch<T, 64, kSplit, 2, 3, kSplit ? 1 : 2>(a, st);
-        case 128: return launch<T, 128, kSplit, 2, 3, kSplit ? 1 : 2>(a, st);
-        default: return launch<T, 256, kSplit, 1, 4, 1>(a, st);
+    constexpr int kCtas = kSplit ? 1 : 2;
+    if constexpr (F::kBits == 4) {
+        switch (a.kv.d) {
+            case 64: return launch<F, T, 64, kSplit, 2, 3, kCtas>(a, st);
+            case 128: return launch<F, T, 128, kSplit, 2, 3, kCtas>(a, st);
+            default: return launch<F, T, 256, kSplit, 1, 4, 1>(a, st);
+        }
+    } else {
+        switch (a.kv.d) {
+            case 64: return launch<F, T, 64, kSplit, 2, 3, kCtas>(a, st);
+            case 128: return launch<F, T, 128, kSplit, 1, 3, kCtas>(a, st);
+            default: return launch<F, T, 256, kSplit, 1, 3, 1>(a, st);
+        }
     }
 }
 
-}  // namespace
-}  // namespace kv
-}  // namespace gdn
-
-extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o,
-                                  float *lse, int max_len, int max_new, float scale, int window,
-                                  unsigned flags, gdn_dtype dt, void *stream) {
-    using namespace gdn::kv;
+template <typename F>
+gdn_status attention(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, float *lse,
+                     int max_len, int max_new, float scale, int window, unsigned flags,
+                     gdn_dtype dt, void *stream) {
     if (!kv || kv->N < 0 || kv->n_tokens < 0 || max_len < 0 || max_new < 0 || window < 0)
         return GDN_ERR_INVALID_ARG;
     if (flags & ~(unsigned)GDN_ATTN_CAUSAL) return GDN_ERR_INVALID_ARG;
@@ -854,11 +1005,28 @@ extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn
     a.scale_log2 = scale * 1.4426950408889634f;
     a.window = window;
     a.causal = (flags & GDN_ATTN_CAUSAL) != 0;
-    a.err = gdn::device_error_word();
-    const long long limit = gdn::option(GDN_OPT_WAIT_LIMIT);
+    a.err = device_error_word();
+    const long long limit = option(GDN_OPT_WAIT_LIMIT);
     a.wait_limit = limit > 0 ? (uint32_t)(limit > 0x7fffffffLL ? 0x7fffffffLL : limit) : (1u << 22);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dt == GDN_F32) return pick<float, true>(a, st);
-    if (a.kv.d <= 128 && (long long)a.max_new * a.G > kMany) return attn_many(a, st);
-    return pick<__nv_bfloat16, false>(a, st);
+    if (dt == GDN_F32) return pick<F, float, true>(a, st);
+    if (a.kv.d <= 128 && (long long)a.max_new * a.G > kMany) return attn_many<F>(a, st);
+    return pick<F, __nv_bfloat16, false>(a, st);
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace gdn
+
+extern "C" gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o,
+                                  float *lse, int max_len, int max_new, float scale, int window,
+                                  unsigned flags, gdn_dtype dt, void *stream) {
+    return gdn::kv::attention<gdn::kv::Fmt4>(kv, q, o, lse, max_len, max_new, scale, window, flags,
+                                             dt, stream);
+}
+extern "C" gdn_status gdn_kv8_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o,
+                                   float *lse, int max_len, int max_new, float scale, int window,
+                                   unsigned flags, gdn_dtype dt, void *stream) {
+    return gdn::kv::attention<gdn::kv::Fmt8>(kv, q, o, lse, max_len, max_new, scale, window, flags,
+                                             dt, stream);
 }

@@ -1,5 +1,5 @@
-// gdn_kv_attn.cuh -- what the attention kernels over the 4-bit cache share: the
-// call's arguments, what each row sees, and the division of the work.
+// gdn_kv_attn.cuh -- what the attention kernels over a paged cache (4 or 8 bits) share:
+// the call's arguments, what each row sees, and the division of the work.
 #pragma once
 
 #include <cmath>
@@ -455,7 +455,8 @@ inline cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k_kv_join<T, D, kRows, kJoin, kStripes>, a);
 }
 
-// Many rows (gdn_kv_attn_tc.cu): bf16 rows, d = 64 or 128.
+// Many rows (gdn_kv_attn_tc.cu): bf16 rows, d = 64 or 128; F: Fmt4 or Fmt8.
+template <typename F>
 gdn_status attn_many(AttnArgs &a, cudaStream_t st);
 
 }  // namespace kv

@@ -50,8 +50,8 @@ constexpr int kThreads = 512;
 constexpr int kConvert = 256;               // first thread of the converting warps
 constexpr int kIssuer = 384;                // first thread of the issuing warps
 // Registers a thread of each role; together no more than the launch's 512 x 128.
-constexpr int kSoftmaxRegs = 168, kConvertRegs = 96, kIssuerRegs = 64;
-static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssuerRegs <= 512 * 128, "registers");
+constexpr int kSoftmaxRegs = 168, kConvertRegs4 = 96, kConvertRegs8 = 112, kIssuerRegs = 64;
+static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs8 + 128 * kIssuerRegs <= 512 * 128, "registers");
 constexpr float kLift = 8.f;                // log2 of the first maximum's probability
 constexpr float kMostSum = 32768.f;         // of a tile: above it `sub` moves
 
@@ -160,8 +160,10 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 // One token's codes and scales of K or V of a head, in registers.
+template <typename F, int D>
+struct Token;
 template <int D>
-struct Token {
+struct Token<Fmt4, D> {
     uint4 w[D / 32];
     uint32_t s[D / 64];       // D / 16 scale bytes
     __device__ __forceinline__ void load(const uint8_t *code, const uint8_t *scale) {
@@ -206,6 +208,49 @@ struct Token {
                 const __half2 f = k < 2 ? lo : hi;
                 st_shared16(chunk_at(tile, row, 4 * i + k), mul2(r[0], f), mul2(r[1], f),
                             mul2(r[2], f), mul2(r[3], f));
+            }
+        }
+    }
+};
+
+template <int D>
+struct Token<Fmt8, D> {
+    uint4 w[D / 16];
+    uint32_t e;               // exponent byte
+    __device__ __forceinline__ void load(const uint8_t *code, const uint8_t *exponent) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(code) + i);
+        e = __ldg(exponent);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        e = 0;
+    }
+    // Zeroes the blocks of 16 neighbours with a NaN among them; their mask.
+    __device__ __forceinline__ uint32_t take_nan() {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            if (e4m3x4_nan(w[i].x) | e4m3x4_nan(w[i].y) | e4m3x4_nan(w[i].z) | e4m3x4_nan(w[i].w)) {
+                bad |= 1u << i;
+                w[i] = make_uint4(0, 0, 0, 0);
+            }
+        return bad;
+    }
+    // Its D numbers as fp16 into row `row` of an operand tile.
+    __device__ __forceinline__ void convert(uint32_t tile, int row) const {
+        const __half2 f = exponent_f16x2(e);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                uint32_t r[2], s[2];
+                e4m3x4_f16(x[k], r);
+                e4m3x4_f16(x[k + 1], s);
+                st_shared16(chunk_at(tile, row, 2 * i + k / 2), mul2(r[0], f), mul2(r[1], f),
+                            mul2(s[0], f), mul2(s[1], f));
             }
         }
     }
@@ -318,9 +363,10 @@ __device__ __forceinline__ void issue(const AttnArgs &a, const typename W::P &pl
     mbar_wait(bar + B_DRAIN + m, 0, kDrainLimit);
 }
 
-template <int D>
+template <typename F, int D>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     using L = Lay<D>;
+    constexpr int kConvertRegs = F::kBits == 4 ? kConvertRegs4 : kConvertRegs8;
     using W = Walk<kTile, kRows, kThreads>;
     using T = __nv_bfloat16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -618,33 +664,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     const int at = place0 + i * kTile + tok;
                     return i < count && at < len ? a.kv.page_raw(w.b, at) : Kv::kNoPage;
                 };
-                Token<D> k, v;
-                auto load = [&](Token<D> &x, int i, int raw, bool key) {
+                Token<F, D> k, v;
+                auto load = [&](Token<F, D> &x, int i, int raw, bool key) {
                     const int page = a.kv.page_checked(raw, a.err);
                     if (page < 0) {
                         x.clear();
                         return;
                     }
                     const int row = (place0 + i * kTile + tok) & (psz - 1);
-                    if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
-                        x.clear();
-                        return;
+                    const uint8_t *blk = a.kv.pages + a.kv.block<F>(page, h);
+                    if constexpr (F::kBits == 4) {
+                        if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
+                            x.clear();
+                            return;
+                        }
+                        x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
+                               blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
+                    } else {
+                        const int at = F::exponents_at(psz, D, row);
+                        if (!a.kv.bytes_ok<F>(page, h, at, 16)) {
+                            x.clear();
+                            return;
+                        }
+                        x.load(blk + F::code_at(D, key ? row : psz + row),
+                               blk + at + (key ? 0 : 8) + F::exponent_of(row));
                     }
-                    const uint8_t *blk = a.kv.pages + a.kv.block(page, h);
-                    x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
-                           blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
                 };
                 // brings a token of a tile to come into L2: its lines from DRAM would take
                 // longer than the conversion of a tile
                 auto prefetch = [&](int i, int raw) {
                     if ((unsigned)raw >= (unsigned)a.kv.n_pages) return;
                     const int row = (place0 + i * kTile + tok) & (psz - 1);
-                    const uint8_t *blk = a.kv.pages + a.kv.block(raw, h);
-                    prefetch_l2(blk + k_code_at(psz, D, row));
-                    prefetch_l2(blk + v_code_at(psz, D, row));
-                    if ((tok & 15) == 0) {      // (a page has 16 tokens at least)
-                        prefetch_l2(blk + k_scale_at(psz, D, row));
-                        prefetch_l2(blk + v_scale_at(psz, D, row));
+                    const uint8_t *blk = a.kv.pages + a.kv.block<F>(raw, h);
+                    if constexpr (F::kBits == 4) {
+                        prefetch_l2(blk + k_code_at(psz, D, row));
+                        prefetch_l2(blk + v_code_at(psz, D, row));
+                        if ((tok & 15) == 0) {      // (a page has 16 tokens at least)
+                            prefetch_l2(blk + k_scale_at(psz, D, row));
+                            prefetch_l2(blk + v_scale_at(psz, D, row));
+                        }
+                    } else {
+                        prefetch_l2(blk + F::code_at(D, row));
+                        prefetch_l2(blk + F::code_at(D, psz + row));
+                        if ((tok & 15) == 0) prefetch_l2(blk + F::exponents_at(psz, D, row));
                     }
                 };
                 int page = page_at(0), next_page = page_at(1), ahead[2] = {page_at(2), page_at(3)};
@@ -690,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     if (warp == kIssuer / 32) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <typename F, int D>
 gdn_status launch(AttnArgs &a, cudaStream_t st) {
-    auto kern = k_kv_attn_tc<D>;
+    auto kern = k_kv_attn_tc<F, D>;
     static std::atomic<int> memo[kMaxDeviceMemo];
     const int sms = per_device(memo, [&](int dev) {
         int n = 0;
@@ -709,7 +771,7 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     const int grid = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
     void *scratch = nullptr;
     if (alloc_pieces<D, kRows>(a, grid, &scratch, st) != cudaSuccess) return GDN_ERR_CUDA;
-    const int slot = timer_begin(st, "k_kv_attn_tc");
+    const int slot = timer_begin(st, F::kBits == 4 ? "k_kv_attn_tc" : "k_kv8_attn_tc");
     kern<<<grid, kThreads, Lay<D>::SIZE, st>>>(a);
     timer_end(slot, st);
     count_launch();
@@ -722,9 +784,12 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+template <typename F>
 gdn_status attn_many(AttnArgs &a, cudaStream_t st) {
-    return a.kv.d == 64 ? launch<64>(a, st) : launch<128>(a, st);
+    return a.kv.d == 64 ? launch<F, 64>(a, st) : launch<F, 128>(a, st);
 }
+template gdn_status attn_many<Fmt4>(AttnArgs &a, cudaStream_t st);
+template gdn_status attn_many<Fmt8>(AttnArgs &a, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace gdn

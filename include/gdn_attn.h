@@ -1,7 +1,7 @@
 /*
  * gdn_attn.h -- C ABI of the softmax-attention layers that stand between gated
  * delta rule layers in a hybrid decoder: rotary positions, a paged key/value
- * cache held in 4 bits, and attention over that cache.  Part of libgdn.so;
+ * cache held in 4 or in 8 bits, and attention over that cache.  Part of libgdn.so;
  * statuses, dtypes, streams, scratch and error reporting as in gdn.h:
  * arguments are checked synchronously, work is enqueued on `stream`, errors
  * found by a kernel (a position outside its table, a page outside the pool, a
@@ -38,6 +38,17 @@
  * 9/8 d bytes hold a token's key and value of one head (144 at d = 128).
  * Place p of sequence b lies in page page_table[b * table_stride + p / page_size], row
  * p % page_size.  What lies in rows that no sequence counts is never used.
+ *
+ * Cache in 8 bits (gdn_kv8_*).  `pages` is [n_pages][H][gdn_kv8_page_bytes(page_size,
+ * d)] bytes.  The block of one (page, head) holds, in this order,
+ *     key codes    [page_size][d]          value codes    [page_size][d]
+ *     exponents    [page_size / 128, at least 1][16]
+ * A code is an e4m3 number.  16 places of a head share an exponent byte e for their
+ * keys and one for their values, 0 <= e <= 22:
+ *     element = e4m3 * 2^(e - 15) * head_scale[0 or 1][h],
+ * and the bytes of places 128 i + 16 j are bytes j (keys) and 8 + j (values) of the
+ * 16 bytes i.  A token's key and value of one head take 2 d + 1/8 bytes (pages of 128).
+ * Everything else is as in 4 bits; a gdn_kv describes either.
  *
  * Sizes.  A call has at most 2^31 - 256 tokens, and a page table as many places a
  * sequence (GDN_ERR_UNSUPPORTED).
@@ -162,6 +173,38 @@ enum { GDN_ATTN_CAUSAL = 1 };
 gdn_status gdn_kv_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, float *lse,
                        int max_len, int max_new, float scale, int window, unsigned flags,
                        gdn_dtype dt, void *stream);
+
+/* Bytes of one (page, head) block in 8 bits, 2 page_size d and 16 for every 128 places
+ * (at least once); 0 if unsupported. */
+int64_t gdn_kv8_page_bytes(int page_size, int d);
+
+/*
+ * gdn_kv_append on a cache in 8 bits, in one launch.  The exponent of a block of 16
+ * places is the least under which the largest magnitude among the call's tokens in it,
+ * over the head's scale, is at most 448 (so 22 where there is an infinity); a block that
+ * has tokens before them keeps at least the one that it has, and where it grows their
+ * codes are divided by the same power of two, to nearest even.  An element becomes the
+ * nearest e4m3 number to its quotient, at most 448 (ties to even).  What is above the
+ * range, 57344 times the head's scale, becomes that; a NaN makes the 16 neighbours
+ * along d that it is among NaN, and they do not count for the exponent.  A page that a
+ * call writes belongs to one sequence of the call.
+ */
+gdn_status gdn_kv8_append(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v,
+                          const gdn_rows *q, const gdn_rows *q_out, const gdn_rotary *rot,
+                          gdn_dtype dt, void *stream);
+
+/* gdn_kv_read from a cache in 8 bits: e4m3 * 2^(e - 15) is exact, its product with the
+ * head's scale is rounded to fp32, and that to dt. */
+gdn_status gdn_kv8_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, gdn_dtype dt,
+                        void *stream);
+
+/* gdn_kv_attn over a cache in 8 bits: the same arguments, rows seen and roundings (e4m3 *
+ * 2^(e - 15) fits fp16 as well).  A NaN among the values reaches the outputs of its own
+ * element, or of the 16 neighbours that gdn_kv8_append gives it to, in the rows that see
+ * its place. */
+gdn_status gdn_kv8_attn(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, float *lse,
+                        int max_len, int max_new, float scale, int window, unsigned flags,
+                        gdn_dtype dt, void *stream);
 
 #ifdef __cplusplus
 }
