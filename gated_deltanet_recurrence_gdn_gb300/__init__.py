@@ -18,6 +18,11 @@ The softmax-attention layers of a hybrid decoder (``attention.py``,
 
 (``gdn_kv8_append``, ``gdn_kv8_attn``: the same over a cache in 8 bits.)
 
+Beam search (``beams.py``, ``include/gdn_beam.h``):
+
+    scores, beam, token = gdn_beam_select(logits, scores)
+    slots = gdn_beam_reorder(beam, slots, states=states)
+
 Layouts follow ``include/gdn.h``: dense q, k [B,H,T,d_k], v [B,H,T,d_v]; packed
 q, k [H,T_total,d_k], v [H,T_total,d_v]; gates fp32; h0 / hT [.., H, d_v, d_k]
 fp32; q, k, v share one dtype (bf16 or fp32), which is also the dtype of o.
@@ -94,6 +99,8 @@ ABI = [
     ("gdn_kv8_append", _i, [_vp] * 6 + [_i, _vp]),
     ("gdn_kv8_read", _i, [_vp] * 3 + [_i, _vp]),
     ("gdn_kv8_attn", _i, [_vp] * 4 + [_i] * 2 + [ctypes.c_float, _i, ctypes.c_uint, _i, _vp]),
+    ("gdn_beam_select", _i, [_vp, ctypes.c_int64] + [_vp] * 2 + [_i] + [_vp] * 3 + [_i] * 5 + [_vp]),
+    ("gdn_beam_reorder", _i, [_vp] * 3 + [_i] * 3 + [_vp, _i, _vp, _vp, _i, _vp]),
     ("gdn_selftest_ring", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
     ("gdn_selftest_wait", _i, [_i, ctypes.c_longlong, ctypes.POINTER(_i), _vp]),
 ]
@@ -491,3 +498,4 @@ from .attention import (gdn_kv8_append, gdn_kv8_attn, gdn_kv8_page_bytes,  # noq
                         gdn_kv8_pages, gdn_kv8_read, gdn_kv_append, gdn_kv_attn, gdn_kv_page_bytes,
                         gdn_kv_pages, gdn_kv_read, gdn_rope, gdn_rope_axes, gdn_rope_bwd,
                         gdn_rope_table)
+from .beams import gdn_beam_reorder, gdn_beam_select  # noqa: E402,F401
