@@ -6,10 +6,11 @@ Beam w of group (request) b is row b W + w wherever the beams of a call lie in o
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import _DT, _i, _ptr, _vp, load
+from . import _DT, _i, _vp, load
 from .attention import _call, _device, _f32, _i32, _int32
 
 _i64 = ctypes.c_int64
@@ -70,19 +71,25 @@ def gdn_beam_select(logits, scores, n=None, *, done=None, eos=None, out=None, ch
     else:
         for name, t, dtype in zip(("out[0]", "out[1]", "out[2]"), out, (_f32, _i32, _i32)):
             _grid(name, t, B, n, (dtype,), at)
-    _call(load().gdn_beam_select, "gdn_beam_select", at, check, _ptr(logits), stride, _ptr(scores),
-          _ptr(done), 0 if eos is None else eos, *map(_ptr, out), B, W, V, n, _DT[logits.dtype])
+    _call(load().gdn_beam_select, "gdn_beam_select", at, check, logits.data_ptr(), stride,
+          scores.data_ptr(), None if done is None else done.data_ptr(), 0 if eos is None else eos,
+          out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), B, W, V, n, _DT[logits.dtype])
     return out
 
 
+# The structures packed into bytes, which costs a call less than filling ctypes ones.
+_POOL, _TABLES = struct.Struct("@Pqi4x"), struct.Struct("@PPPPiiqqq")
+assert (_POOL.size, _TABLES.size) == (ctypes.sizeof(_Pool), ctypes.sizeof(_Tables))
+
+
 def _pools(name, tensors, at):
-    pools = (_Pool * len(tensors))()
-    for p, t in zip(pools, tensors):
+    pools = []
+    for t in tensors:
         if t.dim() < 1 or t.get_device() != at or not t.is_contiguous():
             raise ValueError("%s must be contiguous tensors on the call's device" % name)
-        p.data, p.count = t.data_ptr(), t.shape[0]
-        p.bytes = t.numel() // p.count * t.element_size() if p.count else 0
-    return pools
+        n = t.shape[0]
+        pools.append(_POOL.pack(t.data_ptr(), t.numel() // n * t.element_size() if n else 0, n))
+    return b"".join(pools)
 
 
 def gdn_beam_reorder(parent, slots, *, states=(), caches=(), page_table=None, own_pages=None,
@@ -136,16 +143,16 @@ def gdn_beam_reorder(parent, slots, *, states=(), caches=(), page_table=None, ow
                 kv_len.shape[0] != B * W or own_pages.shape[1] != pages:
             raise ValueError("page_table and kv_len must have a row per beam, and page_table, "
                              "own_pages and out the same number of pages")
-        t = _Tables(page_table.data_ptr(), new_table.data_ptr(), own_pages.data_ptr(),
-                    kv_len.data_ptr(), pages, page_size, page_table.stride(0), new_table.stride(0),
-                    own_pages.stride(0))
-    for name, a in (("slots", new_slots), ("page_table", new_table)):
-        for b in (parent, slots, page_table, own_pages, kv_len):
-            if a is not None and b is not None and a.data_ptr() == b.data_ptr() and a.numel():
-                raise ValueError("the new %s cannot be written to an input" % name)
+        t = _TABLES.pack(page_table.data_ptr(), new_table.data_ptr(), own_pages.data_ptr(),
+                         kv_len.data_ptr(), pages, page_size, page_table.stride(0),
+                         new_table.stride(0), own_pages.stride(0))
+    if out is not None and B * W > 0:
+        given = {x.data_ptr() for x in (parent, slots, page_table, own_pages, kv_len) if x is not None}
+        if new_slots.data_ptr() in given or (paged and new_table.data_ptr() in given):
+            raise ValueError("out cannot be an input")
     if lanes < 1 and B * W > 0:
         raise ValueError("there are no lanes")
-    _call(load().gdn_beam_reorder, "gdn_beam_reorder", at, check, _ptr(parent), _ptr(slots),
-          _ptr(new_slots), B, W, max(lanes, 1), _pools("states", states, at), len(states),
-          None if t is None else ctypes.byref(t), _pools("caches", caches, at), len(caches))
+    _call(load().gdn_beam_reorder, "gdn_beam_reorder", at, check, parent.data_ptr(),
+          slots.data_ptr(), new_slots.data_ptr(), B, W, max(lanes, 1),
+          _pools("states", states, at), len(states), t, _pools("caches", caches, at), len(caches))
     return (new_slots, new_table) if paged else new_slots

@@ -4,14 +4,16 @@
 // Selection: score(w, v) = scores[w] + x[w][v] - log sum_u exp(x[w][u]), the n best of a
 // group's W V.  Within a row the order is that of the logits, so a row's n best need no
 // logarithm, and its logits are read once:
-// - k_beam_rows: a warp takes a run of a row, kVecs vectors of 16 bytes a lane, in one pass
-//   for the largest number and the sum of exponentials.  What it keeps of a vector is its
-//   largest number.  The n-th largest of the 32 lanes' largest numbers is a bound that
-//   n numbers of the run reach at least; vectors that reach it are few, and are read again
-//   from the caches to find the n best (64-bit keys: the number, then the lower index).
+// - k_beam_rows: a CTA takes a run of a row, up to 32 vectors of 16 bytes a thread, in one pass
+//   for the largest number and the sum of exponentials.  What a thread keeps of two vectors
+//   is their largest number.  With k = n / 4 rounded up, the k-th largest thread's of every one
+//   of 4 warps is reached by k numbers, so the least of the 4 is a bound that n numbers of
+//   the run reach; pairs that reach it are few, and their numbers are read again from
+//   the caches to be listed (64-bit keys: the number, then the lower index).
 //   Runs are cut by index, not by address, and sums do not depend on where a row starts.
-// - k_beam_pick, a CTA a group: a warp a row joins the runs' sums in fp64 and their lists
-//   by the same bound, then the W n candidates are ranked by their fp64 scores.
+// - k_beam_pick, a CTA a group: a warp a row joins the runs' sums in fp64 and finds the n
+//   best of their lists; the beams' candidates that a like bound leaves are ranked by their
+//   fp64 scores.
 // Reading the logits bounds a large batch, latency of two launches a small one.
 //
 // Reordering: every CTA finds by itself which beams have to move (a few instructions a
@@ -47,6 +49,10 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
     const long long u = __double_as_longlong(x + 0.0);
     return (unsigned long long)u ^ (u < 0 ? ~0ull : 0x8000000000000000ull);
 }
+__device__ __forceinline__ float number_of_order(unsigned long long o) {
+    if (o == ~0ull) return NAN;
+    return (float)__longlong_as_double((long long)(o ^ (o >> 63 ? 0x8000000000000000ull : ~0ull)));
+}
 // Keys: the number, then the lower index; 0 is none.
 using Key = unsigned long long;
 __device__ __forceinline__ Key key_of(uint32_t order, uint32_t index) {
@@ -60,19 +66,32 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Descending order over a warp of one number a lane.
-template <typename U>
-__device__ __forceinline__ U sorted32(U x) {
+// Descending order over a warp of one key a lane.  (Rolled and called: kernels this short wait
+// for instructions more than for a loop's.)
+__device__ __noinline__ Key sorted32(Key x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll 1
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const Key y = __shfl_xor_sync(kAll, x, j);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
+            x = larger ? (x > y ? x : y) : (x < y ? x : y);
+        }
+    return x;
+}
+
+// The n-th largest of a warp's numbers, one a lane.
+__device__ __forceinline__ uint32_t nth32(uint32_t x, int n) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
         for (int j = k >> 1; j > 0; j >>= 1) {
-            const U y = __shfl_xor_sync(kAll, x, j);
-            const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
-            x = larger ? (x > y ? x : y) : (x < y ? x : y);
+            const uint32_t y = __shfl_xor_sync(kAll, x, j);
+            x = ((lane & j) == 0) == ((lane & k) == 0) ? max(x, y) : min(x, y);
         }
-    return x;
+    return __shfl_sync(kAll, x, n - 1);
 }
 
 // The n best of the keys that a warp has seen, in 64 places of shared memory.
@@ -118,16 +137,22 @@ struct Best {
     }
 };
 
+constexpr int kRowWarps = 4, kRowThreads = kRowWarps * 32;
+
 struct RowArgs {
     const void *logits;
     long long stride;          // elements
     const float *scores;
     const uint8_t *done;
-    int rows, V, n, runs;      // runs of a row
-    Key *keys;                 // [rows][runs][n]
-    double *sums;              // [rows][runs]
-    float *tops;
+    int rows, V, n, runs;      // runs of a row, `batches` batches each
+    int batches;
+    Key *keys;                 // [rows][runs][kRowWarps n]: the run's n best among them, then 0
+    unsigned long long *sums;  // [rows][runs], of exp(x - top), in units of 1 / kOne; kNanSum
+    float *tops;               // the run's largest number
 };
+// Sums over threads are integers, so that their order does not matter.
+constexpr float kOne = 0x1p40f;
+constexpr unsigned long long kNanSum = ~0ull;
 
 // 16 bytes of logits as they lie in memory.
 template <typename T>
@@ -143,11 +168,25 @@ struct Vec<__nv_bfloat16> {
     __device__ static __forceinline__ uint32_t element(const __nv_bfloat16 *p) {
         return *reinterpret_cast<const uint16_t *>(p);
     }
-    // the largest of eight
-    __device__ static __forceinline__ float top(const uint32_t (&w)[4]) {
-        const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(w);
-        const __nv_bfloat162 m = __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3]));
-        return fmaxf(__low2float(m), __high2float(m));
+    // the largest of a vector, two numbers of which one is it; of two of these; as a number
+    using Top = __nv_bfloat162;
+    __device__ static __forceinline__ Top top(const uint32_t (&w)[4]) {
+        const Top *b = reinterpret_cast<const Top *>(w);
+        return __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3]));
+    }
+    __device__ static __forceinline__ Top larger(Top a, Top b) { return __hmax2(a, b); }
+    __device__ static __forceinline__ float number(Top t) {
+        return fmaxf(__low2float(t), __high2float(t));
+    }
+    // whether one of the two reaches `bound`, a bf16 number
+    __device__ static __forceinline__ bool reaches(Top t, float bound) {
+        uint32_t r;
+        asm("{\n\t.reg .pred p, q;\n\tsetp.ge.bf16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(r)
+            : "r"(*reinterpret_cast<const uint32_t *>(&t)),
+              "r"(__byte_perm(__float_as_uint(bound), 0, 0x3232)));
+        return r != 0;
     }
 };
 template <>
@@ -161,29 +200,43 @@ struct Vec<float> {
     __device__ static __forceinline__ uint32_t element(const float *p) {
         return *reinterpret_cast<const uint32_t *>(p);
     }
-    __device__ static __forceinline__ float top(const uint32_t (&w)[4]) {
+    using Top = float;
+    __device__ static __forceinline__ Top top(const uint32_t (&w)[4]) {
         return fmaxf(fmaxf(get(w, 0), get(w, 1)), fmaxf(get(w, 2), get(w, 3)));
     }
+    __device__ static __forceinline__ Top larger(Top a, Top b) { return fmaxf(a, b); }
+    __device__ static __forceinline__ float number(Top t) { return t; }
+    __device__ static __forceinline__ bool reaches(Top t, float bound) { return t >= bound; }
 };
 
 // The 16 bytes that hold elements [i, i + kN) of a row, whose address is a multiple of 16;
 // elements outside [0, V) become -infinity and are not read.
 template <typename T>
-__device__ __forceinline__ void load_whole(const T *row, long long i, int V, uint32_t (&w)[4]) {
+__device__ __forceinline__ void load_whole(const T *row, int i, int V, uint32_t (&w)[4]) {
+    uint4 x = make_uint4(Vec<T>::kHidden, Vec<T>::kHidden, Vec<T>::kHidden, Vec<T>::kHidden);
+    if (i >= 0 && i + Vec<T>::kN <= V) x = __ldg(reinterpret_cast<const uint4 *>(row + i));
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+}
+// The same where an end of the row lies among them: one by one, into what load_whole left.
+template <typename T>
+__device__ __noinline__ uint4 load_ends(const T *row, int i, int V) {
     using X = Vec<T>;
-    if (i >= 0 && i + X::kN <= V) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + i));
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = X::kHidden;
+    uint32_t w[4] = {X::kHidden, X::kHidden, X::kHidden, X::kHidden};
 #pragma unroll
     for (int e = 0; e < X::kN; ++e) {
         if (i + e < 0 || i + e >= V) continue;
         const uint32_t x = X::element(row + i + e);
         if constexpr (X::kN == 4) w[e] = x;
         else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | x << 16 : (w[e / 2] & 0xffff0000u) | x;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void mend_ends(const T *row, int i, int V, uint32_t (&w)[4]) {
+    constexpr int kN = Vec<T>::kN;
+    if ((i < 0 && i + kN > 0) || (i < V && i + kN > V)) {
+        const uint4 x = load_ends(row, i, V);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     }
 }
 
@@ -226,119 +279,253 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
-constexpr int kRowWarps = 8;
-
-template <typename T, int kVecs>
-__global__ void __launch_bounds__(kRowWarps * 32) k_beam_rows(const RowArgs a) {
+// sum2 += 2^(x kLog2e - base), two sums.  The product is not rounded before the difference, so
+// terms that matter, whose exponents are near 0, have their 24 bits; what base is off from
+// top kLog2e by is made up for at the end.
+template <typename T>
+__device__ __forceinline__ void add_exponentials(const uint32_t (&w)[4], float base,
+                                                 uint64_t (&sum2)[2]) {
     using X = Vec<T>;
-    constexpr int kBatch = kVecs < 4 ? kVecs : 4;
+    const uint64_t less = pack64(-base, -base), log2e = pack64(kLog2e, kLog2e);
+#pragma unroll
+    for (int e = 0; e < X::kN; e += 2) {
+        float t0, t1;
+        unpack64(fma_f32x2(pack64(X::get(w, e), X::get(w, e + 1)), log2e, less), t0, t1);
+        sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack64(ex2(t0), ex2(t1)));
+    }
+}
+// Numbers whose products with kLog2e may overflow.
+constexpr float kFar = 1e37f;
+// A thread's sum of exp(x - top) over its vectors i, i + step, ..., in the plainest form: where
+// its largest number is that far away.
+template <typename T>
+__device__ __noinline__ float far_sum(const T *row, int i, int step, int end, float top) {
+    float sum = 0.f;
+    for (; i < end; i += step)
+        for (int e = 0; e < Vec<T>::kN && i + e < end; ++e)
+            sum += ex2((Vec<T>::at(row + i + e) - top) * kLog2e);
+    return sum;
+}
+
+constexpr int kBatch = 4;                             // vectors of a thread in flight
+constexpr int kMostBatches = 8;
+constexpr int kMostV = 1 << 27;                      // (indices and their ends fit an int)
+
+// A batch of a row that begins `shift` bytes behind an address that is a multiple of 16, vectors
+// at i, i + step, ...; -infinity behind its end.
+template <typename T>
+__device__ __forceinline__ void load_any(const T *row, int i, int step, int V, int shift,
+                                         uint32_t (&w)[kBatch][4]) {
+    constexpr int kN = Vec<T>::kN;
+    i -= shift / (int)sizeof(T);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) load_whole(row, i + j * step, V, w[j]);
+    if (shift == 0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) mend_ends(row, i + j * step, V, w[j]);
+        return;
+    }
+    uint32_t b[kBatch][4];                    // (a vector lies in two pieces of 16 bytes)
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) load_whole(row, i + j * step + kN, V, b[j]);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+        mend_ends(row, i + j * step, V, w[j]);
+        mend_ends(row, i + j * step + kN, V, b[j]);
+        shifted(w[j], b[j], shift, w[j]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
+    using X = Vec<T>;
+    using Top = typename X::Top;
+    constexpr int kStep = kRowThreads * X::kN;        // elements from a thread's vector to its next
+    constexpr int kMostKept = kMostBatches * kBatch / 2;
     __shared__ Key buffers[kRowWarps][64];
+    // what a thread keeps: the largest numbers of two vectors each
+    __shared__ Top kept[kMostKept][kRowThreads];
+    __shared__ uint16_t pairs[kRowWarps][32 * kMostKept];
+    __shared__ uint32_t warp_bound[kRowWarps], warp_top[kRowWarps];
+    __shared__ unsigned long long warp_sum[kRowWarps];
+    __shared__ int warp_count[kRowWarps];
+    ptx::griddep_wait();          // (launched while the kernel before it in the stream ends)
     ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long job = (long long)blockIdx.x * kRowWarps + warp;
-    const int r = (int)(job / a.runs), run = (int)(job - (long long)r * a.runs);
-    if (r >= a.rows) return;
-    if ((a.done && a.done[r]) || a.scores[r] == -INFINITY) return;     // (nothing reads its lists)
+    const int r = blockIdx.x, run = blockIdx.y;
+    // the run: from run0 on, `there` numbers
+    const int run0 = run * a.batches * (kBatch * kStep);
+    const int there = min(a.V - run0, a.batches * (kBatch * kStep));
     const T *row = static_cast<const T *>(a.logits) + (long long)r * a.stride;
     const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15);    // bytes
-    const int ahead = shift / (int)sizeof(T);
-    const long long i0 = (long long)run * (32 * X::kN * kVecs) + lane * X::kN;
+    // batches that hold anything, and the first ones of them that can be loaded as they are
+    const int batches = (there + kBatch * kStep - 1) / (kBatch * kStep);
+    const int plain = shift ? 0 : there / (kBatch * kStep);
+    const long long job = (long long)r * a.runs + run;
 
-    float top = -INFINITY, tops[kVecs];
+    float top = -INFINITY, base = 0.f;
     uint64_t sum2[2] = {};
+    // A batch: the same steps wherever it is loaded from, so that equal rows have equal sums.
+    auto add = [&](const uint32_t (&w)[kBatch][4], int b) {
+        Top t;
 #pragma unroll
-    for (int j0 = 0; j0 < kVecs; j0 += kBatch) {
-        uint32_t w[kBatch][4];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            load_whole(row, i0 + (j0 + j) * (32 * X::kN) - ahead, a.V, w[j]);
-        if (shift) {
-            // a vector lies in two pieces of 16 bytes, the second one the next lane's
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                uint32_t b[4], x[4];
-                if (lane == 31)
-                    load_whole(row, i0 + (j0 + j) * (32 * X::kN) + X::kN - ahead, a.V, x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    b[k] = __shfl_down_sync(kAll, w[j][k], 1);
-                    if (lane == 31) b[k] = x[k];
-                }
-                shifted(w[j], b, shift, x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[j][k] = x[k];
-            }
+        for (int j = 0; j < kBatch; j += 2) {
+            const Top two = X::larger(X::top(w[j]), X::top(w[j + 1]));
+            kept[(b * kBatch + j) / 2][threadIdx.x] = two;
+            t = j == 0 ? two : X::larger(t, two);
         }
-        float most = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            tops[j0 + j] = X::top(w[j]);
-            most = fmaxf(most, tops[j0 + j]);
-        }
+        const float most = X::number(t);
         if (most > top) {
-            const float f = ex2((top - most) * kLog2e);
+            // (what lies far off is put right below, but a NaN is never lost)
+            const float to = fmaxf(most * kLog2e, -3e38f), f = top == -INFINITY ? 1.f : ex2(base - to);
             sum2[0] = mul_f32x2(sum2[0], pack64(f, f));
             sum2[1] = mul_f32x2(sum2[1], pack64(f, f));
             top = most;
+            base = to;
         }
-        // (x - top is exact where it matters, and right for numbers near fp32's end)
-        const float less = top == -INFINITY ? 0.f : -top;
-        const uint64_t less2 = pack64(less, less), log2e2 = pack64(kLog2e, kLog2e);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
+        for (int j = 0; j < kBatch; ++j) add_exponentials<T>(w[j], base, sum2);
+    };
+    const T *from = row + run0 + threadIdx.x * X::kN;
+    uint32_t next[kBatch][4];
+    auto load = [&]() {
 #pragma unroll
-            for (int e = 0; e < X::kN; e += 2) {
-                float t0, t1;
-                unpack64(mul_f32x2(add_f32x2(pack64(X::get(w[j], e), X::get(w[j], e + 1)), less2),
-                                   log2e2), t0, t1);
-                sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack64(ex2(t0), ex2(t1)));
-            }
+        for (int j = 0; j < kBatch; ++j) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(from + j * kStep));
+            next[j][0] = x.x; next[j][1] = x.y; next[j][2] = x.z; next[j][3] = x.w;
+        }
+        from += kBatch * kStep;
+    };
+    if (plain > 0) load();
+    if ((a.done && a.done[r]) || a.scores[r] == -INFINITY) return;     // (nothing reads its lists)
+    if (plain > 0) {
+#pragma unroll 2
+        for (int b = 0; b < plain; ++b) {
+            uint32_t w[kBatch][4];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[j][q] = next[j][q];
+            if (b + 1 < plain) load();
+            add(w, b);
+        }
+    }
+#pragma unroll 1
+    for (int b = plain; b < batches; ++b) {
+        uint32_t w[kBatch][4];
+        load_any<T>(row, run0 + (int)threadIdx.x * X::kN + b * (kBatch * kStep), kStep, a.V, shift, w);
+        add(w, b);
+    }
+    if (fabsf(top) > kFar && top != -INFINITY) {
+        base = 0.f;
+        sum2[0] = pack64(far_sum<T>(row, run0 + (int)threadIdx.x * X::kN, kStep, run0 + there, top), 0.f);
+        sum2[1] = 0;
     }
 
-    // the run's largest number and its sum of exponentials
+    // A number that n of the run reach: the k-th largest thread's of every warp is reached by k.
     const uint32_t mine = order_of(top);
-    const float all_top = number_of(__reduce_max_sync(kAll, mine));
+    uint32_t left = mine, bound = 0;
+    for (int k = 0; k < a.n; k += kRowWarps) {
+        bound = __reduce_max_sync(kAll, left);
+        if (k == 0 && lane == 0) warp_top[warp] = bound;
+        if (lane == __ffs(__ballot_sync(kAll, left == bound)) - 1) left = 0;
+    }
+    if (lane == 0) warp_bound[warp] = bound;
+    __syncthreads();
+    const uint32_t run_top = __reduce_max_sync(kAll, warp_top[lane & (kRowWarps - 1)]);
+    bound = __reduce_min_sync(kAll, warp_bound[lane & (kRowWarps - 1)]);
+
+    // the pairs of vectors that reach the bound ...
+    int count = 0;
     {
+        const float least = number_of(bound);
+        uint32_t reach = 0;
+#pragma unroll
+        for (int j = 0; j < kMostKept; ++j)
+            if (j < batches * (kBatch / 2))
+                reach |= X::reaches(kept[j][threadIdx.x], least) ? 1u << j : 0u;
+        for (;;) {
+            const uint32_t mask = __ballot_sync(kAll, reach != 0);
+            if (mask == 0) break;
+            if (reach) {
+                const int j = __ffs(reach) - 1;
+                pairs[warp][count + __popc(mask & ((1u << lane) - 1u))] = (uint16_t)(j * 32 + lane);
+                reach &= reach - 1;
+            }
+            count += __popc(mask);
+        }
+        count *= 2 * X::kN;
+    }
+    __syncwarp();
+    // ... and their numbers, kAhead loads of a lane together
+    constexpr int kAhead = 4;
+    int index[kAhead];
+    float number[kAhead];
+    bool in[kAhead];
+    auto look = [&](int q0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int q = q0 + 32 * k + lane, v = q < count ? pairs[warp][q / (2 * X::kN)] : 0;
+            const int vec = (v >> 5) * 2 + q / X::kN % 2;
+            index[k] = run0 + vec * kStep + (warp * 32 + (v & 31)) * X::kN + q % X::kN;
+            in[k] = q < count && index[k] < run0 + there;
+            number[k] = in[k] ? X::at(row + index[k]) : 0.f;
+        }
+    };
+    look(0);
+
+    // (meanwhile) the sum, over exp(the run's largest number)
+    {
+        const float all = number_of(run_top);
         float s[4];
         unpack64(sum2[0], s[0], s[1]);
         unpack64(sum2[1], s[2], s[3]);
-        const float f = top == all_top ? 1.f : ex2((top - all_top) * kLog2e);
-        double sum = ((double)(s[0] + s[1]) + (double)(s[2] + s[3])) * (double)f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        if (lane == 0) {
-            a.tops[job] = all_top;
-            a.sums[job] = sum;
-        }
+        float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        if (base != 0.f) sum = fmaf(sum, fmaf(-top, kLog2e, base) * 0.69314718f, sum);
+        if (top != all) sum *= ex2((top - all) * kLog2e);
+        const bool nan = __any_sync(kAll, isnan(sum));
+        // (a thread's is below 2^9 kOne; summed in two parts that stay below 2^32)
+        const unsigned long long x = __float2ull_rn(sum * kOne);
+        const uint32_t lo = __reduce_add_sync(kAll, (uint32_t)x & 0xffffffu);
+        const uint32_t hi = __reduce_add_sync(kAll, (uint32_t)(x >> 24));
+        if (lane == 0) warp_sum[warp] = nan ? kNanSum : ((unsigned long long)hi << 24) + lo;
     }
 
-    // its n best
-    Best best{buffers[warp], 0, 0, a.n};
-    best.least = (Key)__shfl_sync(kAll, sorted32(mine), a.n - 1) << 32;
-#pragma unroll 1
-    for (int j = 0; j < kVecs; ++j) {
-        float t = tops[0];
+    Best best{buffers[warp], (Key)bound << 32, 0, a.n};
+    for (int q0 = 0;;) {
 #pragma unroll
-        for (int k = 1; k < kVecs; ++k) t = j == k ? tops[k] : t;
-        const long long i = i0 + j * (32 * X::kN);
-        const bool in = i < a.V && key_of(order_of(t), (uint32_t)i) >= best.least;
-        if (!__any_sync(kAll, in)) continue;
-        float x[X::kN];
+        for (int k = 0; k < kAhead; ++k) {
+            const Key y = key_of(order_of(number[k]), (uint32_t)index[k]);
+            best.add(y, in[k] && y >= best.least);
+        }
+        q0 += 32 * kAhead;
+        if (q0 >= count) break;
+        look(q0);
+    }
+    if (best.count > a.n) best.cut();
+    if (lane == 0) warp_count[warp] = best.count;
+    __syncthreads();
+    const int c = lane < kRowWarps ? warp_count[lane] : 0;
+    const int before = __reduce_add_sync(kAll, lane < warp ? c : 0), all = __reduce_add_sync(kAll, c);
+    Key *keys = a.keys + job * (kRowWarps * a.n);
+    if (lane < best.count) keys[before + lane] = best.buf[lane];
+    for (int i = all + threadIdx.x; i < kRowWarps * a.n; i += kRowThreads) keys[i] = 0;
+    if (warp == 0) {
+        unsigned long long sum = lane < kRowWarps ? warp_sum[lane] : 0;
+        const bool nan = __any_sync(kAll, sum == kNanSum);
 #pragma unroll
-        for (int e = 0; e < X::kN; ++e)
-            x[e] = in && i + e < a.V ? X::at(row + i + e) : -INFINITY;
-#pragma unroll 1
-        for (int e = 0; e < X::kN; ++e) {
-            float y = x[0];
-#pragma unroll
-            for (int k = 1; k < X::kN; ++k) y = e == k ? x[k] : y;
-            const Key k = key_of(order_of(y), (uint32_t)(i + e));
-            best.add(k, in && i + e < a.V && k >= best.least);
+        for (int o = kRowWarps / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        if (lane == 0) {
+            a.sums[job] = nan ? kNanSum : sum;
+            a.tops[job] = number_of(run_top);
         }
     }
-    best.cut();
-    if (lane < a.n) a.keys[job * a.n + lane] = lane < best.count ? best.buf[lane] : 0;
 }
 
 struct PickArgs {
@@ -348,144 +535,195 @@ struct PickArgs {
     int32_t *out_beam, *out_token;
 };
 
-constexpr int kPickWarps = 16;
-
-__global__ void __launch_bounds__(kPickWarps * 32) k_beam_pick(const PickArgs a) {
-    __shared__ Key buffers[kPickWarps][64];
-    __shared__ unsigned long long order[kMaxBeams * kMaxBest];   // of the candidates' scores
-    __shared__ float value[kMaxBeams * kMaxBest];
-    __shared__ uint32_t token[kMaxBeams * kMaxBest];             // kAll: no candidate
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.rows.n, V = a.rows.V;
+// A CTA a group, a warp a beam (four at least).
+__global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) {
+    constexpr int kMost = kMaxBeams * kMaxBest;
+    // (keys are done with when candidates are written)
+    __shared__ union {
+        Key buffers[kMaxBeams][64];
+        struct {
+            unsigned long long order[kMost], id[kMost];     // of the scores; beam and token
+        } all;
+    } sh;
+    __shared__ double row_log[kMaxBeams];
+    __shared__ unsigned long long row_sum[kMaxBeams], kth[kMaxBeams], nth[kMaxBeams];
+    __shared__ int row_count[kMaxBeams];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = a.rows.n, V = a.rows.V;
     const int runs = a.rows.runs;
+    const bool beam = w < a.W;
+    const long long r = (long long)blockIdx.x * a.W + w;
+    const float score = beam ? a.rows.scores[r] : -INFINITY;
+    const bool dead = score == -INFINITY, done = beam && a.rows.done && a.rows.done[r];
     ptx::griddep_wait();
-    for (int w = warp; w < a.W; w += kPickWarps) {
-        const long long r = (long long)blockIdx.x * a.W + w;
-        const float score = a.rows.scores[r];
-        const bool dead = score == -INFINITY, done = a.rows.done && a.rows.done[r];
-        double val = -INFINITY;
-        uint32_t tok = kAll;
-        if (dead) {
-            if (lane < n && lane < V) tok = lane;
-        } else if (done) {
-            // `eos` first, then the lowest tokens that it is not
-            if (lane == 0) {
-                tok = a.eos;
-                val = score;
-            } else if (lane < n && lane < V) {
-                tok = lane - 1 < a.eos ? lane - 1 : lane;
-            }
-        } else {
-            const float *tops = a.rows.tops + r * runs;
-            const double *sums = a.rows.sums + r * runs;
-            float top = -INFINITY;
-            for (int i = lane; i < runs; i += 32) top = fmaxf(top, tops[i]);
-            top = number_of(__reduce_max_sync(kAll, order_of(top)));
-            double sum = 0.0;
-            for (int i = lane; i < runs; i += 32) {
-                const double s = sums[i];
-                sum += tops[i] == top ? s : s * exp((double)tops[i] - (double)top);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (isnan(sum)) {
-                if (lane < n && lane < V) {
-                    tok = lane;
-                    val = NAN;
-                }
-            } else {
-                const Key *keys = a.rows.keys + r * runs * n;
-                const int total = runs * n;
-                Best best{buffers[warp], 0, 0, n};
-                if (total > 32) {
-                    Key most = 0;
-                    for (int i = lane; i < total; i += 32) most = max(most, keys[i]);
-                    best.least = __shfl_sync(kAll, sorted32(most), n - 1);
-                }
-                if (best.least == 0) best.least = 1;          // (0 is no key)
-                for (int i = 0; i < total; i += 32) {
-                    const Key k = i + lane < total ? keys[i + lane] : 0;
-                    best.add(k, k >= best.least);
-                }
-                best.cut();
-                if (lane < best.count) {
-                    const Key k = best.buf[lane];
-                    tok = index_of(k);
-                    const float x = number_of((uint32_t)(k >> 32));
-                    if (x != -INFINITY) val = (double)score + (((double)x - (double)top) - log(sum));
-                }
-                __syncwarp();
-            }
+
+    // the row's n best, one a lane, and its sum
+    uint32_t tok = kAll;             // none
+    float x = -INFINITY, top = -INFINITY;
+    bool nan = false;
+    if (!beam) {
+    } else if (dead) {
+        if (lane < n && lane < V) tok = lane;
+    } else if (done) {
+        // `eos` first, then the lowest tokens that it is not
+        if (lane == 0) tok = a.eos;
+        else if (lane < n && lane < V) tok = lane - 1 < a.eos ? lane - 1 : lane;
+    } else {
+        const long long job = r * runs;
+        uint32_t most = 0;
+        const float first_top = lane < runs ? a.rows.tops[job + lane] : -INFINITY;
+        const unsigned long long first_sum = lane < runs ? a.rows.sums[job + lane] : 0;
+        for (int i = lane; i < runs; i += 32)
+            most = max(most, order_of(i < 32 ? first_top : a.rows.tops[job + i]));
+        top = number_of(__reduce_max_sync(kAll, most));
+        unsigned long long sum = 0;
+        for (int i = lane; i < runs; i += 32) {
+            const unsigned long long s = i < 32 ? first_sum : a.rows.sums[job + i];
+            const float t = i < 32 ? first_top : a.rows.tops[job + i];
+            nan |= s == kNanSum;
+            sum += t == top ? s : (unsigned long long)((float)s * ex2((t - top) * kLog2e));
         }
-        if (lane < n) {
-            order[w * n + lane] = order_of(val);
-            value[w * n + lane] = (float)val;
-            token[w * n + lane] = tok;
+        nan = __any_sync(kAll, nan);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        if (lane == 0) row_sum[w] = sum;
+        if (nan) {
+            if (lane < n && lane < V) tok = lane;
+        } else {
+            // keys of all runs, by a bound that n of them reach
+            Best best{sh.buffers[w], 1, 0, n};             // (0 is no key)
+            const Key *keys = a.rows.keys + job * (kRowWarps * n);
+            const int total = runs * kRowWarps * n;
+            constexpr int kHeld = 8;
+            Key y[kHeld];                                  // (all of them, for a few runs)
+            uint32_t lane_most = 0;
+            auto get = [&](int k0) {
+#pragma unroll
+                for (int q = 0; q < kHeld; ++q) {
+                    const int k = k0 + 32 * q + lane;
+                    y[q] = k < total ? keys[k] : 0;
+                }
+            };
+            for (int k0 = 0; k0 < total; k0 += 32 * kHeld) {
+                get(k0);
+#pragma unroll
+                for (int q = 0; q < kHeld; ++q) lane_most = max(lane_most, (uint32_t)(y[q] >> 32));
+            }
+            best.least = max(1ull, (Key)nth32(lane_most, n) << 32);
+            for (int k0 = 0; k0 < total; k0 += 32 * kHeld) {
+                if (total > 32 * kHeld) get(k0);
+#pragma unroll
+                for (int q = 0; q < kHeld; ++q) best.add(y[q], y[q] >= best.least);
+            }
+            best.cut();
+            if (lane < best.count && lane < n) {
+                const Key y = best.buf[lane];
+                tok = index_of(y);
+                x = number_of((uint32_t)(y >> 32));
+            }
         }
     }
     __syncthreads();
-    // each candidate's rank
-    const int total = a.W * n;
-    for (int c = threadIdx.x; c < total; c += kPickWarps * 32) {
-        const unsigned long long mine = order[c];
-        const uint32_t tok = token[c];
-        const int w = c / n;
-        if (tok == kAll) continue;
+    if (w == 0 && lane < a.W) row_log[lane] = log((double)row_sum[lane] * (1.0 / kOne));
+    __syncthreads();
+    double val = -INFINITY;
+    if (done && !dead) {
+        if (lane == 0) val = score;
+    } else if (nan) {
+        val = NAN;
+    } else if (!dead && x != -INFINITY) {
+        val = (double)score + (((double)x - (double)top) - row_log[w]);
+    }
+    const unsigned long long mine = tok == kAll ? 0 : order_of(val);
+
+    // Candidates that can be among the n best: the k-th of every beam is reached by W k, and the
+    // n-th of any by n.
+    const int k = (n + a.W - 1) / a.W;
+    if (beam && lane == k - 1) kth[w] = mine;
+    if (beam && lane == n - 1) nth[w] = mine;
+    __syncthreads();
+    unsigned long long bound = ~0ull, high = 0;
+    for (int i = 0; i < a.W; ++i) {
+        bound = min(bound, kth[i]);
+        high = max(high, nth[i]);
+    }
+    bound = max(bound, high);
+    const bool in = tok != kAll && mine >= bound;
+    const uint32_t mask = __ballot_sync(kAll, in);
+    if (beam && lane == 0) row_count[w] = __popc(mask);
+    __syncthreads();
+    const int c = lane < a.W ? row_count[lane] : 0;
+    const int total = __reduce_add_sync(kAll, c), before = __reduce_add_sync(kAll, lane < w ? c : 0);
+    if (in) {
+        const int at = before + __popc(mask & ((1u << lane) - 1u));
+        sh.all.order[at] = mine;
+        sh.all.id[at] = (unsigned long long)w << 32 | tok;
+    }
+    __syncthreads();
+    // each one's rank, by eight threads
+    const int each = blockDim.x / 8, part = threadIdx.x & 7;
+    for (int c0 = 0; c0 < total; c0 += each) {
+        const int i = c0 + threadIdx.x / 8;
+        const unsigned long long o = i < total ? sh.all.order[i] : 0, id = i < total ? sh.all.id[i] : 0;
         int rank = 0;
-        for (int i = 0; i < total; ++i) {
-            const unsigned long long o = order[i];
-            const uint32_t t = token[i];
-            // (a row's candidates follow one another, so beams are in order)
-            const bool before = o > mine || (o == mine && (i < w * n || (i < w * n + n && t < tok)));
-            rank += t != kAll && before;
+        for (int q = part; q < total; q += 8) {
+            const unsigned long long y = sh.all.order[q];
+            rank += y > o || (y == o && sh.all.id[q] < id);
         }
-        if (rank < n) {
+        rank += __shfl_xor_sync(kAll, rank, 1);
+        rank += __shfl_xor_sync(kAll, rank, 2);
+        rank += __shfl_xor_sync(kAll, rank, 4);
+        if (part == 0 && i < total && rank < n) {
             const long long at = (long long)blockIdx.x * n + rank;
-            a.out_scores[at] = value[c];
-            a.out_beam[at] = w;
-            a.out_token[at] = (int32_t)tok;
+            a.out_scores[at] = number_of_order(o);
+            a.out_beam[at] = (int32_t)(id >> 32);
+            a.out_token[at] = (int32_t)(uint32_t)id;
         }
     }
-}
-
-template <typename T, int kVecs>
-cudaError_t launch_rows(const RowArgs &a, cudaStream_t st) {
-    const long long jobs = (long long)a.rows * a.runs;
-    const int slot = timer_begin(st, "k_beam_rows");
-    k_beam_rows<T, kVecs>
-        <<<(unsigned)((jobs + kRowWarps - 1) / kRowWarps), kRowWarps * 32, 0, st>>>(a);
-    timer_end(slot, st);
-    count_launch();
-    return cudaGetLastError();
 }
 
 template <typename T>
 gdn_status select(PickArgs a, int B, cudaStream_t st) {
     RowArgs &r = a.rows;
-    // Vectors of a lane: as many as leave some eight warps an SM.
-    auto runs_of = [&](int vecs) {
-        const long long each = 32ll * Vec<T>::kN * vecs;
-        return (int)((r.V + each - 1) / each);
-    };
-    const int vecs = (long long)r.rows * runs_of(16) >= 152 * 8 ? 16 : 4;
-    r.runs = runs_of(vecs);
+    // Batches of a run: as many as fill the CTAs that fit the GPU (8 an SM) best, up to the most;
+    // few rows: one.  (What a run costs beside its batches is some two of them.)
+    constexpr int kEach = kRowThreads * Vec<T>::kN * kBatch;
+    const int all = (r.V + kEach - 1) / kEach;
+    double least = 0.0;
+    for (int b = kMostBatches; b >= 1; --b) {
+        const int runs = (all + b - 1) / b;
+        const double waves = ceil((double)r.rows * runs / (152 * 8));
+        const double cost = waves * ((all + runs - 1) / runs + 2);
+        if (b == kMostBatches || cost < least) {
+            least = cost;
+            r.runs = runs;
+        }
+    }
+    r.batches = (all + r.runs - 1) / r.runs;
+    r.runs = (all + r.batches - 1) / r.batches;
     const long long jobs = (long long)r.rows * r.runs;
-    if (jobs > (1ll << 33)) return GDN_ERR_UNSUPPORTED;
+    if (r.runs > 65535 || jobs > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     void *scratch = nullptr;
-    if (scratch_alloc(&scratch, (size_t)jobs * (8 * r.n + 12), st) != cudaSuccess) return GDN_ERR_CUDA;
+    const size_t list = (size_t)kRowWarps * r.n;
+    if (scratch_alloc(&scratch, jobs * (8 * list + 12), st) != cudaSuccess) return GDN_ERR_CUDA;
     r.keys = static_cast<Key *>(scratch);
-    r.sums = reinterpret_cast<double *>(r.keys + jobs * r.n);
+    r.sums = r.keys + jobs * list;
     r.tops = reinterpret_cast<float *>(r.sums + jobs);
-    cudaError_t e = vecs == 16 ? launch_rows<T, 16>(r, st) : launch_rows<T, 4>(r, st);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(r.rows, r.runs);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int slot = timer_begin(st, "k_beam_rows");
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_beam_rows<T>, r);
+    timer_end(slot, st);
+    count_launch();
     if (e == cudaSuccess) {
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(B);
-        cfg.blockDim = dim3(kPickWarps * 32);
-        cfg.stream = st;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        cfg.blockDim = dim3(32 * (a.W < 4 ? 4 : a.W));
         count_launch();
         e = cudaLaunchKernelEx(&cfg, k_beam_pick, a);
     }
@@ -695,7 +933,8 @@ extern "C" gdn_status gdn_beam_select(const void *logits, int64_t stride_row, co
                                       int n, gdn_dtype dt, void *stream) {
     if (B < 0 || W < 1 || V < 1 || n < 1) return GDN_ERR_INVALID_ARG;
     if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
-    if (W > kMaxBeams || n > kMaxBest || (long long)B * W > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    if (W > kMaxBeams || n > kMaxBest || V > kMostV || (long long)B * W > (1 << 24))
+        return GDN_ERR_UNSUPPORTED;
     if ((long long)W * V < n || (done && (eos < 0 || eos >= V))) return GDN_ERR_INVALID_ARG;
     if (B == 0) return GDN_OK;
     if (!logits || !scores || !out_scores || !out_beam || !out_token) return GDN_ERR_INVALID_ARG;

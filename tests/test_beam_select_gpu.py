@@ -207,6 +207,19 @@ def test_rows_that_are_not_finite_show(dt, bad):
     assert all(torch.equal(a[0], b[0]) for a, b in zip(clean, got))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [5, 30000])
+def test_a_nan_among_the_lowest_numbers_is_not_lost(dt, at):
+    # (before and after the numbers that the sum is about)
+    x = torch.full((1, 2, 40000), torch.finfo(DT[dt]).min, device="cuda").to(DT[dt])
+    x[0, :, 20000] = 1.0
+    s = torch.zeros(1, 2, device="cuda")
+    check(x, s, 3)
+    x[0, 1, at] = float("nan")
+    got = check(x, s, 3)
+    assert got[0].isnan().all() and (got[1] == 1).all()
+
+
 def test_views_streams_graphs_and_outputs():
     V = 5003
     x, s = inputs(4, 3, V, "bf16", 11)
