@@ -11,9 +11,9 @@
 // Append, one launch of two kinds of CTAs:
 // - keys and values: 16 units of 16 elements times 16 places, a thread each, so d
 //   threads a block and 256 / d blocks a CTA.  They walk over the key heads (turn,
-//   largest magnitude of the block, quantise) and the value heads, two at a time: a
-//   warp's maximum is one instruction (magnitudes compare as integers), the warps'
-//   maxima go through shared memory.  The threads of places that were there before
+//   largest magnitude of the block, quantise) and the value heads: a warp's maximum is
+//   one instruction (magnitudes compare as integers), the warps' maxima go through
+//   shared memory.  The threads of places that were there before
 //   move their codes when the block's exponent grows; in the middle of a prompt there
 //   are none, for a single token they are the other 15 sixteenths.
 // - queries: a thread holds a unit of one token with its cosines and sines and walks
@@ -27,7 +27,6 @@ namespace {
 
 using F = Fmt8;
 constexpr int kThreads = 256;
-constexpr int kFly = 2;          // heads of a thread in flight
 
 // The least exponent byte under which magnitude m is at most 448 = 1.75 * 2^8.
 __device__ __forceinline__ int exponent_for(float m) {
@@ -67,8 +66,19 @@ struct Append {
     int Hq, q_ctas_x, q_heads_per;    // CTAs of queries: tokens, then heads
     long long kv_tasks;               // blocks of keys and values, kv_ctas_x CTAs of them
     int kv_ctas_x, kv_items_per;      // items: key heads, then value heads
-    int kv_ctas;                      // CTAs of keys and values, the first of the grid
+    // The two kinds of CTAs in turn, so that the instructions of one run beside the other's
+    // waits for memory: one of the `few` in every `stride`, from the grid's first on.
+    int few, stride;
+    bool few_are_kv;
     bool rotate;
+
+    // This CTA's number among those of its kind.
+    __device__ __forceinline__ int number(bool &kv) const {
+        const int turn = blockIdx.x / stride, at = blockIdx.x - turn * stride;
+        const bool one = at == 0 && turn < few;
+        kv = one == few_are_kv;
+        return one ? turn : (int)blockIdx.x - min(few, turn + 1);
+    }
 };
 
 // The block of a task: sequence and how many blocks behind its first.  With offsets the
@@ -125,18 +135,20 @@ __device__ __forceinline__ void append_queries(const Kv &kv, const Append &ap, R
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+template <typename T, int kMinCtas>
+__global__ void __launch_bounds__(kThreads, kMinCtas)
 k_kv8_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Rows<T> qo,
              const Append ap, const __grid_constant__ Rotary rot, int *err) {
-    __shared__ uint32_t warp_most[2][kThreads / 32][kFly];
-    if ((int)blockIdx.x >= ap.kv_ctas) {
-        append_queries<T>(kv, ap, q, qo, rot, blockIdx.x - ap.kv_ctas, err);
+    __shared__ uint32_t warp_most[2][kThreads / 32];
+    bool is_kv;
+    const int cta = ap.number(is_kv);
+    if (!is_kv) {
+        append_queries<T>(kv, ap, q, qo, rot, cta, err);
         return;
     }
     const int units = kv.d / 16, psz = kv.page_size();
     const int u = threadIdx.x & (units - 1), place_in = threadIdx.x / units % F::kBlock;
-    const int bx = blockIdx.x % ap.kv_ctas_x, by = blockIdx.x / ap.kv_ctas_x;
+    const int bx = cta % ap.kv_ctas_x, by = cta / ap.kv_ctas_x;
     const int i0 = by * ap.kv_items_per, i1 = min(i0 + ap.kv_items_per, 2 * kv.H);
     const Unit un = unit_of(rot, u);
     const Unit whole{16 * u, 16 * u + 8, false};
@@ -164,20 +176,15 @@ k_kv8_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Row
             row = p & (psz - 1);
         }
     }
-    Run<T> x[kFly], y[kFly];
+    Run<T> x{}, y{};
     auto load = [&](int i) {
-#pragma unroll
-        for (int f = 0; f < kFly; ++f)
-            if (fresh && i + f < i1) {
-                const bool key = i + f < kv.H;
-                const T *p = key ? k.at(0, i + f, t) : v.at(0, i + f - kv.H, t);
-                const Unit &w = key ? un : whole;
-                x[f].load(p + w.lo);
-                y[f].load(p + w.hi);
-            }
+        if (!fresh || i >= i1) return;
+        const bool key = i < kv.H;
+        const T *p = key ? k.at(0, i, t) : v.at(0, i - kv.H, t);
+        const Unit &w = key ? un : whole;
+        x.load(p + w.lo);
+        y.load(p + w.hi);
     };
-#pragma unroll
-    for (int f = 0; f < kFly; ++f) x[f] = y[f] = Run<T>{};
     load(i0);
     float c[8], s[8];
     const bool turned = ap.rotate && un.turned;
@@ -188,74 +195,60 @@ k_kv8_append(const Kv kv, Rows<const T> k, Rows<const T> v, Rows<const T> q, Row
     const int exp_at = F::exponents_at(psz, kv.d, row) + F::exponent_of(row);
     const int warp = threadIdx.x / 32, warp0 = threadIdx.x / kv.d * (kv.d / 32);
 
-    for (int i = i0, turn_no = 0; i < i1; i += kFly, turn_no ^= 1) {
-        float a[kFly][8], e[kFly][8];
-        bool nan_a[kFly], nan_e[kFly];
-        int was[kFly];
+    for (int i = i0, turn_no = 0; i < i1; ++i, turn_no ^= 1) {
+        const bool key = i < kv.H;
+        const int h = key ? i : i - kv.H;
+        uint8_t *blk = base + (long long)h * step;
+        uint8_t *codes = blk + code_at + (key ? 0 : F::code_at(kv.d, psz));
+        uint8_t *exponent = blk + exp_at + (key ? 0 : 8);
+        float a[8], e[8];
+        x.get(a);
+        y.get(e);
+        load(i + 1);
+        // (read before the barrier that the new one is written behind)
+        const int was = had && page >= 0 ? *(volatile uint8_t *)exponent : 0;
+        if (key && turned && fresh) turn(rot.adjacent, c, s, a, e);
+        if (kv.head_scale) {
+            const float inv = __frcp_rn(__ldg(kv.head_scale + (key ? 0 : kv.H) + h));
 #pragma unroll
-        for (int f = 0; f < kFly; ++f) {
-            const bool key = i + f < kv.H;
-            const int h = key ? i + f : i + f - kv.H;
-            x[f].get(a[f]);
-            y[f].get(e[f]);
-            was[f] = 0;
-            nan_a[f] = nan_e[f] = false;
-            uint32_t most = 0;
-            if (i + f < i1) {
-                if (had && page >= 0)
-                    was[f] = *(volatile uint8_t *)(base + (long long)h * step + exp_at + (key ? 0 : 8));
-                if (key && turned && fresh) turn(rot.adjacent, c, s, a[f], e[f]);
-                if (kv.head_scale) {
-                    const float inv = __frcp_rn(__ldg(kv.head_scale + (key ? 0 : kv.H) + h));
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        a[f][m] = __fmul_rn(a[f][m], inv);
-                        e[f][m] = __fmul_rn(e[f][m], inv);
-                    }
-                }
-                const float ma = amax8(a[f]), me = amax8(e[f]);
-                // a NaN takes its 16 neighbours: of two lanes where the runs are halves of two
-                const bool halves = key && split;
-                const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
-                const float oe = __shfl_xor_sync(0xffffffffu, me, 1);
-                nan_a[f] = isnan(ma) || isnan(halves ? oa : me);
-                nan_e[f] = isnan(me) || isnan(halves ? oe : ma);
-                if (fresh) {
-                    if (!nan_a[f]) most = __float_as_uint(ma);
-                    if (!nan_e[f]) most = max(most, __float_as_uint(me));
-                }
+            for (int m = 0; m < 8; ++m) {
+                a[m] = __fmul_rn(a[m], inv);
+                e[m] = __fmul_rn(e[m], inv);
             }
-            most = __reduce_max_sync(0xffffffffu, most);
-            if ((threadIdx.x & 31) == 0) warp_most[turn_no][warp][f] = most;
         }
-        load(i + kFly);
+        const float ma = amax8(a), me = amax8(e);
+        // a NaN takes its 16 neighbours: of two lanes where the runs are halves of two
+        const bool halves = key && split;
+        const float oa = __shfl_xor_sync(0xffffffffu, ma, 1);
+        const float oe = __shfl_xor_sync(0xffffffffu, me, 1);
+        const bool nan_a = isnan(ma) || isnan(halves ? oa : me);
+        const bool nan_e = isnan(me) || isnan(halves ? oe : ma);
+        uint32_t most = 0;
+        if (fresh) {
+            if (!nan_a) most = __float_as_uint(ma);
+            if (!nan_e) most = max(most, __float_as_uint(me));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if ((threadIdx.x & 31) == 0) warp_most[turn_no][warp] = most;
         __syncthreads();
-#pragma unroll
-        for (int f = 0; f < kFly; ++f) {
-            if (i + f >= i1 || page < 0) continue;
-            uint32_t most = 0;
-            for (int w = 0; w < kv.d / 32; ++w) most = max(most, warp_most[turn_no][warp0 + w][f]);
-            const int need = exponent_for(__uint_as_float(most)), now = had ? max(need, was[f]) : need;
-            const bool key = i + f < kv.H;
-            const int h = key ? i + f : i + f - kv.H;
-            uint8_t *blk = base + (long long)h * step;
-            if (place_in == 0 && u == 0) blk[exp_at + (key ? 0 : 8)] = (uint8_t)now;
-            uint8_t *codes = blk + code_at + (key ? 0 : F::code_at(kv.d, psz));
-            if (fresh) {
-                const float p = power_of(now);
-                const uint2 ca = codes_of(a[f], p, nan_a[f]), ce = codes_of(e[f], p, nan_e[f]);
-                if (key && split) {
-                    *reinterpret_cast<uint2 *>(codes + un.lo) = ca;
-                    *reinterpret_cast<uint2 *>(codes + un.hi) = ce;
-                } else {
-                    *reinterpret_cast<uint4 *>(codes + whole.lo) = make_uint4(ca.x, ca.y, ce.x, ce.y);
-                }
-            } else if (old && now > was[f]) {
-                uint4 *at = reinterpret_cast<uint4 *>(codes + whole.lo);
-                const uint4 w = *at;
-                const __half2 p = down_f16x2(now - was[f]);
-                *at = make_uint4(moved(w.x, p), moved(w.y, p), moved(w.z, p), moved(w.w, p));
+        if (page < 0) continue;
+        for (int w = 0; w < kv.d / 32; ++w) most = max(most, warp_most[turn_no][warp0 + w]);
+        const int need = exponent_for(__uint_as_float(most)), now = had ? max(need, was) : need;
+        if (place_in == 0 && u == 0) *exponent = (uint8_t)now;
+        if (fresh) {
+            const float p = power_of(now);
+            const uint2 ca = codes_of(a, p, nan_a), ce = codes_of(e, p, nan_e);
+            if (halves) {
+                *reinterpret_cast<uint2 *>(codes + un.lo) = ca;
+                *reinterpret_cast<uint2 *>(codes + un.hi) = ce;
+            } else {
+                *reinterpret_cast<uint4 *>(codes + whole.lo) = make_uint4(ca.x, ca.y, ce.x, ce.y);
             }
+        } else if (old && now > was) {
+            uint4 *at = reinterpret_cast<uint4 *>(codes + whole.lo);
+            const uint4 w = *at;
+            const __half2 p = down_f16x2(now - was);
+            *at = make_uint4(moved(w.x, p), moved(w.y, p), moved(w.z, p), moved(w.w, p));
         }
     }
 }
@@ -320,7 +313,7 @@ int items_per_cta(long long columns, int items, int per_sm, int least_split) {
     return (items + split - 1) / split;
 }
 
-template <typename T>
+template <typename T, int kMinCtas>
 gdn_status launch_append(const Kv &kv, const gdn_rows *k, const gdn_rows *v, const gdn_rows *q,
                          const gdn_rows *qo, bool rotate, const Rotary &rot, cudaStream_t st) {
     Append ap{};
@@ -341,9 +334,11 @@ gdn_status launch_append(const Kv &kv, const gdn_rows *k, const gdn_rows *v, con
     }
     if (kx * ky + q_ctas > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     ap.kv_ctas_x = (int)kx;
-    ap.kv_ctas = (int)(kx * ky);
+    ap.few_are_kv = kx * ky <= q_ctas;
+    ap.few = (int)(ap.few_are_kv ? kx * ky : q_ctas);
+    ap.stride = ap.few > 0 ? (int)((kx * ky + q_ctas) / ap.few) : 1;
     const int slot = timer_begin(st, "k_kv8_append");
-    k_kv8_append<T><<<(unsigned)(kx * ky + q_ctas), kThreads, 0, st>>>(
+    k_kv8_append<T, kMinCtas><<<(unsigned)(kx * ky + q_ctas), kThreads, 0, st>>>(
         kv, rows_of<const T>(k), rows_of<const T>(v), rows_of<const T>(q), rows_of<T>(qo), ap, rot,
         device_error_word());
     timer_end(slot, st);
@@ -400,8 +395,9 @@ gdn_status gdn_kv8_append(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v
     Rotary r{};
     if (rot && (rc = check_rotary(rot, kv->d, true, &r)) != GDN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dt == GDN_BF16 ? launch_append<__nv_bfloat16>(dev, k, v, q, q_out, rot != nullptr, r, st)
-                          : launch_append<float>(dev, k, v, q, q_out, rot != nullptr, r, st);
+    return dt == GDN_BF16
+               ? launch_append<__nv_bfloat16, 4>(dev, k, v, q, q_out, rot != nullptr, r, st)
+               : launch_append<float, 3>(dev, k, v, q, q_out, rot != nullptr, r, st);
 }
 
 gdn_status gdn_kv8_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, gdn_dtype dt,
