@@ -62,6 +62,10 @@ constexpr int kGroup = 16;                    // tokens of a warp's step
 // here.)
 constexpr int kMany = 16;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
+// 8 bits: what the end of a piece is counted as.  64 ragged sequences of 128 to 16384 take 198 us,
+// uncounted 219 and as one tile 204, 128 of up to 8192 190 (212, 203), at d = 256 230 (291, 271);
+// as six tiles they take 198, 193 and 230.
+constexpr int kEndTiles = 3;
 constexpr float kRaise = 1.f;                 // log2: when the running maximum moves
 constexpr float kLift = 14.f;                 // log2: probabilities at the maximum
 
@@ -145,6 +149,7 @@ struct Shape {
     static constexpr int kBars = kRing + kQueries;
     static constexpr int kSmem = kBars + 2 * kStages * 8;
     static constexpr int kLead = kStages - 2;                  // tiles copied ahead
+    static constexpr bool kEnds = F::kBits == 8;
 };
 
 // S^T of a warp's group (its first row at `codes` and `scales`): K, rows
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     using Sh = Shape<F, D, kSplit, kU, kStages>;
     using V = VShare<F, D>;
     constexpr int kTile = Sh::kTile;
-    using W = Walk<kTile, Sh::kRows, kThreads>;
+    using W = Walk<kTile, Sh::kRows, kThreads, Sh::kEnds>;
     constexpr int kT = D / 16;      // m tiles of O^T = k steps of S^T
     constexpr int kParts = Sh::kParts, kRows = Sh::kRows;
     // Least probability (lifted) whose fp16 parts keep all their bits, how far the
@@ -936,6 +941,7 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     most = most > resident ? resident : most * a.kv.N;
     const int grid = (int)(most < resident ? (most < 1 ? 1 : most) : resident);
     const bool cut = a.max_len > kTile;     // else no piece of work has two tiles
+    a.end_tiles = cut && Sh::kEnds ? kEndTiles : 0;
     void *scratch = nullptr;
     if (cut && alloc_pieces<D, Sh::kRows>(a, grid, &scratch, st) != cudaSuccess) return GDN_ERR_CUDA;
     const int slot = timer_begin(st, F::kBits == 4 ? "k_kv_attn" : "k_kv8_attn");

@@ -26,6 +26,7 @@ struct AttnArgs {
     struct Cut *cuts;          // [grid], nullptr where nothing is cut
     int *err;
     uint32_t wait_limit;       // polls of a wait before it gives up
+    int end_tiles;             // what the end of a piece costs, in tiles (Plan, where it counts it)
 
     // The bounds-check build: a row of q, o and lse; one of the pieces' rows, of `rows` each
     // in two slots a CTA.
@@ -79,8 +80,10 @@ struct Seq {
 // written as zero).  CTA i of `grid` takes the tiles [total i / g, total (i + 1)
 // / g), g = min(grid, total): every CTA has the same number of tiles to within
 // one whatever the lengths, and a (sequence, head, row tile) is cut only where
-// one of the g - 1 borders falls inside it.
-template <int kTile, int kRows, int kThreads>
+// one of the g - 1 borders falls inside it.  With kEnds each (sequence, head, row tile)
+// counts `end_tiles` tiles more, behind its own and with nothing in them, for the time
+// that its end takes: a share of many short ones has fewer tiles.
+template <int kTile, int kRows, int kThreads, bool kEnds = false>
 struct Plan {
     long long prefix[kThreads];   // tiles before the sequences of each thread's share
     long long total;
@@ -102,6 +105,9 @@ struct Plan {
     __device__ static __forceinline__ int tiles(int span) {
         return max(1, (span + kTile - 1) / kTile);
     }
+    __device__ static __forceinline__ int counted(const AttnArgs &a, int span) {
+        return tiles(span) + (kEnds ? a.end_tiles : 0);
+    }
     // Tiles of row tiles [r0, r1) of one key/value head of the sequence.
     __device__ static __forceinline__ long long tiles_of(const AttnArgs &a, const Seq &s, int r0,
                                                          int r1) {
@@ -109,7 +115,7 @@ struct Plan {
         for (int rt = r0; rt < r1; ++rt) {
             int lo, span;
             range(a, s, rt, lo, span);
-            sum += tiles(span);
+            sum += counted(a, span);
         }
         return sum;
     }
@@ -179,9 +185,9 @@ struct Plan {
 
 // One CTA's walk over its pieces: the part of its tiles that belongs to one
 // (sequence, head, row tile).
-template <int kTile, int kRows, int kThreads>
+template <int kTile, int kRows, int kThreads, bool kEnds = false>
 struct Walk {
-    using P = Plan<kTile, kRows, kThreads>;
+    using P = Plan<kTile, kRows, kThreads, kEnds>;
     Seq sq;
     int b, h, rt, n_rt, lo, span, n_tiles;
     int tile0, tile1;             // the piece: tiles [tile0, tile1) of n_tiles
@@ -194,11 +200,16 @@ struct Walk {
     __device__ __forceinline__ bool complete() const { return tile0 == 0 && tile1 == n_tiles; }
     __device__ __forceinline__ int place0() const { return lo + tile0 * kTile; }
     // Tiles of the piece that hold anything.
-    __device__ __forceinline__ int count() const { return span > 0 ? tile1 - tile0 : 0; }
+    __device__ __forceinline__ int count() const {
+        if (span <= 0) return 0;
+        if constexpr (!kEnds) return tile1 - tile0;
+        const int real = P::tiles(span);
+        return min(tile1, real) - min(tile0, real);
+    }
 
     __device__ __forceinline__ void piece(const AttnArgs &a, int from) {
         P::range(a, sq, rt, lo, span);
-        n_tiles = P::tiles(span);
+        n_tiles = P::counted(a, span);
         tile0 = from;
         tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
     }
@@ -230,7 +241,7 @@ struct Walk {
         left -= __shfl_sync(0xffffffffu, upto - own, lane);
         for (rt = lane * per;; ++rt) {
             P::range(a, sq, rt, lo, span);
-            const int n = P::tiles(span);
+            const int n = P::counted(a, span);
             if (left < n) break;
             left -= n;
         }

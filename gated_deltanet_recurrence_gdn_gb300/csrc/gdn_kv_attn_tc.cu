@@ -159,6 +159,10 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
+// The same of `bytes` bytes (a multiple of 16, as the address is).
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // One token's codes and scales of K or V of a head, in registers.
 template <typename F, int D>
 struct Token;
@@ -213,43 +217,85 @@ struct Token<Fmt4, D> {
     }
 };
 
+// In 8 bits a warp's 32 tokens, two blocks of 16: a token's row is as long as a line, so its D / 16
+// pieces of 16 numbers are loaded by as many lanes (a token a thread, as in 4 bits, took 422 us
+// for the chunks below where this takes NNN).
 template <int D>
 struct Token<Fmt8, D> {
-    uint4 w[D / 16];
-    uint32_t e;               // exponent byte
-    __device__ __forceinline__ void load(const uint8_t *code, const uint8_t *exponent) {
+    static constexpr int kLanes = D / 16, kStep = 32 / kLanes, kLoads = 32 / kStep;
+    uint4 w[kLoads];
+    uint32_t e[2];            // exponent bytes
+
+    // row of the warp's 32 that load i is of
+    __device__ static __forceinline__ int row(int i) { return i * kStep + (threadIdx.x & 31) / kLanes; }
+    __device__ static __forceinline__ int piece() { return threadIdx.x & (kLanes - 1); }
+
+    // block[b]: the codes of block b's first row; exponent[b]; rows: how many of the 32 there are
+    __device__ __forceinline__ void load(const uint8_t *const (&block)[2],
+                                         const uint8_t *const (&exponent)[2], int rows) {
+        const int at = row(0) * D + 16 * piece();
+        auto get = [&](int i) {
+            return __ldg(reinterpret_cast<const uint4 *>(block[i * kStep / 16] + at + i * kStep % 16 * D));
+        };
+        if (rows >= 32) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(code) + i);
-        e = __ldg(exponent);
+            for (int i = 0; i < kLoads; ++i) w[i] = get(i);
+            e[0] = __ldg(exponent[0]);
+            e[1] = __ldg(exponent[1]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w[i] = row(i) < rows ? get(i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) e[b] = 16 * b < rows ? __ldg(exponent[b]) : 0;
     }
-    __device__ __forceinline__ void clear() {
+    // Zeroes the blocks of 16 neighbours with a NaN among them, their masks by row into `of`;
+    // whether there are any in the warp (else `of` is left as it was).
+    __device__ __forceinline__ uint32_t take_nan(uint8_t *of) {
+        uint32_t all = 0;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        e = 0;
+        for (int i = 0; i < kLoads; ++i)
+            all |= e4m3x4_nan(w[i].x) | e4m3x4_nan(w[i].y) | e4m3x4_nan(w[i].z) | e4m3x4_nan(w[i].w);
+        if (!__any_sync(0xffffffffu, all != 0)) return 0;
+#pragma unroll 1
+        for (int i = 0; i < kLoads; ++i) {
+            uint4 x = w[0];
+#pragma unroll
+            for (int k = 1; k < kLoads; ++k)
+                if (i == k) x = w[k];
+            const bool bad = (e4m3x4_nan(x.x) | e4m3x4_nan(x.y) | e4m3x4_nan(x.z) | e4m3x4_nan(x.w)) != 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, bad);
+            if (piece() == 0)
+                of[row(i)] = (uint8_t)((mask >> (threadIdx.x & 31)) & ((1u << kLanes) - 1u));
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                if (i == k && bad) w[k] = make_uint4(0, 0, 0, 0);
+        }
+        return 1;
     }
-    // Zeroes the blocks of 16 neighbours with a NaN among them; their mask.
-    __device__ __forceinline__ uint32_t take_nan() {
-        uint32_t bad = 0;
+    // The numbers as fp16 into the operand tile, row0 the warp's first row of it.
+    __device__ __forceinline__ void convert(uint32_t tile, int row0) const {
+        // (eight lanes that store together hold one row at D = 128: half of them begin with
+        // their second piece, or they would meet in the same banks)
+        const int swap = D == 128 && (piece() & 4) ? 1 : 0;
+        constexpr int kTurn = 8 / kStep;          // loads after which rows swizzle alike
+        uint32_t at[kTurn][2];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            if (e4m3x4_nan(w[i].x) | e4m3x4_nan(w[i].y) | e4m3x4_nan(w[i].z) | e4m3x4_nan(w[i].w)) {
-                bad |= 1u << i;
-                w[i] = make_uint4(0, 0, 0, 0);
-            }
-        return bad;
-    }
-    // Its D numbers as fp16 into row `row` of an operand tile.
-    __device__ __forceinline__ void convert(uint32_t tile, int row) const {
-        const __half2 f = exponent_f16x2(e);
+        for (int i = 0; i < kTurn; ++i)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            for (int k = 0; k < 2; ++k)
+                at[i][k] = chunk_at(tile, row0 + row(i), 2 * piece() + (k ^ swap)) - i * kStep * 128;
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
+        for (int i = 0; i < kLoads; ++i) {
+            const __half2 f = exponent_f16x2(e[i * kStep / 16]);
+            const uint32_t x[4] = {swap ? w[i].z : w[i].x, swap ? w[i].w : w[i].y,
+                                   swap ? w[i].x : w[i].z, swap ? w[i].y : w[i].w};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
                 uint32_t r[2], s[2];
-                e4m3x4_f16(x[k], r);
-                e4m3x4_f16(x[k + 1], s);
-                st_shared16(chunk_at(tile, row, 2 * i + k / 2), mul2(r[0], f), mul2(r[1], f),
+                e4m3x4_f16(x[2 * k], r);
+                e4m3x4_f16(x[2 * k + 1], s);
+                st_shared16(at[i % kTurn][k] + i * kStep * 128, mul2(r[0], f), mul2(r[1], f),
                             mul2(s[0], f), mul2(s[1], f));
             }
         }
@@ -373,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
     __shared__ typename W::P plan;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    // NaN blocks of V of the last four tiles' tokens, and whether a warp found any.  A tile's
+    // NaN blocks of V of the last four tiles' tokens, and whether a warp found any (if not, its
+    // tokens' may be an older tile's).  A tile's
     // are read by a row tile's softmax before its probabilities of the next tile are stored,
     // and the values of the fourth next tile are converted behind the products of the second
     // next.  A piece's last ones are read by row tile 0 before its next piece's first
@@ -485,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         if ((any[0] | any[1] | any[2] | any[3]) == 0) return;
                         const uint8_t *of = nan_of[(all + i) & 3];
                         const int t0 = place0 + i * kTile;
-                        for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e) nan |= of[e];
+                        for (int e = max(0, from - t0); e < min(kTile, to - t0); ++e)
+                            if (any[e >> 5]) nan |= of[e];
                     };
                     for (int i = 0; i < count; ++i, ++done) {
                         const int t0 = place0 + i * kTile;
@@ -667,13 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 Token<F, D> k, v;
                 auto load = [&](Token<F, D> &x, int i, int raw, bool key) {
                     const int page = a.kv.page_checked(raw, a.err);
-                    if (page < 0) {
-                        x.clear();
-                        return;
-                    }
                     const int row = (place0 + i * kTile + tok) & (psz - 1);
-                    const uint8_t *blk = a.kv.pages + a.kv.block<F>(page, h);
                     if constexpr (F::kBits == 4) {
+                        if (page < 0) {
+                            x.clear();
+                            return;
+                        }
+                        const uint8_t *blk = a.kv.pages + a.kv.block<F>(page, h);
                         if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
                             x.clear();
                             return;
@@ -681,13 +729,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                         x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
                                blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
                     } else {
-                        const int at = F::exponents_at(psz, D, row);
-                        if (!a.kv.bytes_ok<F>(page, h, at, 16)) {
-                            x.clear();
-                            return;
+                        // the two blocks of the warp, by its lanes 0 and 16 (that begin them)
+                        const uint8_t *codes[2], *exponent[2];
+                        int rows = i < count ? min(32, len - (place0 + i * kTile + (tok & ~31))) : 0;
+#pragma unroll
+                        for (int b = 1; b >= 0; --b) {
+                            const int pb = __shfl_sync(0xffffffffu, page, 16 * b);
+                            const int rb = __shfl_sync(0xffffffffu, row, 16 * b);
+                            const int at = F::exponents_at(psz, D, rb);
+                            if (pb < 0 || !a.kv.bytes_ok<F>(pb, h, at, 16)) rows = min(rows, 16 * b);
+                            const uint8_t *blk = a.kv.pages + a.kv.block<F>(max(pb, 0), h);
+                            codes[b] = blk + F::code_at(D, key ? rb : psz + rb);
+                            exponent[b] = blk + at + (key ? 0 : 8) + F::exponent_of(rb);
                         }
-                        x.load(blk + F::code_at(D, key ? row : psz + row),
-                               blk + at + (key ? 0 : 8) + F::exponent_of(row));
+                        x.load(codes, exponent, rows);
                     }
                 };
                 // brings a token of a tile to come into L2: its lines from DRAM would take
@@ -703,12 +758,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                             prefetch_l2(blk + k_scale_at(psz, D, row));
                             prefetch_l2(blk + v_scale_at(psz, D, row));
                         }
-                    } else {
-                        prefetch_l2(blk + F::code_at(D, row));
-                        prefetch_l2(blk + F::code_at(D, psz + row));
-                        if ((tok & 15) == 0) prefetch_l2(blk + F::exponents_at(psz, D, row));
+                    } else if ((tok & 15) == 0) {       // a block of 16 tokens each
+                        prefetch_l2(blk + F::code_at(D, row), 16 * D);
+                        prefetch_l2(blk + F::code_at(D, psz + row), 16 * D);
+                        prefetch_l2(blk + F::exponents_at(psz, D, row));
                     }
                 };
+                // Places that every row of the row tile sees: a NaN among their values may go
+                // through the products, and is not looked for (8 bits).
+                int all_from = 0, all_to = 0, none;
+                if constexpr (F::kBits == 8) {
+                    w.sq.sees(a, (w.row0() + w.rows(a) - 1) / a.G, all_from, none);
+                    w.sq.sees(a, w.row0() / a.G, none, all_to);
+                }
                 int page = page_at(0), next_page = page_at(1), ahead[2] = {page_at(2), page_at(3)};
                 prefetch(1, next_page);
                 prefetch(2, ahead[0]);
@@ -718,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     const int buf = n & 1;
                     const uint32_t reuse = ((n >> 1) + 1) & 1;
                     const bool k_ok = n < 2 || waits.on_lane(bar + B_K_FREE + buf, reuse);
-                    if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, tok);
+                    const int row0 = F::kBits == 4 ? tok : tok & ~31;
+                    if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, row0);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_K_FULL + buf);
@@ -729,11 +792,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     ahead[1] = page_at(i + 4);
                     load(k, i + 1, page, true);
                     const bool v_ok = n < 2 || waits.on_lane(bar + B_V_FREE + buf, reuse);
-                    const uint32_t bad = v.take_nan();
-                    nan_of[n & 3][tok] = (uint8_t)bad;
-                    const uint32_t found = __ballot_sync(0xffffffffu, bad != 0);
+                    uint32_t found;
+                    if constexpr (F::kBits == 4) {
+                        const uint32_t bad = v.take_nan();
+                        nan_of[n & 3][tok] = (uint8_t)bad;
+                        found = __ballot_sync(0xffffffffu, bad != 0);
+                    } else {
+                        const int t0 = place0 + i * kTile;
+                        found = 0;
+                        if (t0 < all_from || t0 + kTile > all_to)
+                            found = v.take_nan(&nan_of[n & 3][tok & ~31]);
+                    }
                     if (lane == 0) nan_any[n & 3][warp & 3] = found;
-                    if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, tok);
+                    if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, row0);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_V_FULL + buf);
