@@ -59,8 +59,10 @@ constexpr int kGroup = 16;                    // tokens of a warp's step
 // there and 474 in three passes of 8 rows here, 16 sequences in a window of 4096 places 34
 // and 42; up to 16 rows take 329 here.  (Some hundred places, which the rule does not look
 // at: 16 sequences of 200 to 800 take 25 and 26 us, 64 of 128 to 512 take 82 there and 63
-// here.)
-constexpr int kMany = 16;
+// here.)  In 8 bits three passes take less than there but for the longest sequences: 20 or 24
+// rows of the 64 ragged ones 563 us (there 522), of 64 of 128 to 512 places 59 (105), in the
+// window of 4096 places 44 (55); four passes, 32 rows, 746 us (522).
+constexpr int kMany4 = 16, kMany8 = 24;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
 // 8 bits: what the end of a piece is counted as.  64 ragged sequences of 128 to 16384 take 198 us,
 // uncounted 219 and as one tile 204, 128 of up to 8192 190 (212, 203), at d = 256 230 (291, 271);
@@ -1016,7 +1018,7 @@ gdn_status attention(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, flo
     a.wait_limit = limit > 0 ? (uint32_t)(limit > 0x7fffffffLL ? 0x7fffffffLL : limit) : (1u << 22);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dt == GDN_F32) return pick<F, float, true>(a, st);
-    if (a.kv.d <= 128 && (long long)a.max_new * a.G > kMany) return attn_many<F>(a, st);
+    if (a.kv.d <= 128 && (long long)a.max_new * a.G > (F::kBits == 4 ? kMany4 : kMany8)) return attn_many<F>(a, st);
     return pick<F, __nv_bfloat16, false>(a, st);
 }
 

@@ -159,10 +159,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-// The same of `bytes` bytes (a multiple of 16, as the address is).
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
+
 // One token's codes and scales of K or V of a head, in registers.
 template <typename F, int D>
 struct Token;
@@ -217,9 +214,19 @@ struct Token<Fmt4, D> {
     }
 };
 
+// 16 bytes of a line whose other parts other lanes load now: of no use in L1.
+__device__ __forceinline__ uint4 load_line(const uint8_t *p) {
+    uint4 x;      // (volatile: they are to leave where they stand, a tile ahead of their use)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+        : "l"(p));
+    return x;
+}
 // In 8 bits a warp's 32 tokens, two blocks of 16: a token's row is as long as a line, so its D / 16
-// pieces of 16 numbers are loaded by as many lanes (a token a thread, as in 4 bits, took 422 us
-// for the chunks below where this takes NNN).
+// pieces of 16 numbers are loaded by as many lanes, each piece right behind the conversion of the
+// one that had its registers, and NaN is looked for only where some row's view ends.  The chunks
+// below take 373 us and 32 rows of 64 ragged sequences 522; a token a thread, loaded behind its
+// conversion with NaN looked for in every tile, as in 4 bits, took 422 and 592.
 template <int D>
 struct Token<Fmt8, D> {
     static constexpr int kLanes = D / 16, kStep = 32 / kLanes, kLoads = 32 / kStep;
@@ -230,24 +237,23 @@ struct Token<Fmt8, D> {
     __device__ static __forceinline__ int row(int i) { return i * kStep + (threadIdx.x & 31) / kLanes; }
     __device__ static __forceinline__ int piece() { return threadIdx.x & (kLanes - 1); }
 
-    // block[b]: the codes of block b's first row; exponent[b]; rows: how many of the 32 there are
-    __device__ __forceinline__ void load(const uint8_t *const (&block)[2],
-                                         const uint8_t *const (&exponent)[2], int rows) {
-        const int at = row(0) * D + 16 * piece();
-        auto get = [&](int i) {
-            return __ldg(reinterpret_cast<const uint4 *>(block[i * kStep / 16] + at + i * kStep % 16 * D));
-        };
-        if (rows >= 32) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) w[i] = get(i);
-            e[0] = __ldg(exponent[0]);
-            e[1] = __ldg(exponent[1]);
-            return;
+    // Where the 32 tokens lie: the codes of their two blocks' first rows, the exponents, and how
+    // many of the 32 there are.
+    struct Place {
+        const uint8_t *codes[2], *exponent[2];
+        int rows;
+        __device__ __forceinline__ uint4 get(int i) const {
+            return load_line(codes[i * kStep / 16] + row(0) * D + 16 * piece() + i * kStep % 16 * D);
         }
+    };
+    __device__ __forceinline__ void load(const Place &p) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) w[i] = row(i) < rows ? get(i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kLoads; ++i) w[i] = row(i) < p.rows ? p.get(i) : make_uint4(0, 0, 0, 0);
+        load_exponents(p);
+    }
+    __device__ __forceinline__ void load_exponents(const Place &p) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) e[b] = 16 * b < rows ? __ldg(exponent[b]) : 0;
+        for (int b = 0; b < 2; ++b) e[b] = 16 * b < p.rows ? __ldg(p.exponent[b]) : 0;
     }
     // Zeroes the blocks of 16 neighbours with a NaN among them, their masks by row into `of`;
     // whether there are any in the warp (else `of` is left as it was).
@@ -273,8 +279,9 @@ struct Token<Fmt8, D> {
         }
         return 1;
     }
-    // The numbers as fp16 into the operand tile, row0 the warp's first row of it.
-    __device__ __forceinline__ void convert(uint32_t tile, int row0) const {
+    // The numbers as fp16 into the operand tile, row0 the warp's first row of it (store: whether
+    // it may be written), and each load of the next ones behind the use of its registers.
+    __device__ __forceinline__ void convert(uint32_t tile, int row0, bool store, const Place &next) {
         // (eight lanes that store together hold one row at D = 128: half of them begin with
         // their second piece, or they would meet in the same banks)
         const int swap = D == 128 && (piece() & 4) ? 1 : 0;
@@ -285,9 +292,10 @@ struct Token<Fmt8, D> {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 at[i][k] = chunk_at(tile, row0 + row(i), 2 * piece() + (k ^ swap)) - i * kStep * 128;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const __half2 f = exponent_f16x2(e[i * kStep / 16]);
+        const __half2 factor[2] = {exponent_f16x2(e[0]), exponent_f16x2(e[1])};
+        load_exponents(next);
+        auto put = [&](int i) {
+            const __half2 f = factor[i * kStep / 16];
             const uint32_t x[4] = {swap ? w[i].z : w[i].x, swap ? w[i].w : w[i].y,
                                    swap ? w[i].x : w[i].z, swap ? w[i].y : w[i].w};
 #pragma unroll
@@ -298,7 +306,20 @@ struct Token<Fmt8, D> {
                 st_shared16(at[i % kTurn][k] + i * kStep * 128, mul2(r[0], f), mul2(r[1], f),
                             mul2(s[0], f), mul2(s[1], f));
             }
+        };
+        if (store && next.rows >= 32) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                put(i);
+                w[i] = next.get(i);
+            }
+            return;
         }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (store) put(i);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w[i] = row(i) < next.rows ? next.get(i) : make_uint4(0, 0, 0, 0);
     }
 };
 
@@ -713,55 +734,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     return i < count && at < len ? a.kv.page_raw(w.b, at) : Kv::kNoPage;
                 };
                 Token<F, D> k, v;
-                auto load = [&](Token<F, D> &x, int i, int raw, bool key) {
+                auto load = [&](Token<Fmt4, D> &x, int i, int raw, bool key) {
+                    const int page = a.kv.page_checked(raw, a.err);
+                    if (page < 0) {
+                        x.clear();
+                        return;
+                    }
+                    const int row = (place0 + i * kTile + tok) & (psz - 1);
+                    if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
+                        x.clear();
+                        return;
+                    }
+                    const uint8_t *blk = a.kv.pages + a.kv.block(page, h);
+                    x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
+                           blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
+                };
+                // 8 bits: the two blocks of the warp's tokens, by its lanes 0 and 16 (that begin them)
+                auto place_of = [&](int i, int raw, bool key) {
+                    typename Token<Fmt8, D>::Place p;
                     const int page = a.kv.page_checked(raw, a.err);
                     const int row = (place0 + i * kTile + tok) & (psz - 1);
-                    if constexpr (F::kBits == 4) {
-                        if (page < 0) {
-                            x.clear();
-                            return;
-                        }
-                        const uint8_t *blk = a.kv.pages + a.kv.block<F>(page, h);
-                        if (!a.kv.bytes_ok(page, h, v_scale_at(psz, D, row), D / 16)) {
-                            x.clear();
-                            return;
-                        }
-                        x.load(blk + (key ? k_code_at(psz, D, row) : v_code_at(psz, D, row)),
-                               blk + (key ? k_scale_at(psz, D, row) : v_scale_at(psz, D, row)));
-                    } else {
-                        // the two blocks of the warp, by its lanes 0 and 16 (that begin them)
-                        const uint8_t *codes[2], *exponent[2];
-                        int rows = i < count ? min(32, len - (place0 + i * kTile + (tok & ~31))) : 0;
+                    p.rows = i < count ? min(32, len - (place0 + i * kTile + (tok & ~31))) : 0;
 #pragma unroll
-                        for (int b = 1; b >= 0; --b) {
-                            const int pb = __shfl_sync(0xffffffffu, page, 16 * b);
-                            const int rb = __shfl_sync(0xffffffffu, row, 16 * b);
-                            const int at = F::exponents_at(psz, D, rb);
-                            if (pb < 0 || !a.kv.bytes_ok<F>(pb, h, at, 16)) rows = min(rows, 16 * b);
-                            const uint8_t *blk = a.kv.pages + a.kv.block<F>(max(pb, 0), h);
-                            codes[b] = blk + F::code_at(D, key ? rb : psz + rb);
-                            exponent[b] = blk + at + (key ? 0 : 8) + F::exponent_of(rb);
-                        }
-                        x.load(codes, exponent, rows);
+                    for (int b = 1; b >= 0; --b) {
+                        const int pb = __shfl_sync(0xffffffffu, page, 16 * b);
+                        const int rb = __shfl_sync(0xffffffffu, row, 16 * b);
+                        const int at = Fmt8::exponents_at(psz, D, rb);
+                        if (pb < 0 || !a.kv.bytes_ok<Fmt8>(pb, h, at, 16)) p.rows = min(p.rows, 16 * b);
+                        const uint8_t *blk = a.kv.pages + a.kv.block<Fmt8>(max(pb, 0), h);
+                        p.codes[b] = blk + Fmt8::code_at(D, key ? rb : psz + rb);
+                        p.exponent[b] = blk + at + (key ? 0 : 8) + Fmt8::exponent_of(rb);
                     }
+                    return p;
                 };
-                // brings a token of a tile to come into L2: its lines from DRAM would take
-                // longer than the conversion of a tile
+                // 4 bits: brings a token of a tile to come into L2: its lines from DRAM would take
+                // longer than the conversion of a tile (8 bits: loads between the conversion's
+                // instructions have longer, and it changes nothing)
                 auto prefetch = [&](int i, int raw) {
-                    if ((unsigned)raw >= (unsigned)a.kv.n_pages) return;
-                    const int row = (place0 + i * kTile + tok) & (psz - 1);
-                    const uint8_t *blk = a.kv.pages + a.kv.block<F>(raw, h);
                     if constexpr (F::kBits == 4) {
+                        if ((unsigned)raw >= (unsigned)a.kv.n_pages) return;
+                        const int row = (place0 + i * kTile + tok) & (psz - 1);
+                        const uint8_t *blk = a.kv.pages + a.kv.block(raw, h);
                         prefetch_l2(blk + k_code_at(psz, D, row));
                         prefetch_l2(blk + v_code_at(psz, D, row));
                         if ((tok & 15) == 0) {      // (a page has 16 tokens at least)
                             prefetch_l2(blk + k_scale_at(psz, D, row));
                             prefetch_l2(blk + v_scale_at(psz, D, row));
                         }
-                    } else if ((tok & 15) == 0) {       // a block of 16 tokens each
-                        prefetch_l2(blk + F::code_at(D, row), 16 * D);
-                        prefetch_l2(blk + F::code_at(D, psz + row), 16 * D);
-                        prefetch_l2(blk + F::exponents_at(psz, D, row));
                     }
                 };
                 // Places that every row of the row tile sees: a NaN among their values may go
@@ -774,14 +793,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                 int page = page_at(0), next_page = page_at(1), ahead[2] = {page_at(2), page_at(3)};
                 prefetch(1, next_page);
                 prefetch(2, ahead[0]);
-                load(k, 0, page, true);
-                load(v, 0, page, false);
+                if constexpr (F::kBits == 4) {
+                    load(k, 0, page, true);
+                    load(v, 0, page, false);
+                } else {
+                    k.load(place_of(0, page, true));
+                    v.load(place_of(0, page, false));
+                }
                 for (int i = 0; i < count; ++i, ++n) {
                     const int buf = n & 1;
                     const uint32_t reuse = ((n >> 1) + 1) & 1;
                     const bool k_ok = n < 2 || waits.on_lane(bar + B_K_FREE + buf, reuse);
-                    const int row0 = F::kBits == 4 ? tok : tok & ~31;
-                    if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, row0);
+                    if constexpr (F::kBits == 4) {
+                        if (k_ok) k.convert(base + L::OFF_K + buf * L::kOperand, tok);
+                    } else {
+                        k.convert(base + L::OFF_K + buf * L::kOperand, tok & ~31, k_ok,
+                                  place_of(i + 1, next_page, true));
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_K_FULL + buf);
@@ -790,25 +818,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attn_tc(const AttnArgs a) {
                     ahead[0] = ahead[1];
                     prefetch(i + 3, ahead[0]);
                     ahead[1] = page_at(i + 4);
-                    load(k, i + 1, page, true);
+                    if constexpr (F::kBits == 4) load(k, i + 1, page, true);
                     const bool v_ok = n < 2 || waits.on_lane(bar + B_V_FREE + buf, reuse);
-                    uint32_t found;
+                    uint32_t found = 0;
                     if constexpr (F::kBits == 4) {
                         const uint32_t bad = v.take_nan();
                         nan_of[n & 3][tok] = (uint8_t)bad;
                         found = __ballot_sync(0xffffffffu, bad != 0);
                     } else {
                         const int t0 = place0 + i * kTile;
-                        found = 0;
                         if (t0 < all_from || t0 + kTile > all_to)
                             found = v.take_nan(&nan_of[n & 3][tok & ~31]);
                     }
                     if (lane == 0) nan_any[n & 3][warp & 3] = found;
-                    if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, row0);
+                    if constexpr (F::kBits == 4) {
+                        if (v_ok) v.convert(base + L::OFF_V + buf * L::kOperand, tok);
+                    } else {
+                        v.convert(base + L::OFF_V + buf * L::kOperand, tok & ~31, v_ok,
+                                  place_of(i + 1, page, false));
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + B_V_FULL + buf);
-                    load(v, i + 1, page, false);
+                    if constexpr (F::kBits == 4) load(v, i + 1, page, false);
                 }
             } while (w.next(a));
         } else {
