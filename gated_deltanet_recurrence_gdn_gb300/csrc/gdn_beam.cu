@@ -315,7 +315,7 @@ __device__ __noinline__ float far_sum(const T *row, int i, int step, int end, fl
 
 constexpr int kBatch = 4;                             // vectors of a thread in flight
 constexpr int kMostBatches = 8;
-constexpr int kMostV = 1 << 27;                      // (indices and their ends fit an int)
+constexpr int kMostV = 1 << 22;                      // (a row's sum stays below 2^63 / kOne)
 
 // A batch of a row that begins `shift` bytes behind an address that is a multiple of 16, vectors
 // at i, i + step, ...; -infinity behind its end.

@@ -960,7 +960,9 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
 }
 
 // By the head's width alone: registers hold d / 4 sums a lane, and a stage has to
-// hold the merge of the warps' sums.  (8 bits: tiles of half the places, of as many bytes.)
+// hold the merge of the warps' sums.  8 bits: tiles of half the places, of as many bytes, but
+// where one CTA an SM has the whole ring (64 ragged sequences with fp32 rows 226 us, in tiles
+// of 128 places and three stages 272, six stages 237; at d = 64 158, 172 and 167).
 template <typename F, typename T, bool kSplit>
 gdn_status pick(AttnArgs &a, cudaStream_t st) {
     constexpr int kCtas = kSplit ? 1 : 2;
@@ -972,8 +974,8 @@ gdn_status pick(AttnArgs &a, cudaStream_t st) {
         }
     } else {
         switch (a.kv.d) {
-            case 64: return launch<F, T, 64, kSplit, 2, 3, kCtas>(a, st);
-            case 128: return launch<F, T, 128, kSplit, 1, 3, kCtas>(a, st);
+            case 64: return launch<F, T, 64, kSplit, kSplit ? 4 : 2, 3, kCtas>(a, st);
+            case 128: return launch<F, T, 128, kSplit, kSplit ? 2 : 1, 3, kCtas>(a, st);
             default: return launch<F, T, 256, kSplit, 1, 3, 1>(a, st);
         }
     }

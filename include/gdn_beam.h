@@ -31,7 +31,7 @@ extern "C" {
  *   out_scores, out_beam, out_token   fp32, int32, int32 [B][n]: the continuation's score,
  *             its beam w and its token v.
  *   n         1 .. 32 (GDN_ERR_UNSUPPORTED above), at most W V.
- *   V         at most 2^27 (GDN_ERR_UNSUPPORTED above).
+ *   V         at most 2^22 (GDN_ERR_UNSUPPORTED above).
  * Equal scores go to the lowest (w, v).  Scores are compared as fp64 numbers, formed from
  * the logits exactly and from a logarithm that is within some 2^-21 of its own; they are
  * rounded to fp32 in out_scores.  A logit of -infinity scores -infinity, and so do all

@@ -19,7 +19,7 @@ def test_select_refusals(lib):  # noqa: F811
 
     assert f(B=0) == gdn.GDN_OK
     assert f(B=-1) == bad and f(W=0) == bad and f(V=0) == bad and f(n=0) == bad and f(dt=2) == bad
-    assert f(W=33) == un and f(n=33) == un and f(B=1 << 24) == un and f(V=(1 << 27) + 1) == un
+    assert f(W=33) == un and f(n=33) == un and f(B=1 << 24) == un and f(V=(1 << 22) + 1) == un
     assert f(V=1, n=4) == bad                                   # three continuations in all
     assert f(done=FAKE, eos=100) == bad and f(done=FAKE, eos=-1) == bad
     assert f(logits=None) == bad and f(scores=None) == bad

@@ -253,6 +253,17 @@ def test_views_streams_graphs_and_outputs():
         assert all(torch.equal(a, b) for a, b in zip(want, other))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("far", [False, True])
+def test_the_largest_vocabulary(dt, far):
+    # equal numbers: the largest sum that there is; and one number far above the others
+    V = 1 << 22
+    x = torch.full((1, 2, V), -1.0, device="cuda").to(DT[dt])
+    if far:
+        x[0, 0, V - 1] = x[0, 1, 0] = 30.0
+    check(x, torch.tensor([[-1.0, -1.5]], device="cuda"), 32)
+
+
 def test_rows_past_32_bits():
     # rows more than 2^31 elements apart
     V, far = 1000, (1 << 31) + 8
