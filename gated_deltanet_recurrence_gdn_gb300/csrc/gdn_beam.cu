@@ -11,14 +11,14 @@
 //   the run reach; pairs that reach it are few, and their numbers are read again from
 //   the caches to be listed (64-bit keys: the number, then the lower index).
 //   Runs are cut by index, not by address, and sums do not depend on where a row starts.
-// - k_beam_pick, a CTA a group: a warp a row joins the runs' sums in fp64 and finds the n
-//   best of their lists; the beams' candidates that a like bound leaves are ranked by their
-//   fp64 scores.
+// - k_beam_pick, a CTA a group: a warp a row joins the runs' sums and finds the n best of
+//   their lists; the beams' candidates that a like bound leaves are ranked by their scores,
+//   sums of two fp32 numbers.
 // Reading the logits bounds a large batch, latency of two launches a small one: 64 groups of 8
-// beams over 128256 bf16 logits take 37 us (131 MB; the first kernel 30, in a copy's time 19),
-// one group of 4 over 32000 in fp32 9 us.  One pass without the lists would take 23 us; the
+// beams over 128256 bf16 logits take 34 us (131 MB; the first kernel 30, in a copy's time 19),
+// one group of 4 over 32000 in fp32 8 us.  One pass without the lists would take 23 us; the
 // rest is the end of a run, which no loads run beside.  Warps that each listed the n best of
-// their runs took 154 us for the first kernel.
+// their runs took 154 us for the first kernel; scores in fp64 3 us more for the second.
 //
 // Reordering: every CTA finds by itself which beams have to move (a few instructions a
 // group, a warp each) and copies its share of 16 KB pieces.  Copying bounds it: 96 beams of six
@@ -50,15 +50,29 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 __device__ __forceinline__ float number_of(uint32_t o) {
     return __uint_as_float(o ^ ((int)o < 0 ? 0x80000000u : 0xffffffffu));
 }
-// The same of fp64, NaN above everything.
-__device__ __forceinline__ unsigned long long order_of(double x) {
-    if (isnan(x)) return ~0ull;
-    const long long u = __double_as_longlong(x + 0.0);
-    return (unsigned long long)u ^ (u < 0 ? ~0ull : 0x8000000000000000ull);
+// A sum held as two fp32 numbers, the second at most half a step of the first: 48 bits, in
+// instructions that take a tenth of fp64's time here.
+struct Two {
+    float hi, lo;
+};
+// a + b, exactly (where it does not overflow).
+__device__ __forceinline__ Two sum_of(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Two{s, isinf(s) ? 0.f : __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ float number_of_order(unsigned long long o) {
-    if (o == ~0ull) return NAN;
-    return (float)__longlong_as_double((long long)(o ^ (o >> 63 ? 0x8000000000000000ull : ~0ull)));
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two h = sum_of(a.hi, b.hi);
+    return sum_of(h.hi, __fadd_rn(h.lo, __fadd_rn(a.lo, b.lo)));
+}
+// As integers of the same order, NaN above everything.  A second number that fp64 would not hold
+// beside the first (next to a logit that masks with its type's lowest number) is left out.
+__device__ __forceinline__ unsigned long long order_of(Two x) {
+    if (isnan(x.hi)) return ~0ull;
+    if (fabsf(x.lo) < fabsf(x.hi) * 0x1p-53f) x.lo = 0.f;
+    return (unsigned long long)order_of(x.hi) << 32 | order_of(x.lo);
+}
+__device__ __forceinline__ float number_of(unsigned long long o) {
+    return o == ~0ull ? NAN : number_of((uint32_t)(o >> 32));
 }
 // Keys: the number, then the lower index; 0 is none.
 using Key = unsigned long long;
@@ -73,13 +87,12 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Descending order over a warp of one key a lane.  (Rolled and called: kernels this short wait
-// for instructions more than for a loop's.)
+// Descending order over a warp of one key a lane.  (Called, so that it is fetched once.)
 __device__ __noinline__ Key sorted32(Key x) {
     const int lane = threadIdx.x & 31;
-#pragma unroll 1
+#pragma unroll
     for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll 1
+#pragma unroll
         for (int j = k >> 1; j > 0; j >>= 1) {
             const Key y = __shfl_xor_sync(kAll, x, j);
             const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
@@ -542,7 +555,20 @@ struct PickArgs {
     int32_t *out_beam, *out_token;
 };
 
-// A CTA a group, a warp a beam (four at least).
+// A CTA a group, a warp a beam (four at least), and one more for the logarithms of their sums
+// (31 beams at most: a block has 32 warps).
+__host__ __device__ constexpr bool has_log_warp(int W) { return W < kMaxBeams; }
+__host__ __device__ constexpr int pick_warps(int W) {
+    return (W < 4 ? 4 : W) + (has_log_warp(W) ? 1 : 0);
+}
+// Named barrier 1, on which the beams' warps only arrive.
+__device__ __forceinline__ void sums_written(int warps) {
+    asm volatile("bar.arrive 1, %0;" ::"r"(32 * warps) : "memory");
+}
+__device__ __forceinline__ void sums_awaited(int warps) {
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory");
+}
+
 __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) {
     constexpr int kMost = kMaxBeams * kMaxBest;
     // (keys are done with when candidates are written)
@@ -552,7 +578,7 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
             unsigned long long order[kMost], id[kMost];     // of the scores; beam and token
         } all;
     } sh;
-    __shared__ double row_log[kMaxBeams];
+    __shared__ Two row_log[kMaxBeams];
     __shared__ unsigned long long row_sum[kMaxBeams], kth[kMaxBeams], nth[kMaxBeams];
     __shared__ int row_count[kMaxBeams];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = a.rows.n, V = a.rows.V;
@@ -561,12 +587,31 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
     const long long r = (long long)blockIdx.x * a.W + w;
     const float score = beam ? a.rows.scores[r] : -INFINITY;
     const bool dead = score == -INFINITY, done = beam && a.rows.done && a.rows.done[r];
+    // Logarithms of the rows' sums, a row a lane of one warp: fp64 instructions are few here and
+    // take long, so they run beside the other warps' search.
+    const bool log_warp = has_log_warp(a.W) ? w == (int)(blockDim.x >> 5) - 1 : w == 0;
+    auto logarithms = [&]() {
+        if (lane >= a.W) return;
+        const double x = log((double)row_sum[lane] * (1.0 / kOne));
+        const float hi = (float)x;
+        row_log[lane] = Two{hi, (float)(x - (double)hi)};
+    };
     ptx::griddep_wait();
 
     // the row's n best, one a lane, and its sum
     uint32_t tok = kAll;             // none
     float x = -INFINITY, top = -INFINITY;
     bool nan = false;
+    if (has_log_warp(a.W) && log_warp) {
+        sums_awaited(a.W + 1);
+        logarithms();
+    }
+    if (!beam) {
+    } else if (dead || done) {
+        if (lane == 0) row_sum[w] = (unsigned long long)kOne;
+        __syncwarp();
+        if (has_log_warp(a.W)) sums_written(a.W + 1);
+    }
     if (!beam) {
     } else if (dead) {
         if (lane < n && lane < V) tok = lane;
@@ -593,6 +638,8 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
         if (lane == 0) row_sum[w] = sum;
+        __syncwarp();
+        if (has_log_warp(a.W)) sums_written(a.W + 1);
         if (nan) {
             if (lane < n && lane < V) tok = lane;
         } else {
@@ -630,15 +677,18 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
         }
     }
     __syncthreads();
-    if (w == 0 && lane < a.W) row_log[lane] = log((double)row_sum[lane] * (1.0 / kOne));
-    __syncthreads();
-    double val = -INFINITY;
+    if (!has_log_warp(a.W)) {
+        if (log_warp) logarithms();
+        __syncthreads();
+    }
+    Two val{-INFINITY, 0.f};
     if (done && !dead) {
-        if (lane == 0) val = score;
+        if (lane == 0) val.hi = score;
     } else if (nan) {
-        val = NAN;
+        val.hi = NAN;
     } else if (!dead && x != -INFINITY) {
-        val = (double)score + (((double)x - (double)top) - row_log[w]);
+        const Two l = row_log[w];
+        val = add(add(sum_of(x, -top), Two{-l.hi, -l.lo}), Two{score, 0.f});
     }
     const unsigned long long mine = tok == kAll ? 0 : order_of(val);
 
@@ -681,7 +731,7 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
         rank += __shfl_xor_sync(kAll, rank, 4);
         if (part == 0 && i < total && rank < n) {
             const long long at = (long long)blockIdx.x * n + rank;
-            a.out_scores[at] = number_of_order(o);
+            a.out_scores[at] = number_of(o);
             a.out_beam[at] = (int32_t)(id >> 32);
             a.out_token[at] = (int32_t)(uint32_t)id;
         }
@@ -691,15 +741,18 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
 template <typename T>
 gdn_status select(PickArgs a, int B, cudaStream_t st) {
     RowArgs &r = a.rows;
-    // Batches of a run: as many as fill the CTAs that fit the GPU (8 an SM) best, up to the most;
-    // few rows: one.  (What a run costs beside its batches is some two of them.)
+    // Batches of a run, by the time that they take, in batches: a CTA's, and two for its end, as
+    // often as the CTAs that fit the GPU (8 an SM) are filled, and for a row's second kernel n / 14
+    // for every run.  (8, 4, 2 and 1 of them, a call's GPU time in us: 512 rows of 128256 with
+    // n = 16 41, 45, 56 and 79; 64 rows 12, 13, 14 and 20; 40 rows of 50257 with n = 5 12.6, 10.6,
+    // 9.8 and 10.2; 4 rows of 32000 in fp32 with n = 4 8.4, 7.9, 7.8 and 7.4.)
     constexpr int kEach = kRowThreads * Vec<T>::kN * kBatch;
     const int all = (r.V + kEach - 1) / kEach;
     double least = 0.0;
     for (int b = kMostBatches; b >= 1; --b) {
         const int runs = (all + b - 1) / b;
         const double waves = ceil((double)r.rows * runs / (152 * 8));
-        const double cost = waves * ((all + runs - 1) / runs + 2);
+        const double cost = waves * ((all + runs - 1) / runs + 2) + runs * r.n / 14.0;
         if (b == kMostBatches || cost < least) {
             least = cost;
             r.runs = runs;
@@ -730,7 +783,7 @@ gdn_status select(PickArgs a, int B, cudaStream_t st) {
     count_launch();
     if (e == cudaSuccess) {
         cfg.gridDim = dim3(B);
-        cfg.blockDim = dim3(32 * (a.W < 4 ? 4 : a.W));
+        cfg.blockDim = dim3(32 * pick_warps(a.W));
         count_launch();
         e = cudaLaunchKernelEx(&cfg, k_beam_pick, a);
     }

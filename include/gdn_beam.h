@@ -32,9 +32,9 @@ extern "C" {
  *             its beam w and its token v.
  *   n         1 .. 32 (GDN_ERR_UNSUPPORTED above), at most W V.
  *   V         at most 2^22 (GDN_ERR_UNSUPPORTED above).
- * Equal scores go to the lowest (w, v).  Scores are compared as fp64 numbers, formed from
- * the logits exactly and from a logarithm that is within some 2^-21 of its own; they are
- * rounded to fp32 in out_scores.  A logit of -infinity scores -infinity, and so do all
+ * Equal scores go to the lowest (w, v).  Scores are compared as sums of two fp32 numbers (48
+ * bits), formed from the logits exactly and from a logarithm that is within some 2^-21 of its
+ * own; they are rounded to fp32 in out_scores, and count as -infinity where that overflows.  A logit of -infinity scores -infinity, and so do all
  * continuations of a beam whose score is -infinity (its logits are not read) or whose
  * logits all are.  A NaN or +infinity among a beam's logits makes all its continuations
  * NaN, and a NaN ranks before every number, so that it is seen.  Scores are numbers or

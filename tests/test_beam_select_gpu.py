@@ -78,7 +78,7 @@ def inputs(B, W, V, dt, seed, size=2.0):
 
 CASES = [
     (1, 1, 1, 1), (1, 1, 2, 1), (2, 3, 1, 3), (1, 2, 7, 14), (3, 4, 31, 32), (2, 5, 257, 10),
-    (1, 4, 1000, 4), (5, 3, 4095, 6), (2, 2, 4097, 32), (1, 32, 513, 32), (7, 8, 8191, 16),
+    (1, 4, 1000, 4), (2, 31, 600, 20), (5, 3, 4095, 6), (2, 2, 4097, 32), (1, 32, 513, 32), (7, 8, 8191, 16),
     (2, 4, 32000, 8), (1, 5, 50257, 5), (40, 8, 32003, 16), (3, 16, 65536, 32), (1, 1, 300001, 20),
 ]
 
@@ -162,6 +162,19 @@ def test_banned_tokens(dt, lowest):
     x[2, 2] = off
     for n in (4, 20):
         check(x, s, n)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [3, 31, 32])
+def test_fewer_tokens_left_than_wanted(dt, W):
+    """All but two tokens at the type's lowest number: the rest goes by index (in fp64 too a score
+    next to that number is lost)."""
+    x, s = inputs(2, W, 700, dt, 17)
+    y = torch.full_like(x, torch.finfo(DT[dt]).min)
+    y[..., 50] = x[..., 50]
+    y[..., 600] = x[..., 600]
+    s[:, 3:] = -float("inf")
+    check(y, s, 20)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
