@@ -49,7 +49,8 @@
 // In 8 bits (Fmt8) the same kernel reads e4m3 codes: a warp's 16 tokens are one block, so
 // its keys' exponent is a factor of the scores, and its values' one of the converted numbers
 // (exact in fp16).  Two tokens' bytes are put side by side before the conversion (one
-// instruction per 2 numbers).  It reads twice the bytes with hardly more instructions, and
+// instruction per 2 numbers).  Above 8 rows a piece has two or three n = 8 tiles, which share
+// the conversion (eights_of).  It reads twice the bytes with hardly more instructions, and
 // DRAM bounds it:
 //   256 sequences of 8000 to 8192, 8 heads:    640 us, 6.6 TB/s (4.25 GB);
 //   64 ragged ones of 128 to 16384, 8 heads:   196 us, 6.0 TB/s (1.18 GB; 189 without the
@@ -69,11 +70,14 @@ constexpr int kGroup = 16;                    // tokens of a warp's step
 // there and 474 in three passes of 8 rows here, 16 sequences in a window of 4096 places 34
 // and 42; up to 16 rows take 329 here.  (Some hundred places, which the rule does not look
 // at: 16 sequences of 200 to 800 take 25 and 26 us, 64 of 128 to 512 take 82 there and 63
-// here.)  In 8 bits three passes take less than there but for the longest sequences: 20 or 24
-// rows of the 64 ragged ones 563 us (there 522), of 64 of 128 to 512 places 59 (105), in the
-// window of 4096 places 44 (55); four passes, 32 rows, 746 us (522).
-constexpr int kMany4 = 16, kMany8 = 24;
+// here.)  In 8 bits, up to 24 rows at once, 32 rows of the 64 ragged ones take 532 us here
+// and 517 there (at d = 64 295 and 395), of 64 of 128 to 512 places 74 and 103, in the window
+// of 4096 places 52 both; 40 rows 699 and 518 (421 and 396), 88 and 105, 65 and 53.
+constexpr int kMany4 = 16, kMany8 = 32;
 constexpr int kQueryWarp = 4, kWalkWarp = 5;  // (the first tile is copied by warp 0)
+// Which eight rows each warp brings the queries of, a hexadecimal digit a warp from the right: warps
+// 4, 6 and 7 in turn.
+constexpr uint32_t kQueryTurn = 0x21f0ffffu;
 // 8 bits: what the end of a piece is counted as.  64 ragged sequences of 128 to 16384 take 198 us,
 // uncounted 219 and as one tile 204, 128 of up to 8192 190 (212, 203), at d = 256 230 (291, 271);
 // as six tiles they take 198, 193 and 230.
@@ -139,10 +143,11 @@ __device__ __forceinline__ void operand_of(const float (&p)[4], uint32_t (&hi)[2
 // kSplit: queries and probabilities as two fp16 numbers each (fp32 I/O).
 // kU: groups of a warp in a tile.  Two groups and three stages leave room for two
 // CTAs an SM (bf16, d <= 128); two stages took 522 us where three took 462.
-template <typename F, int D, bool kSplit, int kU, int kStages>
+// kN: rows of a piece, in eights (8 bits: up to three, which share a token's conversion).
+template <typename F, int D, bool kSplit, int kN, int kU, int kStages>
 struct Shape {
     static constexpr int kTile = kWarps * kU * kGroup;
-    static constexpr int kRows = 8;
+    static constexpr int kRows = 8 * kN;
     static constexpr int kParts = kSplit ? 2 : 1;
     // a stage: key codes, value codes, key scales, value scales of a tile (8 bits: and the
     // exponents, 16 bytes a page or 128 places of it)
@@ -151,7 +156,7 @@ struct Shape {
     static constexpr int kVScale = kKScale + (F::kBits == 4 ? kTile * D / 16 : 0);
     static constexpr int kStage = kKScale + (F::kBits == 4 ? kTile * D / 8 : kTile);
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kQueries = kParts * (D / 16) * 32 * 8;
+    static constexpr int kQueries = kN * kParts * (D / 16) * 32 * 8;
     // rows of every warp that are merged at a time, in one stage
     static constexpr int kMergeRows = kWarps * 8 * D * 4 <= kStage ? 8 : 4;
     static_assert(kWarps * kMergeRows * D * 4 <= kStage, "a stage holds a merge");
@@ -168,7 +173,8 @@ struct Shape {
 // place_of(g) and 8 more, times Q^T.
 template <int D, int kParts>
 __device__ __forceinline__ void scores(Fmt4, const uint8_t *codes, const uint8_t *scales, int g,
-                                       int t4, const uint4 *queries, float (&s)[4]) {
+                                       int t4, const uint4 *queries, float (&s1)[1][4]) {
+    float (&s)[4] = s1[0];
     constexpr int kW = D / 32;      // 32-bit words of a lane's share of a row
     uint32_t kw[2][kW];
     __half2 ks[2][kW / 2];          // scale of each block, twice
@@ -223,10 +229,10 @@ __device__ __forceinline__ void scores(Fmt4, const uint8_t *codes, const uint8_t
 
 // The same of 8-bit numbers, rows g and g + 8: the group is one block, whose exponent
 // (at `exponent`) the scores are multiplied by.
-template <int D, int kParts>
+template <int D, int kParts, int kN>
 __device__ __forceinline__ void scores(Fmt8, const uint8_t *codes, const uint8_t *exponent, int g,
-                                       int t4, const uint4 *queries, float (&s)[4]) {
-    float s2[4];                    // a second chain of products
+                                       int t4, const uint4 *queries, float (&s)[kN][4]) {
+    float s2[kN][4];                // a second chain of products
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {      // 16 numbers of a row at a time
         uint32_t k[2][4];
@@ -244,21 +250,25 @@ __device__ __forceinline__ void scores(Fmt8, const uint8_t *codes, const uint8_t
             e4m3x4_f16(k[0][i + 1], b0);
             e4m3x4_f16(k[1][i + 1], b1);
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-                const uint4 q = queries[(part * (D / 32) + 2 * w + i / 2) * 32];
-                if (w == 0 && i == 0 && part == 0) {
-                    mma16816_zero(s, a0[0], a1[0], a0[1], a1[1], q.x, q.y);
-                    mma16816_zero(s2, b0[0], b1[0], b0[1], b1[1], q.z, q.w);
-                } else {
-                    mma16816(s, a0[0], a1[0], a0[1], a1[1], q.x, q.y);
-                    mma16816(s2, b0[0], b1[0], b0[1], b1[1], q.z, q.w);
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const uint4 q = queries[((n * kParts + part) * (D / 32) + 2 * w + i / 2) * 32];
+                    if (w == 0 && i == 0 && part == 0) {
+                        mma16816_zero(s[n], a0[0], a1[0], a0[1], a1[1], q.x, q.y);
+                        mma16816_zero(s2[n], b0[0], b1[0], b0[1], b1[1], q.z, q.w);
+                    } else {
+                        mma16816(s[n], a0[0], a1[0], a0[1], a1[1], q.x, q.y);
+                        mma16816(s2[n], b0[0], b1[0], b0[1], b1[1], q.z, q.w);
+                    }
                 }
-            }
         }
     }
     const float f = exponent_f32(*exponent);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * f;
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * f;
 }
 
 // A lane's numbers of V of one group: D / 8 elements of the tokens t4, 4 + (t4 ^ 1)
@@ -374,8 +384,9 @@ __device__ __forceinline__ void add_product(float (&acc)[4], uint32_t a0, uint32
 
 // O^T += V^T P^T, or with kScaled O^T += factor * (V^T P^T).
 template <int D, int kParts, bool kScaled>
-__device__ __forceinline__ void product(const VShare<Fmt4, D> &v, const uint32_t (&pf)[kParts][2],
-                                        float factor, float (&o)[D / 16][4]) {
+__device__ __forceinline__ void product(const VShare<Fmt4, D> &v,
+                                        const uint32_t (&pf)[1][kParts][2], float factor,
+                                        float (&o)[1][D / 16][4]) {
     using V = VShare<Fmt4, D>;
     __half2 sc[V::kBlocks][2];
 #pragma unroll
@@ -393,13 +404,14 @@ __device__ __forceinline__ void product(const VShare<Fmt4, D> &v, const uint32_t
         const __half2 s1 = sc[w / 2 % V::kBlocks][0], s2 = sc[w / 2 % V::kBlocks][1];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            add_product<kParts, kScaled>(o[4 * w + k], mul2(e1[k], s1), mul2(d1[k], s1),
-                                         mul2(e2[k], s2), mul2(d2[k], s2), pf, factor);
+            add_product<kParts, kScaled>(o[0][4 * w + k], mul2(e1[k], s1), mul2(d1[k], s1),
+                                         mul2(e2[k], s2), mul2(d2[k], s2), pf[0], factor);
     }
 }
-template <int D, int kParts, bool kScaled>
-__device__ __forceinline__ void product(const VShare<Fmt8, D> &v, const uint32_t (&pf)[kParts][2],
-                                        float factor, float (&o)[D / 16][4]) {
+template <int D, int kParts, bool kScaled, int kN>
+__device__ __forceinline__ void product(const VShare<Fmt8, D> &v,
+                                        const uint32_t (&pf)[kN][kParts][2], float factor,
+                                        float (&o)[kN][D / 16][4]) {
     const __half2 f = exponent_f16x2(v.e);
 #pragma unroll
     for (int w = 0; w < VShare<Fmt8, D>::kWords; ++w) {
@@ -409,15 +421,17 @@ __device__ __forceinline__ void product(const VShare<Fmt8, D> &v, const uint32_t
             uint32_t x[2], y[2];
             e4m3x4_f16(__byte_perm(v.w[0][w], v.w[1][w], k == 0 ? 0x5140 : 0x7362), x);
             e4m3x4_f16(__byte_perm(v.w[2][w], v.w[3][w], k == 0 ? 0x5140 : 0x7362), y);
-            add_product<kParts, kScaled>(o[2 * w + k], mul2(x[0], f), mul2(x[1], f), mul2(y[0], f),
-                                         mul2(y[1], f), pf, factor);
+            const uint32_t a[4] = {mul2(x[0], f), mul2(x[1], f), mul2(y[0], f), mul2(y[1], f)};
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+                add_product<kParts, kScaled>(o[n][2 * w + k], a[0], a[1], a[2], a[3], pf[n], factor);
         }
     }
 }
 
-template <typename F, typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename F, typename T, int D, bool kSplit, int kN, int kU, int kStages, int kMinCtas>
 __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a) {
-    using Sh = Shape<F, D, kSplit, kU, kStages>;
+    using Sh = Shape<F, D, kSplit, kN, kU, kStages>;
     using V = VShare<F, D>;
     constexpr int kTile = Sh::kTile;
     using W = Walk<kTile, Sh::kRows, kThreads, Sh::kEnds>;
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     __shared__ float row_mul[kRows];
     __shared__ W walk[3];           // the piece at work and the two after it, in a ring
     __shared__ bool walk_more[3];   // whether there is one behind each
-    __shared__ int row_from[kRows], row_to[kRows], all_seen[2];
+    __shared__ int row_from[kRows], row_to[kRows], all_seen[kN][2];
     uint4 *queries = reinterpret_cast<uint4 *>(smem + Sh::kRing);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Sh::kBars), *empty = full + kStages;
 
@@ -524,10 +538,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         }
     };
 
-    // Queries of a piece, by one warp: the lane's part of row g, loaded ...
+    // Queries of a piece, eight rows a warp: the lane's part of row 8 n + g, loaded ...
+    const int q_n = kN == 1 ? 0 : (int)(kQueryTurn >> 4 * warp) & 15;
+    const bool q_warp = kN == 1 ? warp == kQueryWarp : q_n < kN;
     auto row_of = [&](const W &w, bool &there, int &j) {
-        const int r = w.row0() + g;
-        there = g < w.rows(a);
+        const int r = w.row0() + 8 * q_n + g;
+        there = 8 * q_n + g < w.rows(a);
         j = there ? r / a.G : 0;
         const int i = there ? r - j * a.G : 0;
         if (there) there = a.row_ok((long long)w.sq.first + j, w.h * a.G + i);
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
                 lo[e] = pack_f16(u - f.x, y - f.y);
             }
-            uint4 *q = queries + k * 32 + lane;
+            uint4 *q = queries + (q_n * kParts * (D / 32) + k) * 32 + lane;
             q[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             if constexpr (kSplit) q[(D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -584,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         if (there) w.sq.sees(a, j, from, to);
         if (t4 == 0) {
             const float gk = a.kv.head_scale ? __ldg(a.kv.head_scale + w.h) : 1.f;
-            row_mul[g] = down * a.scale_log2 * gk;
-            row_from[g] = from;
-            row_to[g] = to;
+            row_mul[8 * q_n + g] = down * a.scale_log2 * gk;
+            row_from[8 * q_n + g] = from;
+            row_to[8 * q_n + g] = to;
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
@@ -594,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
             to = min(to, __shfl_xor_sync(0xffffffffu, to, o));
         }
         if (lane == 0) {
-            all_seen[0] = from;
-            all_seen[1] = to;
+            all_seen[q_n][0] = from;
+            all_seen[q_n][1] = to;
         }
     };
 
@@ -616,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     }
     __syncthreads();
     Run<T> raw_q[D / 32];
-    if (warp == kQueryWarp) {
+    if (q_warp) {
         load_queries(walk[0], raw_q);
         put_queries(walk[0], raw_q);
     } else if (warp == kWalkWarp) {
@@ -644,17 +660,25 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         fetch_next();
         if (next < min(Sh::kLead, n_copy)) produce_next();
         if (tiles_before == 0) __syncthreads();     // (later ones: with the merge's last)
-        const int all_from = all_seen[0], all_to = all_seen[1];   // places that every row sees
-        float mul[2], o[kT][4], sub[2], sum[2];   // sub: what scores lose before ex2
+        int all_from = all_seen[0][0], all_to = all_seen[0][1];   // places that every row sees
 #pragma unroll
-        for (int i = 0; i < kT; ++i)
+        for (int n = 1; n < kN; ++n) {
+            all_from = max(all_from, all_seen[n][0]);
+            all_to = min(all_to, all_seen[n][1]);
+        }
+        float mul[kN][2], o[kN][kT][4], sub[kN][2], sum[kN][2];   // sub: what scores lose before ex2
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        for (int n = 0; n < kN; ++n) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mul[e] = row_mul[2 * t4 + e];
-            sub[e] = -INFINITY;
-            sum[e] = 0.f;
+            for (int i = 0; i < kT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mul[n][e] = row_mul[8 * n + 2 * t4 + e];
+                sub[n][e] = -INFINITY;
+                sum[n][e] = 0.f;
+            }
         }
         // The first tile of the piece after this one, copied by warp `after`: its pages are
         // looked up before this piece's last tile is worked on and copied behind it.
@@ -686,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 if (!arrived || t0 >= len) break;
                 const bool whole = t0 >= all_from && t0 + kGroup <= all_to;
 
-                float s[4];
+                float s[kN][4];
                 V v;
                 if constexpr (F::kBits == 4) {
                     scores<D, kParts>(F(), buf, sbuf, g, t4, queries + lane, s);
@@ -704,68 +728,78 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                 // Scores in log2 units less the row's `sub`, so that the row's largest number
                 // is about kLift.  One comparison finds those that call for more: above
                 // kLift + kRaise the maximum moves; below kLow probabilities lose bits.
-                float t[4];
+                float t[kN][4];
                 bool more = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t[e] = fmaf(s[e], mul[e & 1], -sub[e & 1]);
-                    if (!whole) {
-                        const int at = t0 + row_of_place<F>(g) + 8 * (e >> 1), r = 2 * t4 + (e & 1);
-                        if (at < row_from[r] || at >= row_to[r]) t[e] = -INFINITY;
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        t[n][e] = fmaf(s[n][e], mul[n][e & 1], -sub[n][e & 1]);
+                        if (!whole) {
+                            const int at = t0 + row_of_place<F>(g) + 8 * (e >> 1);
+                            const int r = 8 * n + 2 * t4 + (e & 1);
+                            if (at < row_from[r] || at >= row_to[r]) t[n][e] = -INFINITY;
+                        }
+                        more |= fabsf(t[n][e] - kMid) > kHalf;
                     }
-                    more |= fabsf(t[e] - kMid) > kHalf;
-                }
                 const bool extra = __any_sync(0xffffffffu, more);
                 if (extra) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // (+infinity in t is a row's first score: its own value decides)
-                        float m = -INFINITY;
+                    for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int k = e; k < 4; k += 2)
-                            m = fmaxf(m, t[k] == -INFINITY ? -INFINITY : s[k] * mul[e]);
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m -= kLift;
-                        if (m > sub[e] + kRaise) {
-                            const float f = ex2(sub[e] - m);
-                            sub[e] = m;
-                            sum[e] *= f;
+                        for (int e = 0; e < 2; ++e) {
+                            // (+infinity in t is a row's first score: its own value decides)
+                            float m = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < kT; ++k) {
-                                o[k][e] *= f;
-                                o[k][e + 2] *= f;
+                            for (int k = e; k < 4; k += 2)
+                                m = fmaxf(m, t[n][k] == -INFINITY ? -INFINITY : s[n][k] * mul[n][e]);
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            m -= kLift;
+                            if (m > sub[n][e] + kRaise) {
+                                const float f = ex2(sub[n][e] - m);
+                                sub[n][e] = m;
+                                sum[n][e] *= f;
+#pragma unroll
+                                for (int k = 0; k < kT; ++k) {
+                                    o[n][k][e] *= f;
+                                    o[n][k][e + 2] *= f;
+                                }
                             }
-                        }
 #pragma unroll
-                        for (int k = e; k < 4; k += 2)
-                            if (t[k] != -INFINITY) t[k] = fmaf(s[k], mul[e], -sub[e]);
-                    }
+                            for (int k = e; k < 4; k += 2)
+                                if (t[n][k] != -INFINITY)
+                                    t[n][k] = fmaf(s[n][k], mul[n][e], -sub[n][e]);
+                        }
                 }
 
-                uint32_t pf[kParts][2];
-                float p[4], rest[4];
+                uint32_t pf[kN][kParts][2];
+                float p[kN][4], rest[kN][4];
                 bool low = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(t[e]);
-                    sum[e & 1] += p[e];
-                }
-                if (extra) {      // the small ones later, in a product of their own
+                for (int n = 0; n < kN; ++n) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        rest[e] = 0.f;
-                        if (p[e] < kLow) {
-                            rest[e] = p[e];
-                            p[e] = 0.f;
-                        }
-                        low |= rest[e] > 0.f;
+                        p[n][e] = ex2(t[n][e]);
+                        sum[n][e & 1] += p[n][e];
                     }
+                    if (extra) {      // the small ones later, in a product of their own
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            rest[n][e] = 0.f;
+                            if (p[n][e] < kLow) {
+                                rest[n][e] = p[n][e];
+                                p[n][e] = 0.f;
+                            }
+                            low |= rest[n][e] > 0.f;
+                        }
+                    }
+                    operand_of<kSplit>(p[n], pf[n][0], pf[n][kParts - 1]);
                 }
-                operand_of<kSplit>(p, pf[0], pf[kParts - 1]);
                 if (!whole) {
-                    // Places behind the sequence's end may hold anything: they become 0.  A NaN that some rows see and others do not would reach all of them through
+                    // Places behind the sequence's end may hold anything: they become 0.  A NaN
+                    // that some rows see and others do not would reach all of them through
                     // 0 * NaN: it is taken out of the product and put into the rows that see it.
                     constexpr int kBlocks = V::kBlocks;
                     uint32_t nan[kBlocks] = {};
@@ -787,19 +821,21 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                             nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 1);
                             nan[k] |= __shfl_xor_sync(0xffffffffu, nan[k], 2);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int r = 2 * t4 + e;
-                                const int lo = min(16, max(0, row_from[r] - t0));
-                                const int hi = min(16, max(0, row_to[r] - t0));
-                                const uint32_t seen = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
-                                if (nan[k] & seen) {
+                            for (int n = 0; n < kN; ++n)
 #pragma unroll
-                                    for (int m = 0; m < kT / kBlocks; ++m) {
-                                        o[k * (kT / kBlocks) + m][e] = NAN;
-                                        o[k * (kT / kBlocks) + m][e + 2] = NAN;
+                                for (int e = 0; e < 2; ++e) {
+                                    const int r = 8 * n + 2 * t4 + e;
+                                    const int lo = min(16, max(0, row_from[r] - t0));
+                                    const int hi = min(16, max(0, row_to[r] - t0));
+                                    const uint32_t seen = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+                                    if (nan[k] & seen) {
+#pragma unroll
+                                        for (int m = 0; m < kT / kBlocks; ++m) {
+                                            o[n][k * (kT / kBlocks) + m][e] = NAN;
+                                            o[n][k * (kT / kBlocks) + m][e + 2] = NAN;
+                                        }
                                     }
                                 }
-                            }
                         }
                     }
                 }
@@ -812,13 +848,16 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
                         factor *= 1.f / kBand;
                         low = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            rest[e] *= kBand;
-                            p[e] = rest[e] >= kLow ? rest[e] : 0.f;
-                            if (p[e] > 0.f) rest[e] = 0.f;
-                            low |= rest[e] > 0.f;
+                        for (int n = 0; n < kN; ++n) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                rest[n][e] *= kBand;
+                                p[n][e] = rest[n][e] >= kLow ? rest[n][e] : 0.f;
+                                if (p[n][e] > 0.f) rest[n][e] = 0.f;
+                                low |= rest[n][e] > 0.f;
+                            }
+                            operand_of<kSplit>(p[n], pf[n][0], pf[n][kParts - 1]);
                         }
-                        operand_of<kSplit>(p, pf[0], pf[kParts - 1]);
                         product<D, kParts, true>(v, pf, factor, o);
                     } while (__any_sync(0xffffffffu, low));
                 }
@@ -841,13 +880,15 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
 
         // the warps' sums of this piece
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x = sum[e];
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            x += __shfl_xor_sync(0xffffffffu, x, 8);
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            if (g == 0) warp_ml[warp][2 * t4 + e] = make_float2(sub[e], x);
-        }
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = sum[n][e];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (g == 0) warp_ml[warp][8 * n + 2 * t4 + e] = make_float2(sub[n][e], x);
+            }
         __syncthreads();
         if (*waits.abort) break;        // (no wait is made between here and the next barrier)
         const W &w = walk[piece];
@@ -867,26 +908,28 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
         constexpr int kMr = Sh::kMergeRows;
         const bool more = walk_more[piece];
         // what the next piece starts with, by warps that have less of the merge to do
-        if (more && warp == kQueryWarp) load_queries(walk[after_piece], raw_q);
+        if (more && q_warp) load_queries(walk[after_piece], raw_q);
 #pragma unroll
         for (int half = 0; half < kRows / kMr; ++half) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 2 * t4 + e - half * kMr;
-                if (r < 0 || r >= kMr) continue;
-                float m = -INFINITY;
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][2 * t4 + e].x);
-                const float f = m == -INFINITY ? 1.f : ex2(sub[e] - m);
-                float *p = merge + (warp * kMr + r) * D + g * (D / 8);
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * n + 2 * t4 + e - half * kMr;
+                    if (r < 0 || r >= kMr) continue;
+                    float m = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < kT; ++k)
-                    *reinterpret_cast<float2 *>(p + 2 * k) =
-                        make_float2(o[k][e] * f, o[k][e + 2] * f);
-            }
+                    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, warp_ml[k][8 * n + 2 * t4 + e].x);
+                    const float f = m == -INFINITY ? 1.f : ex2(sub[n][e] - m);
+                    float *p = merge + (warp * kMr + r) * D + g * (D / 8);
+#pragma unroll
+                    for (int k = 0; k < kT; ++k)
+                        *reinterpret_cast<float2 *>(p + 2 * k) =
+                            make_float2(o[n][k][e] * f, o[n][k][e + 2] * f);
+                }
             __syncthreads();
             if (half == 0 && more) {
-                if (warp == kQueryWarp) put_queries(walk[after_piece], raw_q);
+                if (q_warp) put_queries(walk[after_piece], raw_q);
                 else if (warp == kWalkWarp) walk_on(after_piece, 3 - piece - after_piece);
             }
             for (int x = threadIdx.x; x < min(kMr, rows - half * kMr) * (D / 4); x += kThreads) {
@@ -929,10 +972,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_kv_attn(const AttnArgs a
     if (*waits.abort && warp == 0) drain_ring<kStages>(full, armed);
 }
 
-template <typename F, typename T, int D, bool kSplit, int kU, int kStages, int kMinCtas>
+template <typename F, typename T, int D, bool kSplit, int kN, int kU, int kStages, int kMinCtas>
 gdn_status launch(AttnArgs &a, cudaStream_t st) {
-    using Sh = Shape<F, D, kSplit, kU, kStages>;
-    auto kern = k_kv_attn<F, T, D, kSplit, kU, kStages, kMinCtas>;
+    using Sh = Shape<F, D, kSplit, kN, kU, kStages>;
+    auto kern = k_kv_attn<F, T, D, kSplit, kN, kU, kStages, kMinCtas>;
     constexpr int kTile = Sh::kTile;
     static std::atomic<int> memo[kMaxDeviceMemo];
     // resident CTAs of the device, and the opt-in to the ring's shared memory
@@ -969,25 +1012,51 @@ gdn_status launch(AttnArgs &a, cudaStream_t st) {
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// By the head's width alone: registers hold d / 4 sums a lane, and a stage has to
+// Eights of rows that a piece has in 8 bits: as many as the registers hold sums for (d / 4 a lane
+// each), in passes of the same number.  64 ragged sequences of 128 to 16384 places, 16 rows: two
+// eights 276 us, one by one 384 (d = 256 340 and 468, fp32 rows 345 and 454); 24 rows three eights
+// 372, two 517, one 564 (fp32 490, 635; d = 64 in fp32 338, 439).  512 rows over 12001 to 16384
+// places, fp32: three eights 872 us, two 900, one 1238; at d = 256 two 1458, one 2121.  At d = 64
+// two fit twice on an SM: 24 rows 285 us, as three once 270; 16 rows 163, once 200.  Up to 1024
+// places the ends of the pieces count for more, and twice as many CTAs an SM (bf16, d = 128) take
+// 47 us for 16 rows of 64 sequences of 512 where two eights take 52, 63 and 65 at 1024 places
+// (at 2048 92 and 87).
+int eights_of(const AttnArgs &a, bool split) {
+    if (a.kv.d == 128 && !split && a.max_len <= 1024) return 1;
+    const int most = a.kv.d == 256 || (a.kv.d == 64 && !split) ? 2 : 3;
+    const long long rows = (long long)a.max_new * a.G, all = rows > 8 ? (rows + 7) / 8 : 1;
+    const long long passes = (all + most - 1) / most;
+    return (int)((all + passes - 1) / passes);
+}
+
+// By the head's width: registers hold d / 4 sums a lane and eight rows, and a stage has to
 // hold the merge of the warps' sums.  8 bits: tiles of half the places, of as many bytes, but
 // where one CTA an SM has the whole ring (64 ragged sequences with fp32 rows 226 us, in tiles
 // of 128 places and three stages 272, six stages 237; at d = 64 158, 172 and 167).
 template <typename F, typename T, bool kSplit>
 gdn_status pick(AttnArgs &a, cudaStream_t st) {
-    constexpr int kCtas = kSplit ? 1 : 2;
+    constexpr int kCtas = kSplit ? 1 : 2, kWide = kSplit ? 2 : 1;
     if constexpr (F::kBits == 4) {
         switch (a.kv.d) {
-            case 64: return launch<F, T, 64, kSplit, 2, 3, kCtas>(a, st);
-            case 128: return launch<F, T, 128, kSplit, 2, 3, kCtas>(a, st);
-            default: return launch<F, T, 256, kSplit, 1, 4, 1>(a, st);
+            case 64: return launch<F, T, 64, kSplit, 1, 2, 3, kCtas>(a, st);
+            case 128: return launch<F, T, 128, kSplit, 1, 2, 3, kCtas>(a, st);
+            default: return launch<F, T, 256, kSplit, 1, 1, 4, 1>(a, st);
         }
     } else {
-        switch (a.kv.d) {
-            case 64: return launch<F, T, 64, kSplit, kSplit ? 4 : 2, 3, kCtas>(a, st);
-            case 128: return launch<F, T, 128, kSplit, kSplit ? 2 : 1, 3, kCtas>(a, st);
-            default: return launch<F, T, 256, kSplit, 1, 3, 1>(a, st);
+        const int n = eights_of(a, kSplit);
+        if (a.kv.d == 64) {
+            if (n == 1) return launch<F, T, 64, kSplit, 1, 2 * kWide, 3, kCtas>(a, st);
+            if constexpr (kSplit)
+                if (n == 3) return launch<F, T, 64, kSplit, 3, 2 * kWide, 3, kCtas>(a, st);
+            return launch<F, T, 64, kSplit, 2, 2 * kWide, 3, kCtas>(a, st);
         }
+        if (a.kv.d == 128) {
+            if (n == 1) return launch<F, T, 128, kSplit, 1, kWide, 3, kCtas>(a, st);
+            return n == 2 ? launch<F, T, 128, kSplit, 2, 2, 3, 1>(a, st)
+                          : launch<F, T, 128, kSplit, 3, 2, 3, 1>(a, st);
+        }
+        return n == 1 ? launch<F, T, 256, kSplit, 1, 1, 3, 1>(a, st)
+                      : launch<F, T, 256, kSplit, 2, 1, 3, 1>(a, st);
     }
 }
 
@@ -1030,7 +1099,8 @@ gdn_status attention(const gdn_kv *kv, const gdn_rows *q, const gdn_rows *o, flo
     a.wait_limit = limit > 0 ? (uint32_t)(limit > 0x7fffffffLL ? 0x7fffffffLL : limit) : (1u << 22);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dt == GDN_F32) return pick<F, float, true>(a, st);
-    if (a.kv.d <= 128 && (long long)a.max_new * a.G > (F::kBits == 4 ? kMany4 : kMany8)) return attn_many<F>(a, st);
+    constexpr int kMany = F::kBits == 4 ? kMany4 : kMany8;
+    if (a.kv.d <= 128 && (long long)a.max_new * a.G > kMany) return attn_many<F>(a, st);
     return pick<F, __nv_bfloat16, false>(a, st);
 }
 

@@ -159,7 +159,7 @@ gdn_status gdn_kv_read(const gdn_kv *kv, const gdn_rows *k, const gdn_rows *v, g
  *             from which the launch is planned (a larger device value is
  *             reported as GDN_ERR_INVALID_ARG by gdn_sync_check()).  max_new
  *             also chooses the kernel for the whole call (bf16, d <= 128: above
- *             16 rows max_new * Hq / H, in 8 bits 24, the one for many rows), so a bound far
+ *             16 rows max_new * Hq / H, in 8 bits 32, the one for many rows), so a bound far
  *             above what the sequences have costs time.
  * The cache's numbers enter the tensor cores exactly (e2m1 * e4m3 fits fp16);
  * with bf16 rows the probabilities are rounded to fp16 (11 bits, down to 2^-22

@@ -104,3 +104,14 @@ def test_a_page_outside_the_pool_is_no_access(checked_lib):
                 call()
             assert e.value.status == gdn.GDN_ERR_INVALID_ARG
             clean(checked_lib)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [10, 20])
+def test_attention_of_several_eights_of_rows(checked_lib, new, d, io):
+    from tests.test_kv8_attn_gpu import check, queries
+    c = R8.Cache8([1800, 0, 1025, 7], 2, 32, d, new=[new] * 4, seed=78)
+    check(c, queries(c.tokens, 2, d, io, "thd", 79))
+    clean(checked_lib)
