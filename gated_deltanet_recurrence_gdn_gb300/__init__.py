@@ -125,6 +125,9 @@ def load(path: str | None = None):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    # (for the binding's native part, which calls them itself)
+    lib.address = {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                   for name, _, _ in ABI}
     if path is None:
         _lib = lib
     return lib

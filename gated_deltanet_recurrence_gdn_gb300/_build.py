@@ -1,9 +1,11 @@
-"""Builds libgdn.so in-tree with nvcc for sm_103a (no cmake, no torch)."""
+"""Builds libgdn.so in-tree with nvcc for sm_103a (no cmake, no torch), and beside it _bind.so, the
+binding's native part, with the host compiler against Python's and PyTorch's headers."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -11,6 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BIND, BIND_SRC = os.path.join(PKG, "_bind.so"), os.path.join(CSRC, "gdn_bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 
@@ -29,6 +32,21 @@ def _stale(out, deps):
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _bind_job(out):
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    system = [sysconfig.get_paths()["include"], os.path.join(at, "include"),
+              os.path.join(at, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-I", os.path.join(ROOT, "include")]
+    for path in system:
+        cmd += ["-isystem", path]
+    return cmd + [BIND_SRC, "-o", out, "-L" + os.path.join(at, "lib"), "-ltorch_python",
+                  "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 # Build variants: name -> extra nvcc flags.  "check" is the debug
@@ -54,19 +72,25 @@ def build(force: bool = False, verbose: bool = False, extra=(), variant=None) ->
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             jobs.append([NVCC] + _flags() + list(extra) + ["-c", src, "-o", obj])
+    objects = len(jobs)
+    bind_tmp = BIND + ".tmp%d" % os.getpid()
+    if variant is None and (force or _stale(BIND, [BIND_SRC] + headers)):
+        jobs.append(_bind_job(bind_tmp))
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n%s\n%s" % (" ".join(cmd), r.stdout + r.stderr))
+            raise RuntimeError("compiler failed:\n%s\n%s" % (" ".join(cmd), r.stdout + r.stderr))
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(lib_path, objs):
+    if len(jobs) > objects:
+        os.replace(bind_tmp, BIND)
+    if force or objects or _stale(lib_path, objs):
         tmp = lib_path + ".tmp%d" % os.getpid()
         run([NVCC] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, lib_path)

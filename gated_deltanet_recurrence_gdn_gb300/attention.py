@@ -131,6 +131,9 @@ def _page_size8(size, d):
     return n if n > 0 and 2 * n * d + 16 * max(1, n // 128) == size else 0
 
 
+_PAGE_SIZE = {4: _page_size4, 8: _page_size8}
+
+
 def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at, page_size_of=_page_size4):
     """The packed gdn_kv, and the cache's heads and page size."""
     if pages.dim() != 3 or pages.dtype != _u8 or pages.get_device() != at or \
@@ -164,6 +167,23 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at, page_s
     return _KV.pack(pages.data_ptr(), scale, page_table.data_ptr(), kv_len.data_ptr(), cu, n_pages,
                     page_size, heads, d, N, max_pages, n_tokens, page_table.stride(0)), \
         heads, page_size
+
+
+_native_kept = None
+
+
+def _native():
+    """The binding's native part (csrc/gdn_bind.cpp): its functions make a call whose arguments are
+    all as they have to be, and else answer NotImplemented, upon which Python's checks follow."""
+    global _native_kept
+    if _native_kept is None:
+        try:
+            from . import _bind as native
+        except ImportError as e:
+            raise ImportError("_bind.so is not built; run __graft_entry__.build()") from e
+        native.set_error(GdnError)
+        _native_kept = native
+    return _native_kept
 
 
 def _call(fn, what, at, check, *args):
@@ -280,7 +300,7 @@ def gdn_kv_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, k
     pages: the cache (gdn_kv_pages), written in place; page_table int32 [N, pages]; kv_len int32
     [N], the sequences' tokens with the new ones; cu_seqlens int32 [N + 1] or None for the same
     number of new tokens each; kv_scale fp32 [2, heads]: a further scale per head."""
-    return _append("gdn_kv_append", _page_size4, pages, k, v, page_table, kv_len, q, cu_seqlens,
+    return _append("gdn_kv_append", 4, pages, k, v, page_table, kv_len, q, cu_seqlens,
                    kv_scale, cos, sin, pos, axes, adjacent, out, check)
 
 
@@ -289,12 +309,18 @@ def gdn_kv8_append(pages, k, v, page_table, kv_len, *, q=None, cu_seqlens=None, 
     """gdn_kv_append to a cache in 8 bits (gdn_kv8_pages).  A block of 16 places has one exponent
     for its keys and one for its values: where a new token is too large for it, the block's other
     rows are rounded again under the larger one."""
-    return _append("gdn_kv8_append", _page_size8, pages, k, v, page_table, kv_len, q, cu_seqlens,
+    return _append("gdn_kv8_append", 8, pages, k, v, page_table, kv_len, q, cu_seqlens,
                    kv_scale, cos, sin, pos, axes, adjacent, out, check)
 
 
-def _append(name, page_size_of, pages, k, v, page_table, kv_len, q, cu_seqlens, kv_scale, cos, sin,
+def _append(name, bits, pages, k, v, page_table, kv_len, q, cu_seqlens, kv_scale, cos, sin,
             pos, axes, adjacent, out, check):
+    if not check:
+        r = _native().append(load().address[name], name, bits, pages, k, v, page_table, kv_len, q,
+                             cu_seqlens, kv_scale, cos, sin, pos, axes, adjacent, out)
+        if r is not NotImplemented:
+            return r
+    page_size_of = _PAGE_SIZE[bits]
     if k.dtype not in _DT or k.dim() != 3:
         raise ValueError("k must be [tokens, heads, d], bf16 or fp32")
     at = _device("k", k)
@@ -324,19 +350,25 @@ def gdn_kv_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_s
                 dtype=torch.bfloat16, out=None, check=False):
     """The last n_tokens tokens (packed as in gdn_kv_append) back from the cache, as the values
     they are held as: (k, v), each [tokens, heads, d] of `dtype`."""
-    return _read("gdn_kv_read", _page_size4, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
+    return _read("gdn_kv_read", 4, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
                  kv_scale, dtype, out, check)
 
 
 def gdn_kv8_read(pages, page_table, kv_len, n_tokens, d, *, cu_seqlens=None, kv_scale=None,
                  dtype=torch.bfloat16, out=None, check=False):
     """gdn_kv_read from a cache in 8 bits."""
-    return _read("gdn_kv8_read", _page_size8, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
+    return _read("gdn_kv8_read", 8, pages, page_table, kv_len, n_tokens, d, cu_seqlens,
                  kv_scale, dtype, out, check)
 
 
-def _read(name, page_size_of, pages, page_table, kv_len, n_tokens, d, cu_seqlens, kv_scale, dtype,
+def _read(name, bits, pages, page_table, kv_len, n_tokens, d, cu_seqlens, kv_scale, dtype,
           out, check):
+    if not check:
+        r = _native().read(load().address[name], name, bits, pages, page_table, kv_len, n_tokens, d,
+                           cu_seqlens, kv_scale, dtype, out)
+        if r is not NotImplemented:
+            return r
+    page_size_of = _PAGE_SIZE[bits]
     if dtype not in _DT:
         raise ValueError("k and v are read as bf16 or fp32")
     at = _device("pages", pages)
@@ -365,7 +397,7 @@ def gdn_kv_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None,
     plan the launch and choose its kernel.  A decode step that carries cu_seqlens should pass
     max_new=1: without it the call is planned for one sequence that has all the tokens.  scale:
     default d^-1/2.  window: a token sees the last `window` places up to its own (0: all)."""
-    return _attn("gdn_kv_attn", _page_size4, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
+    return _attn("gdn_kv_attn", 4, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
                  max_len, max_new, scale, causal, window, out, return_lse, check)
 
 
@@ -373,12 +405,19 @@ def gdn_kv8_attn(q, pages, page_table, kv_len, *, cu_seqlens=None, kv_scale=None
                  max_new=None, scale=None, causal=True, window=0, out=None, return_lse=False,
                  check=False):
     """gdn_kv_attn over a cache in 8 bits."""
-    return _attn("gdn_kv8_attn", _page_size8, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
+    return _attn("gdn_kv8_attn", 8, q, pages, page_table, kv_len, cu_seqlens, kv_scale,
                  max_len, max_new, scale, causal, window, out, return_lse, check)
 
 
-def _attn(name, page_size_of, q, pages, page_table, kv_len, cu_seqlens, kv_scale, max_len, max_new,
+def _attn(name, bits, q, pages, page_table, kv_len, cu_seqlens, kv_scale, max_len, max_new,
           scale, causal, window, out, return_lse, check):
+    if not check:
+        r = _native().attn(load().address[name], name, bits, q, pages, page_table, kv_len,
+                           cu_seqlens, kv_scale, max_len, max_new, scale, causal, window, out,
+                           return_lse)
+        if r is not NotImplemented:
+            return r
+    page_size_of = _PAGE_SIZE[bits]
     if q.dtype not in _DT or q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d], bf16 or fp32")
     at = _device("q", q)

@@ -11,7 +11,7 @@ import struct
 import torch
 
 from . import _DT, _i, _vp, load
-from .attention import _call, _device, _f32, _i32, _int32
+from .attention import _call, _device, _f32, _i32, _int32, _native
 
 _i64 = ctypes.c_int64
 
@@ -41,6 +41,11 @@ def gdn_beam_select(logits, scores, n=None, *, done=None, eos=None, out=None, ch
     [B, W], the beams' own, to which a token's log-probability is added.  done: bool or uint8
     [B, W], beams that go on with token `eos` alone, at the score that they have.  Equal scores go
     to the lowest (beam, token).  out: (scores, beam, token) to write."""
+    if not check:
+        r = _native().select(load().address["gdn_beam_select"], "gdn_beam_select", logits, scores, n,
+                             done, eos, out)
+        if r is not NotImplemented:
+            return r
     at = _device("logits", logits)
     if scores.dim() != 2 or logits.dtype not in _DT or logits.dim() not in (2, 3):
         raise ValueError("logits must be [B, W, V] or [B * W, V], bf16 or fp32, and scores [B, W]")
@@ -107,6 +112,11 @@ def gdn_beam_reorder(parent, slots, *, states=(), caches=(), page_table=None, ow
     pages are shared by the tables, and of a page that is partly filled the others get a copy in
     every cache of `caches` (gdn_kv_pages, gdn_kv8_pages).  A sequence starts with table rows
     own_pages[slots].  out: slots, or (slots, page_table), to write; not the inputs."""
+    if not check:
+        r = _native().reorder(load().address["gdn_beam_reorder"], "gdn_beam_reorder", parent, slots,
+                              states, caches, page_table, own_pages, kv_len, page_size, out)
+        if r is not NotImplemented:
+            return r
     at = _device("parent", parent)
     if parent.dim() != 2:
         raise ValueError("parent must be [B, W]")
