@@ -34,9 +34,13 @@ def _stale(out, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _bind_job(out):
+def _torch():
     import torch
-    at = os.path.dirname(torch.__file__)
+    return os.path.dirname(torch.__file__)
+
+
+def _bind_job(out):
+    at = _torch()
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     system = [sysconfig.get_paths()["include"], os.path.join(at, "include"),
               os.path.join(at, "include", "torch", "csrc", "api", "include"),
@@ -74,7 +78,8 @@ def build(force: bool = False, verbose: bool = False, extra=(), variant=None) ->
             jobs.append([NVCC] + _flags() + list(extra) + ["-c", src, "-o", obj])
     objects = len(jobs)
     bind_tmp = BIND + ".tmp%d" % os.getpid()
-    if variant is None and (force or _stale(BIND, [BIND_SRC] + headers)):
+    bind_deps = [BIND_SRC, os.path.join(_torch(), "version.py")] + headers
+    if variant is None and (force or _stale(BIND, bind_deps)):
         jobs.append(_bind_job(bind_tmp))
 
     def run(cmd):
