@@ -213,6 +213,22 @@ struct Walk {
         tile0 = from;
         tile1 = (int)min((long long)n_tiles, tile0 + (end - cur));
     }
+    // Of a call whose pieces are one tile each (nothing is cut and no end counted), the same
+    // number in every sequence: without a plan.
+    __device__ static __forceinline__ long long alike_total(const AttnArgs &a) {
+        return (long long)a.kv.N * a.kv.H * P::row_tiles(a, Seq{0, a.kv.n_tokens / a.kv.N, 0});
+    }
+    __device__ __forceinline__ void start_alike(const AttnArgs &a, long long at, long long until) {
+        cur = at;
+        end = until;
+        n_rt = P::row_tiles(a, Seq{0, a.kv.n_tokens / a.kv.N, 0});
+        const long long head = quot(at, n_rt);
+        rt = (int)(at - head * n_rt);
+        b = (int)quot(head, a.kv.H);
+        h = (int)(head - (long long)b * a.kv.H);
+        sq.get(a, b);
+        piece(a, 0);
+    }
     // By whole warps.
     __device__ void start(const AttnArgs &a, const P &plan, long long at, long long until) {
         cur = at;
