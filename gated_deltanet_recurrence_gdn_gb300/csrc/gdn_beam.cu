@@ -320,10 +320,17 @@ __device__ __forceinline__ void add_exponentials(const uint32_t (&w)[4], float b
         sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack64(ex2(t0), ex2(t1)));
     }
 }
-// Numbers whose products with kLog2e may overflow.
-constexpr float kFar = 1e37f;
-// A thread's sum of exp(x - top) over its vectors i, i + step, ..., in the plainest form: where
-// its largest number is that far away.
+// Where base = top kLog2e is rounded, every term is off by 2^r, r up to half a step of base.  Below
+// kFar r is at most 2^-11, and 1 - r ln 2 makes up for it to 2^-24.  Further out (a vocabulary
+// masked with -1e10, say) only a sum of exp(x - top), top taken off first, is right.
+constexpr float kFar = 1e4f;
+// So base stops here, where a thread's top is that far down: its terms become 0, not infinite.
+constexpr float kLeastBase = -16384.f;
+static_assert(kLeastBase < -kFar * kLog2e, "numbers that are not far have their own base");
+// log2 of what a thread's sum is at least divided by where it does not count any more (of 2^8 terms,
+// in units of 1 / kOne).
+constexpr float kApart = 64.f;
+// A thread's sum of exp(x - top) over its vectors i, i + step, ..., in the plainest form.
 template <typename T>
 __device__ __noinline__ float far_sum(const T *row, int i, int step, int end, float top) {
     float sum = 0.f;
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
         const float most = X::number(t);
         if (most > top) {
             // (what lies far off is put right below, but a NaN is never lost)
-            const float to = fmaxf(most * kLog2e, -3e38f), f = top == -INFINITY ? 1.f : ex2(base - to);
+            const float to = fmaxf(most * kLog2e, kLeastBase), f = top == -INFINITY ? 1.f : ex2(base - to);
             sum2[0] = mul_f32x2(sum2[0], pack64(f, f));
             sum2[1] = mul_f32x2(sum2[1], pack64(f, f));
             top = most;
@@ -442,12 +449,6 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
         load_any<T>(row, run0 + (int)threadIdx.x * X::kN + b * (kBatch * kStep), kStep, a.V, shift, w);
         add(w, b);
     }
-    if (fabsf(top) > kFar && top != -INFINITY) {
-        base = 0.f;
-        sum2[0] = pack64(far_sum<T>(row, run0 + (int)threadIdx.x * X::kN, kStep, run0 + there, top), 0.f);
-        sum2[1] = 0;
-    }
-
     // A number that n of the run reach: the k-th largest thread's of every warp is reached by k.
     const uint32_t mine = order_of(top);
     uint32_t left = mine, bound = 0;
@@ -460,6 +461,19 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
     __syncthreads();
     const uint32_t run_top = __reduce_max_sync(kAll, warp_top[lane & (kRowWarps - 1)]);
     bound = __reduce_min_sync(kAll, warp_bound[lane & (kRowWarps - 1)]);
+    const float all = number_of(run_top);
+
+    // A thread with numbers that are far down alone, next to others in the run: its sum does not
+    // count.  (It is 0, or NaN; above 0 it may be infinite, and is always formed again.)  So 512
+    // rows of 128256, 99 % of them masked, take what unmasked ones do; with every such thread's
+    // numbers read again they took 41 us more.
+    if (fabsf(top) > kFar && top != -INFINITY) {
+        base = 0.f;
+        if (top > 0.f || (all - top) * kLog2e < kApart) {
+            sum2[0] = pack64(far_sum<T>(row, run0 + (int)threadIdx.x * X::kN, kStep, run0 + there, top), 0.f);
+            sum2[1] = 0;
+        }
+    }
 
     // the pairs of vectors that reach the bound ...
     int count = 0;
@@ -502,7 +516,6 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
 
     // (meanwhile) the sum, over exp(the run's largest number)
     {
-        const float all = number_of(run_top);
         float s[4];
         unpack64(sum2[0], s[0], s[1]);
         unpack64(sum2[1], s[2], s[3]);
@@ -532,10 +545,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_beam_rows(const RowArgs a) {
     if (lane == 0) warp_count[warp] = best.count;
     __syncthreads();
     const int c = lane < kRowWarps ? warp_count[lane] : 0;
-    const int before = __reduce_add_sync(kAll, lane < warp ? c : 0), all = __reduce_add_sync(kAll, c);
+    const int before = __reduce_add_sync(kAll, lane < warp ? c : 0), kept_all = __reduce_add_sync(kAll, c);
     Key *keys = a.keys + job * (kRowWarps * a.n);
     if (lane < best.count) keys[before + lane] = best.buf[lane];
-    for (int i = all + threadIdx.x; i < kRowWarps * a.n; i += kRowThreads) keys[i] = 0;
+    for (int i = kept_all + threadIdx.x; i < kRowWarps * a.n; i += kRowThreads) keys[i] = 0;
     if (warp == 0) {
         unsigned long long sum = lane < kRowWarps ? warp_sum[lane] : 0;
         const bool nan = __any_sync(kAll, sum == kNanSum);
