@@ -703,7 +703,11 @@ __global__ void __launch_bounds__(kMaxBeams * 32) k_beam_pick(const PickArgs a) 
         const Two l = row_log[w];
         val = add(add(sum_of(x, -top), Two{-l.hi, -l.lo}), Two{score, 0.f});
     }
-    const unsigned long long mine = tok == kAll ? 0 : order_of(val);
+    // (The lanes' logits fall, but their sums' roundings may turn two neighbours around: such a
+    // sum counts as the one before it, so that a beam's k-th is the least of its first k.)
+    unsigned long long mine = tok == kAll ? 0 : order_of(val);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) mine = min(mine, __shfl_up_sync(kAll, mine, o));
 
     // Candidates that can be among the n best: the k-th of every beam is reached by W k, and the
     // n-th of any by n.
