@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+import warnings
 
 import torch
 
@@ -172,6 +173,15 @@ def _kv(pages, page_table, kv_len, cu_seqlens, kv_scale, n_tokens, d, at, page_s
 _native_kept = None
 
 
+class _NoNative:
+    """In place of the binding's native part where that cannot be loaded: Python makes every call."""
+
+    @staticmethod
+    def append(*args):
+        return NotImplemented
+    read = attn = select = reorder = append
+
+
 def _native():
     """The binding's native part (csrc/gdn_bind.cpp): its functions make a call whose arguments are
     all as they have to be, and else answer NotImplemented, upon which Python's checks follow."""
@@ -179,9 +189,11 @@ def _native():
     if _native_kept is None:
         try:
             from . import _bind as native
+            native.set_error(GdnError)
         except ImportError as e:
-            raise ImportError("_bind.so is not built; run __graft_entry__.build()") from e
-        native.set_error(GdnError)
+            warnings.warn("calls go without the binding's native part, which takes the host 5 to 20 us "
+                          "more each: %s (run __graft_entry__.build())" % e, RuntimeWarning)
+            native = _NoNative
         _native_kept = native
     return _native_kept
 
