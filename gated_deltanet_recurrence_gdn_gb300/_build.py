@@ -1,11 +1,14 @@
-"""Builds libgdn.so in-tree with nvcc for sm_103a (no cmake, no torch), and beside it _bind.so, the
-binding's native part, with the host compiler against Python's and PyTorch's headers."""
+"""Builds libgdn.so in-tree with nvcc for sm_103a (no cmake, no torch), and beside it, where that can
+be done, _bind.so, the binding's native part, with the host compiler against Python's and PyTorch's
+headers."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,12 +38,13 @@ def _stale(out, deps):
 
 
 def _torch():
-    import torch
-    return os.path.dirname(torch.__file__)
+    """PyTorch's folder (it is not imported for this), None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
-def _bind_job(out):
-    at = _torch()
+def _bind_job(at, out):
+    """The command that builds _bind.so as `out` against PyTorch in folder `at`."""
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     system = [sysconfig.get_paths()["include"], os.path.join(at, "include"),
               os.path.join(at, "include", "torch", "csrc", "api", "include"),
@@ -51,6 +55,26 @@ def _bind_job(out):
         cmd += ["-isystem", path]
     return cmd + [BIND_SRC, "-o", out, "-L" + os.path.join(at, "lib"), "-ltorch_python",
                   "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _build_bind(force, headers, run):
+    """Builds _bind.so where it is not up to date.  Answers why that cannot be done (None: it is
+    done): calls then go by Python, and one that is out of date is taken away."""
+    at = _torch()
+    if at is None:
+        return "there is no PyTorch"
+    if not force and not _stale(BIND, [BIND_SRC, os.path.join(at, "version.py")] + headers):
+        return None
+    tmp = BIND + ".tmp%d" % os.getpid()
+    try:
+        run(_bind_job(at, tmp))
+        os.replace(tmp, BIND)
+        return None
+    except (OSError, RuntimeError) as e:
+        for path in (tmp, BIND):
+            if os.path.exists(path):
+                os.remove(path)
+        return str(e)
 
 
 # Build variants: name -> extra nvcc flags.  "check" is the debug
@@ -76,11 +100,6 @@ def build(force: bool = False, verbose: bool = False, extra=(), variant=None) ->
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             jobs.append([NVCC] + _flags() + list(extra) + ["-c", src, "-o", obj])
-    objects = len(jobs)
-    bind_tmp = BIND + ".tmp%d" % os.getpid()
-    bind_deps = [BIND_SRC, os.path.join(_torch(), "version.py")] + headers
-    if variant is None and (force or _stale(BIND, bind_deps)):
-        jobs.append(_bind_job(bind_tmp))
 
     def run(cmd):
         if verbose:
@@ -91,11 +110,13 @@ def build(force: bool = False, verbose: bool = False, extra=(), variant=None) ->
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        bind = ex.submit(_build_bind, force, headers, run) if variant is None else None
         list(ex.map(run, jobs))
-    if len(jobs) > objects:
-        os.replace(bind_tmp, BIND)
-    if force or objects or _stale(lib_path, objs):
+    error = bind.result() if bind else None
+    if error:
+        warnings.warn("the binding's native part is not built: %s" % error, RuntimeWarning)
+    if force or jobs or _stale(lib_path, objs):
         tmp = lib_path + ".tmp%d" % os.getpid()
         run([NVCC] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, lib_path)
