@@ -17,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BIND, BIND_SRC = os.path.join(PKG, "_bind.so"), os.path.join(CSRC, "gdn_bind.cpp")
+BIND_MADE_OF = os.path.join(BUILD, "bind.txt")     # what _bind.so was built by and against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 
@@ -57,18 +58,30 @@ def _bind_job(at, out):
                   "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _bind_made_of(at):
+    """What a _bind.so is good for: the command, Python's ABI, and the PyTorch, whatever its date."""
+    with open(os.path.join(at, "version.py")) as f:
+        version = f.read()
+    return "\n".join(_bind_job(at, "") + [str(sysconfig.get_config_var("SOABI")), version])
+
+
 def _build_bind(force, headers, run):
     """Builds _bind.so where it is not up to date.  Answers why that cannot be done (None: it is
     done): calls then go by Python, and one that is out of date is taken away."""
     at = _torch()
     if at is None:
         return "there is no PyTorch"
-    if not force and not _stale(BIND, [BIND_SRC, os.path.join(at, "version.py")] + headers):
-        return None
     tmp = BIND + ".tmp%d" % os.getpid()
     try:
+        made_of = _bind_made_of(at)
+        if not force and not _stale(BIND, [BIND_SRC] + headers) and os.path.exists(BIND_MADE_OF):
+            with open(BIND_MADE_OF) as f:
+                if f.read() == made_of:
+                    return None
         run(_bind_job(at, tmp))
         os.replace(tmp, BIND)
+        with open(BIND_MADE_OF, "w") as f:
+            f.write(made_of)
         return None
     except (OSError, RuntimeError) as e:
         for path in (tmp, BIND):
