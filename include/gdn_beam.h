@@ -34,11 +34,15 @@ extern "C" {
  *   V         at most 2^22 (GDN_ERR_UNSUPPORTED above).
  * Equal scores go to the lowest (w, v).  Scores are compared as sums of two fp32 numbers (48
  * bits), formed from the logits exactly and from a logarithm that is within some 2^-21 of its
- * own; they are rounded to fp32 in out_scores, and count as -infinity where that overflows.  A logit of -infinity scores -infinity, and so do all
- * continuations of a beam whose score is -infinity (its logits are not read) or whose
- * logits all are.  A NaN or +infinity among a beam's logits makes all its continuations
- * NaN, and a NaN ranks before every number, so that it is seen.  Scores are numbers or
- * -infinity.  The same inputs give the same bits, and equal rows of a call equal scores.
+ * own, whatever the logits' magnitude; they are rounded to fp32 in out_scores, and count as
+ * -infinity where that overflows.  Within a beam they fall with the logits: what rounding would
+ * put above a larger logit's counts as equal to it.
+ * A logit of -infinity scores -infinity, and so do all continuations of a beam whose score is
+ * -infinity or whose logits all are.  A NaN or +infinity among a beam's logits makes all its
+ * continuations NaN, and a NaN ranks before every number, so that it is seen.  The logits of a
+ * beam that is done, or whose score is -infinity, do not matter, but are memory that is read
+ * all the same.  Scores are numbers or -infinity.  The same inputs give the same bits, and equal
+ * rows of a call equal scores.
  */
 gdn_status gdn_beam_select(const void *logits, int64_t stride_row, const float *scores,
                            const uint8_t *done, int eos, float *out_scores, int32_t *out_beam,
