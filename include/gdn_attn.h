@@ -184,7 +184,8 @@ int64_t gdn_kv8_page_bytes(int page_size, int d);
  * over the head's scale, is at most 448 (so 22 where there is an infinity); a block that
  * has tokens before them keeps at least the one that it has, and where it grows their
  * codes are divided by the same power of two, to nearest even.  An element becomes the
- * nearest e4m3 number to its quotient, at most 448 (ties to even).  What is above the
+ * nearest e4m3 number to its quotient, at most 448 (ties to even; quotients by the head's
+ * scale are products with its fp32 reciprocal, here and in the largest magnitude).  What is above the
  * range, 57344 times the head's scale, becomes that; a NaN makes the 16 neighbours
  * along d that it is among NaN, and they do not count for the exponent.  A page that a
  * call writes belongs to one sequence of the call.
