@@ -18,7 +18,11 @@
 // beams over 128256 bf16 logits take 34 us (131 MB; the first kernel 30, in a copy's time 19),
 // one group of 4 over 32000 in fp32 8 us.  One pass without the lists would take 23 us; the
 // rest is the end of a run, which no loads run beside.  Warps that each listed the n best of
-// their runs took 154 us for the first kernel; scores in fp64 3 us more for the second.
+// their runs took 154 us for the first kernel; scores in fp64 3 us more for the second.  Rows that do
+// not begin at a multiple of 16 bytes load nothing ahead (64 x 8 beams over 50257 take 25 us, over
+// 50264 17), and of a run whose numbers are nearly all alike all are listed (the 64 groups over 128256,
+// all tokens but 30 neighbours masked: 128 us with -infinity, 160 with a number, whose sums are
+// formed again as well; with 1 % of the tokens left 35).
 //
 // Reordering: every CTA finds by itself which beams have to move (a few instructions a
 // group, a warp each) and copies its share of 16 KB pieces.  Copying bounds it: 96 beams of six

@@ -52,7 +52,7 @@
 // instruction per 2 numbers).  Above 8 rows a piece has two or three n = 8 tiles, which share
 // the conversion (eights_of).  It reads twice the bytes with hardly more instructions, and
 // DRAM bounds it:
-//   256 sequences of 8000 to 8192, 8 heads:    640 us, 6.6 TB/s (4.25 GB);
+//   256 sequences of 8000 to 8192, 8 heads:    646 us, 6.6 TB/s (4.25 GB);
 //   64 ragged ones of 128 to 16384, 8 heads:   196 us, 6.0 TB/s (1.18 GB; 189 without the
 //                                              join: 6.3 TB/s, issue slots 43 %);
 //   one of 131072, 4 heads:                     40 us, 3.3 TB/s (134 MB).

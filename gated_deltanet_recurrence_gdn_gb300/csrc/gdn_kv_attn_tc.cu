@@ -33,7 +33,7 @@
 // let products and softmax overlap: with whole tiles 10 % more).  Drafts of 5
 // tokens in a window of 4096, 16 sequences: 34 us, in 20 rows of the 256: a tile takes
 // 3000 to 3500 cycles there too, bound by the chain from scores to probabilities to
-// the next scores.  In 8 bits the same chunks take 373 us (1.17 PFLOP/s), 345
+// the next scores.  In 8 bits the same chunks take 380 us (1.15 PFLOP/s); 345
 // of which are left if nothing is converted or stored.
 #include "gdn_kv_attn.cuh"
 
@@ -226,7 +226,7 @@ __device__ __forceinline__ uint4 load_line(const uint8_t *p) {
 // In 8 bits a warp's 32 tokens, two blocks of 16: a token's row is as long as a line, so its D / 16
 // pieces of 16 numbers are loaded by as many lanes, each piece right behind the conversion of the
 // one that had its registers, and NaN is looked for only where some row's view ends.  The chunks
-// below take 373 us and 32 rows of 64 ragged sequences 522; a token a thread, loaded behind its
+// below took 373 us then and 32 rows of 64 ragged sequences 522; a token a thread, loaded behind its
 // conversion with NaN looked for in every tile, as in 4 bits, took 422 and 592.
 template <int D>
 struct Token<Fmt8, D> {
